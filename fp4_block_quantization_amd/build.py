@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfos.so")
 
 SOURCES = ["amax.hip", "quantize.hip", "dequantize.hip", "qlinear.hip", "mxfp4.hip", "selftest.hip",
-           "api.cpp"]
+           "wlinear.hip", "kvcache.hip", "paged_decode.hip", "api.cpp", "api_serving.cpp"]
 # measured HBM ceilings for the benchmark (include/fos_ceiling.h), a library of its own
 CEILING_SOURCES = ["ceiling.hip"]
 CEILING_LIB = os.path.join(PKG, "libfos_ceiling.so")

@@ -11,6 +11,7 @@ device tensors; ``quantize`` / ``dequantize`` / ``qlinear_fwd`` allocate the out
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple, Union
@@ -26,6 +27,7 @@ FOS_ROUND_RNE, FOS_ROUND_STOCHASTIC, FOS_ROUND_STOCHASTIC_FULL = 0, 1, 2
 FOS_BLOCK_1D, FOS_BLOCK_2D = 0, 1
 FOS_OUT_ROWWISE, FOS_OUT_COLWISE = 1, 2
 FOS_OUT_F32, FOS_OUT_BF16 = 0, 1
+FOS_KV_BF16, FOS_KV_NVFP4 = 0, 1
 
 
 class FosError(RuntimeError):
@@ -41,12 +43,23 @@ class FosQuantConfig(ctypes.Structure):
                 ("hadamard_seed", ctypes.c_uint64), ("sr_seed", ctypes.c_uint64)]
 
 
+class FosKVCache(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("format", ctypes.c_uint32),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("k_data", ctypes.c_void_p),
+                ("v_data", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_tensor_scale", ctypes.c_void_p),
+                ("v_tensor_scale", ctypes.c_void_p)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m fp4_block_quantization_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
     cfgp = ctypes.POINTER(FosQuantConfig)
+    cachep = ctypes.POINTER(FosKVCache)
     sigs = {
         "fos_abi_version": ([], ctypes.c_int),
         "fos_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -71,6 +84,13 @@ def _load() -> ctypes.CDLL:
         "fos_mx_quantize": ([P, I64, I64, P, P, P], ctypes.c_int),
         "fos_mx_dequantize": ([P, P, I64, I64, ctypes.c_int, P, P], ctypes.c_int),
         "fos_mx_qlinear_fwd": ([P, P, P, P, I64, I64, I64, P, P], ctypes.c_int),
+        "fos_wlinear_fwd": ([P, I64, P, P, P, P, I64, I64, I64, ctypes.c_int, P, P], ctypes.c_int),
+        "fos_mx_wlinear_fwd": ([P, I64, P, P, P, I64, I64, I64, ctypes.c_int, P, P], ctypes.c_int),
+        "fos_kv_append": ([cachep, ctypes.c_int, P, I64, P, I64, P, I64, P], ctypes.c_int),
+        "fos_kv_gather": ([cachep, P, I64, P, I64, P, I64, P], ctypes.c_int),
+        "fos_paged_decode_workspace_bytes": ([I64, I64, I64, I64], SZ),
+        "fos_paged_decode": ([cachep, P, I64, I64, I64, P, I64, I64, P, ctypes.c_float, I64, P, P,
+                              P, SZ, P], ctypes.c_int),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -510,3 +530,243 @@ def mx_qlinear_fwd(aq: MXFP4Tensor, bq: MXFP4Tensor, out: Optional[torch.Tensor]
                                    M, N, K, _ptr(y), _stream(y.device)), "fos_mx_qlinear_fwd")
     return y
 
+
+# ---------------------------------------------------------------- serving one token at a time
+# These calls run once per layer and token, so their wrappers marshal raw addresses and
+# check no more than the library needs to stay inside its tensors.
+
+def _raw_stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_OUT_CODE = {torch.float32: FOS_OUT_F32, torch.bfloat16: FOS_OUT_BF16}
+
+
+def _wlinear_args(x, wq, bias, out_dtype, out, block):
+    """Checked (M, N, K, row stride, y) of a weight-only product."""
+    data, scales = wq.data, wq.scales
+    dev = data.device
+    if x.dim() != 2 or x.dtype != torch.bfloat16 or not x.is_cuda or x.stride(1) != 1:
+        raise ValueError("x must be a 2-D bfloat16 CUDA tensor with contiguous rows")
+    M, K = x.shape
+    N, K2 = data.shape[0], 2 * data.shape[1]
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    if (data.dtype != torch.uint8 or scales.dtype != torch.uint8 or not data.is_contiguous()
+            or not scales.is_contiguous() or tuple(scales.shape) != (N, K // block)):
+        raise ValueError(f"the record must be contiguous uint8 data [N, K/2] and scales [N, K/{block}]")
+    if x.device != dev or scales.device != dev:
+        raise ValueError("x and the weight record are on different devices")
+    if bias is not None and (bias.shape != (N,) or bias.dtype != torch.bfloat16
+                             or bias.device != dev or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous bf16 [N] tensor on x's device")
+    if out is None:
+        if out_dtype not in _OUT_CODE:
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    elif (out.shape != (M, N) or out.dtype != out_dtype or out_dtype not in _OUT_CODE
+          or out.device != dev or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous [M, N] tensor of out_dtype on x's device")
+    return M, N, K, (x.stride(0) if M > 1 else K), out
+
+
+def wlinear_fwd(x: torch.Tensor, wq: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
+                out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None
+                ) -> torch.Tensor:
+    """Y = X deq(W)^T (+ bias) for a bf16 activation X [M, K], which is not quantized, and
+    a weight record W [N, K]: the layer of a decode step (M = the sequences of the
+    batch; made for up to 64).  X's rows may be strided.  ``bias``: bf16 [N];
+    ``out``: optional [M, N] destination of ``out_dtype`` (bf16 or fp32)."""
+    if wq.hadamard_seed is not None:
+        raise ValueError("the weight record carries a Hadamard transform that x does not")
+    t = wq.tensor_scale
+    if t.dtype != torch.float32 or t.numel() != 1 or t.device != x.device:
+        raise ValueError("tensor_scale must be a one-element fp32 tensor on x's device")
+    M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 16)
+    _check(_lib.fos_wlinear_fwd(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
+                                t.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K,
+                                _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(x.device)),
+           "fos_wlinear_fwd")
+    return y
+
+
+def mx_wlinear_fwd(x: torch.Tensor, wq: MXFP4Tensor, bias: Optional[torch.Tensor] = None,
+                   out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None
+                   ) -> torch.Tensor:
+    """wlinear_fwd for an MXFP4 weight record."""
+    M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 32)
+    _check(_lib.fos_mx_wlinear_fwd(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
+                                   None if bias is None else bias.data_ptr(), M, N, K,
+                                   _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(x.device)),
+           "fos_mx_wlinear_fwd")
+    return y
+
+
+class PagedKVCache:
+    """A paged key-value cache over caller-owned CUDA tensors (not copied; they must not
+    be replaced afterwards): k, v [pages, kv heads, page size, head dim] bf16, or, for
+    an NVFP4 cache, uint8 nibbles [.., head dim / 2] with k_scales, v_scales uint8
+    [.., head dim / 16] and the static tensor scales k_tensor_scale, v_tensor_scale
+    (fp32 [1]).  ``kv_cache`` allocates one."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "k_tensor_scale", "v_tensor_scale",
+                 "num_pages", "num_kv_heads", "page_size", "head_dim", "format", "device", "_c",
+                 "_ref")
+
+    def __init__(self, k, v, k_scales=None, v_scales=None, k_tensor_scale=None,
+                 v_tensor_scale=None):
+        nvfp4 = k.dtype == torch.uint8
+        if not nvfp4 and k.dtype != torch.bfloat16:
+            raise ValueError("k and v must be bf16, or uint8 nibbles")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [pages, kv heads, page size, ..] of one shape and type")
+        P, H, S, D = k.shape
+        D = 2 * D if nvfp4 else D
+        tensors = [k, v]
+        if nvfp4:
+            if None in (k_scales, v_scales, k_tensor_scale, v_tensor_scale):
+                raise ValueError("an NVFP4 cache needs block scales and tensor scales of K and V")
+            for s in (k_scales, v_scales):
+                if s.dtype != torch.uint8 or tuple(s.shape) != (P, H, S, D // 16):
+                    raise ValueError("block scales must be uint8 [pages, kv heads, page size, head dim / 16]")
+            for t in (k_tensor_scale, v_tensor_scale):
+                if t.dtype != torch.float32 or t.numel() != 1:
+                    raise ValueError("tensor scales must be one-element fp32 tensors")
+            tensors += [k_scales, v_scales, k_tensor_scale, v_tensor_scale]
+        for t in tensors:
+            if not t.is_cuda or t.device != k.device or not t.is_contiguous():
+                raise ValueError("cache tensors must be contiguous CUDA tensors on one device")
+        if not (16 <= S <= 4096 and S % 16 == 0 and 32 <= D <= 256 and D % 32 == 0 and H >= 1):
+            raise ValueError("page size must be a multiple of 16 from 16 to 4096, head dim a "
+                             "multiple of 32 from 32 to 256")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.k_tensor_scale, self.v_tensor_scale = k_tensor_scale, v_tensor_scale
+        self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = P, H, S, D
+        self.format, self.device = ("nvfp4" if nvfp4 else "bf16"), k.device
+        ptr = lambda t: t.data_ptr() if nvfp4 else None
+        self._c = FosKVCache(ctypes.sizeof(FosKVCache), FOS_KV_NVFP4 if nvfp4 else FOS_KV_BF16, P,
+                             S, H, D, 0, k.data_ptr(), v.data_ptr(), ptr(k_scales), ptr(v_scales),
+                             ptr(k_tensor_scale), ptr(v_tensor_scale))
+        self._ref = ctypes.byref(self._c)
+
+
+def kv_cache(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+             format: str = "nvfp4", k_tensor_scale: Optional[torch.Tensor] = None,
+             v_tensor_scale: Optional[torch.Tensor] = None, device="cuda") -> PagedKVCache:
+    """An empty (zeroed) cache.  An NVFP4 cache needs the static tensor scales of K and V:
+    fp32 [1] device tensors, e.g. ``tensor_scale`` of keys and values seen beforehand."""
+    shape = (num_pages, num_kv_heads, page_size)
+    if format == "bf16":
+        return PagedKVCache(*(torch.zeros(*shape, head_dim, dtype=torch.bfloat16, device=device)
+                              for _ in range(2)))
+    if format != "nvfp4":
+        raise ValueError("format must be 'nvfp4' or 'bf16'")
+    u8 = dict(dtype=torch.uint8, device=device)
+    k, v = (torch.zeros(*shape, head_dim // 2, **u8) for _ in range(2))
+    ks, vs = (torch.zeros(*shape, head_dim // 16, **u8) for _ in range(2))
+    return PagedKVCache(k, v, ks, vs, k_tensor_scale, v_tensor_scale)
+
+
+def _check_rows(cache: PagedKVCache, x: torch.Tensor, what: str):
+    s = x.stride()
+    if (x.dim() != 3 or x.shape[1] != cache.num_kv_heads or x.shape[2] != cache.head_dim
+            or x.dtype != torch.bfloat16 or x.device != cache.device or s[2] != 1
+            or (x.shape[1] > 1 and s[1] != cache.head_dim)):
+        raise ValueError(f"{what} must be bf16 [tokens, kv heads, head dim] on the cache's device, "
+                         "each token's heads in one run")
+
+
+def _check_slots(cache: PagedKVCache, slots: torch.Tensor):
+    if (slots.dim() != 1 or slots.dtype != torch.int64 or slots.device != cache.device
+            or not slots.is_contiguous()):
+        raise ValueError("slots must be a contiguous 1-D int64 tensor on the cache's device")
+
+
+def kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+              rule: str = "4/6") -> None:
+    """Write the keys and values of new tokens (bf16 [T, kv heads, head dim]; the token
+    stride is free, so columns of a fused projection need no copy) to ``slots`` (int64
+    [T], page * page_size + token of the page; negative or past the cache: skipped).
+    An NVFP4 cache quantizes each 16 values with ``rule`` ("4/6" or "6") under the
+    cache's tensor scales.  Slots of one call must be distinct."""
+    _check_rows(cache, k, "k")
+    _check_rows(cache, v, "v")
+    _check_slots(cache, slots)
+    T = slots.shape[0]
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("k, v and slots disagree on the number of tokens")
+    rules = {"4/6": FOS_RULE_4OVER6, "6": FOS_RULE_6ONLY}
+    _check(_lib.fos_kv_append(cache._ref, rules[rule], k.data_ptr(), k.stride(0), v.data_ptr(),
+                              v.stride(0), slots.data_ptr(), T, _raw_stream(cache.device)),
+           "fos_kv_append")
+
+
+def kv_gather(cache: PagedKVCache, slots: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Keys and values of ``slots`` (int64 [T]) as bf16 [T, kv heads, head dim]; zeros for
+    slots outside the cache."""
+    _check_slots(cache, slots)
+    T, H, D = slots.shape[0], cache.num_kv_heads, cache.head_dim
+    k = torch.empty(T, H, D, dtype=torch.bfloat16, device=cache.device)
+    v = torch.empty(T, H, D, dtype=torch.bfloat16, device=cache.device)
+    _check(_lib.fos_kv_gather(cache._ref, slots.data_ptr(), T, k.data_ptr(), H * D, v.data_ptr(),
+                              H * D, _raw_stream(cache.device)), "fos_kv_gather")
+    return k, v
+
+
+_decode_workspaces = {}
+
+
+def _decode_workspace(device: torch.device, stream: int, need: int) -> torch.Tensor:
+    """Scratch of paged_decode for one stream.  It grows by powers of two, and an outgrown
+    one is kept: a captured graph may hold its address."""
+    key = (device.index, stream)
+    held = _decode_workspaces.setdefault(key, [])
+    if not held or held[-1].numel() < need:
+        held.append(torch.empty(1 << max(need - 1, 4095).bit_length(), dtype=torch.uint8,
+                                device=device))
+    return held[-1]
+
+
+def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, scale: Optional[float] = None, window: int = 0,
+                 return_lse: bool = False, out: Optional[torch.Tensor] = None):
+    """Attention of one new token per sequence over the paged cache.
+
+    q: bf16 [B, query heads, head dim] (the sequence stride is free; query heads a
+    multiple of the cache's kv heads).  block_table: int32 [B, pages], rows may be
+    strided; an id outside the cache is a page no longer held, whose tokens are not
+    visible.  seq_lens: int32 [B], the new token included.  scale: default
+    1/sqrt(head dim).  window > 0: only the last ``window`` tokens are visible.
+    Returns bf16 [B, query heads, head dim] (``out`` if given), and with
+    ``return_lse`` also the fp32 [B, query heads] log-sum-exp of the scaled scores.
+    Where nothing is visible the output is 0 and its lse -inf."""
+    dev, D = cache.device, cache.head_dim
+    s = q.stride()
+    if (q.dim() != 3 or q.dtype != torch.bfloat16 or q.device != dev or q.shape[2] != D
+            or s[2] != 1 or (q.shape[1] > 1 and s[1] != D)):
+        raise ValueError("q must be bf16 [sequences, query heads, head dim] on the cache's device, "
+                         "each sequence's heads in one run")
+    B, Hq, _ = q.shape
+    if Hq < 1 or Hq % cache.num_kv_heads:
+        raise ValueError("query heads must be a multiple of the cache's kv heads")
+    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev
+            or block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be int32 [sequences, pages] on the cache's device")
+    if (seq_lens.shape != (B,) or seq_lens.dtype != torch.int32 or seq_lens.device != dev
+            or not seq_lens.is_contiguous()):
+        raise ValueError("seq_lens must be a contiguous int32 [sequences] tensor on the cache's device")
+    if out is None:
+        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev)
+    elif (out.shape != (B, Hq, D) or out.dtype != torch.bfloat16 or out.device != dev
+          or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape on the cache's device")
+    lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
+    stream = _raw_stream(dev)
+    need = _lib.fos_paged_decode_workspace_bytes(B, Hq, cache.num_kv_heads, D)
+    ws = _decode_workspace(dev, stream, need)
+    _check(_lib.fos_paged_decode(cache._ref, q.data_ptr(), s[0], B, Hq, block_table.data_ptr(),
+                                 block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
+                                 1.0 / math.sqrt(D) if scale is None else scale, int(window),
+                                 out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), stream), "fos_paged_decode")
+    return (out, lse) if return_lse else out

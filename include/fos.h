@@ -60,7 +60,9 @@ typedef enum {
   FOS_E_WORKSPACE = 5, /* workspace NULL, not 16-byte aligned, or smaller than
                           fos_workspace_bytes() (fos_qlinear_fwd_act: not 256-byte
                           aligned, or smaller than
-                          fos_qlinear_act_workspace_bytes(M, K))                   */
+                          fos_qlinear_act_workspace_bytes(M, K); fos_paged_decode:
+                          not 256-byte aligned, or smaller than
+                          fos_paged_decode_workspace_bytes(...))                    */
   FOS_E_HIP = 6        /* a HIP launch failed                                        */
 } fos_status;
 
@@ -385,6 +387,127 @@ fos_status fos_mx_dequantize(const uint8_t* data, const uint8_t* scales, int64_t
 fos_status fos_mx_qlinear_fwd(const uint8_t* a_data, const uint8_t* a_scales,
                               const uint8_t* b_data, const uint8_t* b_scales, int64_t M,
                               int64_t N, int64_t K, void* y_bf16, void* stream);
+
+/* ---- Serving one token at a time ------------------------------------------------
+ * A decode step of a layer whose weights are 4-bit records: products of a few bf16
+ * activation rows with a record (the activation is not quantized), a paged key-value
+ * cache that holds bf16 rows or NVFP4 records, and the attention of each sequence's
+ * new token over that cache.  (The Four Over Six documentation page simulates the
+ * quantized layer "with a higher-precision matrix multiplication", section "Four Over
+ * Six"; the Ultralytics glossary "FP4", "FP4 for inference and training", names
+ * 4-bit inference as the format's use.  Neither fixes these operators; the formulas
+ * below do.) */
+
+/* Weight-only linear layer: bf16 activations times an NVFP4 weight record,
+ *   Y[m][n] = RN( t_w * sum_k X[m][k] * (E*D)_w[n][k] + bias[n] )
+ * with exact products, fp32 sums (in an unspecified order that is the same for every
+ * call of the same shape), and one rounding to the output type.  Made for few rows
+ * (M = 1 is a token of one sequence; up to 64 rows share one pass over the weight);
+ * any M is accepted.  2D records work (they carry one scale per 16 values too); a
+ * record made with the Hadamard transform needs an activation that carries the same
+ * transform.
+ *   X: bf16, row m at x_bf16 + m * x_stride elements, 16-byte aligned, x_stride >= K
+ *   and a multiple of 8 (both for M > 1).  w_data [N][K/2] 16-byte aligned, w_scales
+ *   [N][K/16] 4-byte aligned.  bias_bf16 [N] or NULL.  y [M][N] of out_dtype
+ *   (FOS_OUT_F32: 4-byte aligned, FOS_OUT_BF16: 2-byte).
+ *   M >= 0 (0: nothing is launched), N >= 1, K >= 16 and K % 16 == 0.
+ * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_HIP. */
+fos_status fos_wlinear_fwd(const void* x_bf16, int64_t x_stride, const uint8_t* w_data,
+                           const uint8_t* w_scales, const float* w_tensor_scale,
+                           const void* bias_bf16, int64_t M, int64_t N, int64_t K, int out_dtype,
+                           void* y, void* stream);
+
+/* The same with an MXFP4 weight record (w_scales [N][K/32] E8M0 bytes, no tensor
+ * scale): Y[m][n] = RN( sum_k X[m][k] * deq(W)[n][k] + bias[n] ); K % 32 == 0. */
+fos_status fos_mx_wlinear_fwd(const void* x_bf16, int64_t x_stride, const uint8_t* w_data,
+                              const uint8_t* w_scales, const void* bias_bf16, int64_t M,
+                              int64_t N, int64_t K, int out_dtype, void* y, void* stream);
+
+/* Element format of a paged key-value cache. */
+enum { FOS_KV_BF16 = 0, FOS_KV_NVFP4 = 1 };
+
+/* A paged key-value cache in caller-owned device memory.  K and V are stored as
+ *   [num_pages][num_kv_heads][page_size][head_dim]
+ * so that a page holds each head's tokens in one run.  FOS_KV_BF16: k_data and v_data
+ * hold bf16 values, the scale pointers are ignored.  FOS_KV_NVFP4: k_data and v_data
+ * hold nibbles ([..][head_dim/2]), k_scales and v_scales E4M3 block scales
+ * ([..][head_dim/16]): the page of a head is an NVFP4 record [page_size][head_dim],
+ * and the whole cache one of num_pages*num_kv_heads*page_size rows.  The tensor
+ * scales are static (one device fp32 for K, one for V, fixed before the first append):
+ * rows appended at different times share them.
+ *   page_size: 16 to 4096, a multiple of 16; head_dim: 32 to 256, a multiple of 32;
+ *   num_kv_heads >= 1; num_pages >= 0; fewer than 2^40 values in each of K and V.
+ *   Data and scales 16-byte aligned, tensor scales 4-byte. */
+typedef struct {
+  uint32_t struct_size;       /* must equal sizeof(fos_kv_cache)                      */
+  uint32_t format;            /* FOS_KV_*                                             */
+  int64_t num_pages;
+  int32_t page_size, num_kv_heads, head_dim;
+  int32_t reserved;           /* 0                                                    */
+  void *k_data, *v_data;
+  uint8_t *k_scales, *v_scales;
+  const float *k_tensor_scale, *v_tensor_scale;
+} fos_kv_cache;               /* host struct, read only during the call               */
+
+/* Write the keys and values of num_tokens new tokens into the cache.  Token i goes to
+ * slot slots[i] = page * page_size + token of the page (device int64); a slot below 0
+ * or past the cache is skipped (padding rows).  Slots of one call must be distinct: of
+ * two rows with one slot, either may remain, also block by block.  An NVFP4 cache
+ * quantizes each row in blocks of 16 consecutive values, exactly as
+ * fos_quantize_scaled with `rule`, nearest-even rounding and the cache's tensor scale
+ * (a block whose maximum is above 2688 times the tensor scale saturates); a bf16
+ * cache copies, and ignores the rule.
+ *   k_bf16, v_bf16: bf16 [num_tokens][num_kv_heads][head_dim], token strides in
+ *   elements (columns of a fused projection's output need no copy), 16-byte aligned,
+ *   strides at least num_kv_heads*head_dim and multiples of 8 (for num_tokens > 1).
+ * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_HIP. */
+fos_status fos_kv_append(const fos_kv_cache* cache, int rule, const void* k_bf16,
+                         int64_t k_stride, const void* v_bf16, int64_t v_stride,
+                         const int64_t* slots, int64_t num_tokens, void* stream);
+
+/* Read slots back as bf16 (the inverse of fos_kv_append; NVFP4 rows are dequantized
+ * as by fos_dequantize with FOS_OUT_BF16): row i of k_bf16 and v_bf16
+ * ([num_tokens][num_kv_heads][head_dim], token strides) is slot slots[i], zeros for a
+ * slot below 0 or past the cache.  Slots may repeat.  Alignment and errors as for
+ * fos_kv_append. */
+fos_status fos_kv_gather(const fos_kv_cache* cache, const int64_t* slots, int64_t num_tokens,
+                         void* k_bf16, int64_t k_stride, void* v_bf16, int64_t v_stride,
+                         void* stream);
+
+/* Bytes of device workspace that fos_paged_decode needs for these sizes (whatever the
+ * lengths); 0 for sizes that it refuses. */
+size_t fos_paged_decode_workspace_bytes(int64_t num_seqs, int64_t num_q_heads,
+                                        int64_t num_kv_heads, int64_t head_dim);
+
+/* Attention of one new token per sequence over its pages of the cache.  Sequence b
+ * holds seq_lens[b] tokens (the new one included, once appended); token j is row
+ * j % page_size of page block_table[b][j / page_size].  Query head h reads kv head
+ * h / (num_q_heads / num_kv_heads).  With the visible tokens
+ *   max(0, seq_lens[b] - window) <= j < seq_lens[b]   (window 0: all below the length)
+ * and the softmax taken over them,
+ *   s_j = softmax_scale * q . k_j,   lse = log sum_j exp(s_j),
+ *   out = RN_bf16( sum_j exp(s_j - lse) v_j ).
+ * A page id below 0 or not below num_pages is a page that the cache no longer holds:
+ * its tokens are not visible.  So are tokens past pages_per_seq pages, and a length
+ * below 1 has none.  Where nothing is visible, out is 0 and lse -infinity.  What the
+ * pages hold in places that are not visible does not matter (NaN included); q and the
+ * visible rows must be finite.  Statistics and sums are fp32; results do not depend
+ * on what else the GPU runs (no atomic sums).
+ *   q_bf16: [num_seqs][num_q_heads][head_dim], sequence stride q_stride elements;
+ *   block_table: int32 [num_seqs][pages_per_seq], row stride table_stride elements;
+ *   out_bf16 [num_seqs][num_q_heads][head_dim] contiguous; lse fp32
+ *   [num_seqs][num_q_heads] or NULL (natural logarithm).
+ *   q_bf16 16-byte aligned with q_stride % 8 == 0 (for num_seqs > 1), out_bf16
+ *   16-byte aligned; fewer than 2^31 tokens per sequence.
+ *   workspace: device scratch, 256-byte aligned, at least
+ *   fos_paged_decode_workspace_bytes(...) bytes; calls that may overlap need their own.
+ * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS (also a negative window or
+ * a softmax_scale that is not finite), FOS_E_WORKSPACE, FOS_E_HIP. */
+fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64_t q_stride,
+                            int64_t num_seqs, int64_t num_q_heads, const int32_t* block_table,
+                            int64_t table_stride, int64_t pages_per_seq, const int32_t* seq_lens,
+                            float softmax_scale, int64_t window, void* out_bf16, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
