@@ -15,6 +15,7 @@ constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int kMinPage = 16, kMaxPage = 4096;
 constexpr int kMaxHeadDim = 256;
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;   // of one sequence
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -196,13 +197,15 @@ fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64
   if (num_seqs < 0 || num_q_heads < 1 || num_q_heads % cache->num_kv_heads ||
       num_seqs >= kMaxDim || num_q_heads >= kMaxDim || num_seqs * num_q_heads >= kMaxDim ||
       pages_per_seq < 0 || pages_per_seq >= kMaxDim ||
-      pages_per_seq * cache->page_size >= kMaxDim || q_stride < 0 || table_stride < 0)
+      pages_per_seq * cache->page_size > kMaxTokens || q_stride < 0 || table_stride < 0)
     return FOS_E_SHAPE;
   const int64_t width = num_q_heads * cache->head_dim;
   if (num_seqs > 1 && (q_stride < width || table_stride < pages_per_seq ||
                        q_stride > kMaxElems / num_seqs || table_stride > kMaxElems / num_seqs))
     return FOS_E_SHAPE;
-  if (num_seqs * num_q_heads > fos::kMaxGrid) return FOS_E_SHAPE;
+  if (num_seqs * num_q_heads > fos::kMaxGrid ||
+      fos::decode_items(num_seqs, num_q_heads, cache->num_kv_heads) > fos::kMaxGrid)
+    return FOS_E_SHAPE;
   if (window < 0 || !std::isfinite(softmax_scale)) return FOS_E_FLAGS;
   if (num_seqs == 0) return FOS_OK;
   if (!q_bf16 || !seq_lens || !out_bf16 || (pages_per_seq > 0 && !block_table)) return FOS_E_NULL;

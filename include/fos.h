@@ -498,7 +498,7 @@ size_t fos_paged_decode_workspace_bytes(int64_t num_seqs, int64_t num_q_heads,
  *   out_bf16 [num_seqs][num_q_heads][head_dim] contiguous; lse fp32
  *   [num_seqs][num_q_heads] or NULL (natural logarithm).
  *   q_bf16 16-byte aligned with q_stride % 8 == 0 (for num_seqs > 1), out_bf16
- *   16-byte aligned; fewer than 2^31 tokens per sequence.
+ *   16-byte aligned; pages_per_seq * page_size at most 2^30.
  *   workspace: device scratch, 256-byte aligned, at least
  *   fos_paged_decode_workspace_bytes(...) bytes; calls that may overlap need their own.
  * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS (also a negative window or
