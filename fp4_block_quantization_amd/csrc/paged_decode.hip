@@ -35,6 +35,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kHeads = 16;            // query heads per workgroup: columns of the products
 constexpr int kTargetItems = 1024;    // chunks wanted over the whole batch
 constexpr int kMinChunk = 512;        // tokens of a chunk, at least
+constexpr int kChunkStep = 64 * kWaves;   // a step of every wave
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -79,8 +80,8 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
   return v;
 }
 
-// Tokens per chunk, a multiple of `step`: enough that the batch gives about kTargetItems.
-__device__ __forceinline__ int chunk_tokens(const Plan& p, int lane, int step) {
+// Tokens per chunk, a multiple of kChunkStep: enough that the batch gives about kTargetItems.
+__device__ __forceinline__ int chunk_tokens(const Plan& p, int lane) {
   int64_t total = 0;
   for (int b = lane; b < p.a.B; b += 64) {
     const Range r = range_of(p, p.a.lens[b]);
@@ -89,7 +90,7 @@ __device__ __forceinline__ int chunk_tokens(const Plan& p, int lane, int step) {
   total = wave_sum(total) * (p.a.c.heads * p.groups);
   int64_t c = (total + kTargetItems - 1) / kTargetItems;
   c = max(c, (int64_t)kMinChunk);
-  c = (c + step - 1) / step * step;
+  c = (c + kChunkStep - 1) / kChunkStep * kChunkStep;
   return (int)min(c, (int64_t)1 << 30);
 }
 
@@ -150,12 +151,9 @@ __device__ __forceinline__ float sum_over_groups(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// Eight nibbles times one block scale as eight halves: E2M1 x E4M3 has at most 6
-// significant bits between 2^-10 and 2688, so it is exact in half precision.
-__device__ __forceinline__ f16x2 e4m3_pair(uint32_t byte) {
-  const f16x2 s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(byte, 1.0f, false);
-  return f16x2{s.x, s.x};
-}
+// E2M1 x E4M3 has at most 6 significant bits between 2^-10 and 2688: exact in half
+// precision.
+// Eight nibbles times the block scale in both halves of s.
 __device__ __forceinline__ u32x4 dequant8(uint32_t w, f16x2 s) {
   const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s;
   const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s;
@@ -163,6 +161,15 @@ __device__ __forceinline__ u32x4 dequant8(uint32_t w, f16x2 s) {
   const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s;
   return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
                __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)};
+}
+// Byte kSel of w (two nibbles) times the two scales of s.
+template <int kSel>
+__device__ __forceinline__ uint32_t dequant2(uint32_t w, f16x2 s) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, kSel) * s);
+}
+// The nibbles selected by 0x0f0f0f0f from x, the others from y.
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t x, uint32_t y) {
+  return (x & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
 }
 
 template <bool kNVFP4>
@@ -179,28 +186,187 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
 }
 
-// Cache row of the first token of a group of 8 (a group never crosses a page), or -1.
-__device__ __forceinline__ int64_t group_row(const Plan& p, const int32_t* table, int head, int tok) {
+// Page id of the group of 8 tokens that starts at `tok` (a group never crosses a page)
+// and the group's first row in the page; id -1 past `end`.
+struct Group {
+  int id, off;
+};
+__device__ __forceinline__ Group find_group(const Plan& p, const int32_t* table, int tok, int end) {
   const uint32_t g = (uint32_t)tok >> 3;
   const int page = (int)((g * p.page_magic) >> 36);
-  if (page >= p.a.pages_per_seq) return -1;
-  const int id = table[page];
-  if (id < 0 || id >= p.a.c.num_pages) return -1;
-  return ((int64_t)id * p.a.c.heads + head) * p.a.c.page_size + (tok - page * p.a.c.page_size);
+  Group x;
+  x.id = tok < end ? table[page] : -1;
+  x.off = tok - page * p.a.c.page_size;
+  return x;
+}
+__device__ __forceinline__ bool held(const Plan& p, const Group& x) {
+  return (uint32_t)x.id < (uint32_t)p.a.c.num_pages;   // num_pages < 2^31
+}
+// The group's first row in the cache; row 0 for a page that is not held (what is read
+// there is masked).
+__device__ __forceinline__ int64_t row_of(const Plan& p, const Group& x, int head) {
+  return held(p, x) ? ((int64_t)x.id * p.a.c.heads + head) * p.a.c.page_size + x.off : 0;
 }
 
+// K and V of 32 tokens as one lane loads them: K rows as A operand rows, V rows of the
+// lane's 8 tokens.
 template <bool kNVFP4, int D>
-__global__ __launch_bounds__(kThreads) void paged_decode_kernel(Plan p) {
+struct Raw;
+template <int D>
+struct Raw<false, D> {
+  using P = Pieces<D>;
+  u32x4 k[2][D / 32];
+  uint32_t v[8][D / 32];
+  __device__ __forceinline__ void load_k(const KVCacheArgs& c, int64_t row, int q) {
+    const uint16_t* base = reinterpret_cast<const uint16_t*>(c.k) + row * D + 8 * q;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+        k[u][j] = *reinterpret_cast<const u32x4*>(base + 4 * u * D + 32 * j);
+  }
+  __device__ __forceinline__ void load_v(const KVCacheArgs& c, int64_t row, int r) {
+    const uint16_t* base = reinterpret_cast<const uint16_t*>(c.v) + row * D;
+#pragma unroll
+    for (int i = 0; i < P::count; ++i) {
+      const int n = P::size(i) / 16, at = P::at(i) / 32;   // values of the lane; its dwords
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t* w = base + P::at(i) + n * r + e * D;
+        if (n == 8) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(w);
+          v[e][at] = x.x; v[e][at + 1] = x.y; v[e][at + 2] = x.z; v[e][at + 3] = x.w;
+        } else if (n == 4) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(w);
+          v[e][at] = x.x; v[e][at + 1] = x.y;
+        } else {
+          v[e][at] = *reinterpret_cast<const uint32_t*>(w);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ u32x4 k_step(int u, int j) const { return k[u][j]; }
+  __device__ __forceinline__ void mask_v(uint32_t seen) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) v[e][i] = (seen >> e) & 1 ? v[e][i] : 0u;
+  }
+  // Tiles 2 i and 2 i + 1 of V^T: two values of each of the 8 tokens.
+  __device__ __forceinline__ void v_tiles(int i, u32x4& even, u32x4& odd) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      even[e] = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x05040100u);
+      odd[e] = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x07060302u);
+    }
+  }
+};
+template <int D>
+struct Raw<true, D> {
+  using P = Pieces<D>;
+  uint32_t k[2][D / 32];           // 8 nibbles of each step
+  uint32_t ks[2][P::count];        // one or two block scales of each piece
+  uint32_t v[8][P::count];         // 8, 4 or 2 nibbles
+  uint32_t vs[8][P::count];        // their block scale
+  __device__ __forceinline__ void load_k(const KVCacheArgs& c, int64_t row, int q) {
+    const uint8_t* base = c.k + row * (D / 2);
+    const uint8_t* sbase = c.ks + row * (D / 16);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < P::count; ++i) {
+        const int n = P::size(i) / 32, at = P::at(i) / 32;
+        const uint8_t* w = base + 4 * u * (D / 2) + P::at(i) / 2 + 4 * n * q;
+        const uint8_t* sp = sbase + 4 * u * (D / 16) + P::at(i) / 16;
+        if (n == 4) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(w);
+          k[u][at] = x.x; k[u][at + 1] = x.y; k[u][at + 2] = x.z; k[u][at + 3] = x.w;
+          ks[u][i] = *reinterpret_cast<const uint16_t*>(sp + 2 * q);
+        } else if (n == 2) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(w);
+          k[u][at] = x.x; k[u][at + 1] = x.y;
+          ks[u][i] = sp[q];
+        } else {
+          k[u][at] = *reinterpret_cast<const uint32_t*>(w);
+          ks[u][i] = sp[q / 2];
+        }
+      }
+  }
+  __device__ __forceinline__ void load_v(const KVCacheArgs& c, int64_t row, int r) {
+    const uint8_t* base = c.v + row * (D / 2);
+    const uint8_t* sbase = c.vs + row * (D / 16);
+#pragma unroll
+    for (int i = 0; i < P::count; ++i) {
+      const int n = P::size(i) / 16;
+      const uint8_t* w = base + P::at(i) / 2 + n * r / 2;
+      const uint8_t* sp = sbase + (P::at(i) + n * r) / 16;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t* we = w + e * (D / 2);
+        v[e][i] = n == 8 ? *reinterpret_cast<const uint32_t*>(we)
+                  : n == 4 ? *reinterpret_cast<const uint16_t*>(we) : *we;
+        vs[e][i] = sp[e * (D / 16)];
+      }
+    }
+  }
+  __device__ __forceinline__ u32x4 k_step(int u, int j) const {
+    int i = 0;
+#pragma unroll
+    for (int x = 1; x < P::count; ++x) i = 32 * j >= P::at(x) ? x : i;
+    const int in = j - P::at(i) / 32;          // step of the piece
+    const f16x2 s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(ks[u][i], 1.0f, false);
+    const _Float16 x = in >= 2 ? s.y : s.x;
+    return dequant8(k[u][j], f16x2{x, x});
+  }
+  __device__ __forceinline__ void mask_v(uint32_t seen) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int i = 0; i < P::count; ++i) vs[e][i] = (seen >> e) & 1 ? vs[e][i] : 0u;
+  }
+  // The nibbles of two tokens are brought together (four tokens' worth of bit selects for
+  // eight conversions), so that one conversion gives two tokens of one d.
+  __device__ __forceinline__ void v_tiles(int t, u32x4& even, u32x4& odd) const {
+    int i = 0;
+#pragma unroll
+    for (int x = 1; x < P::count; ++x) i = 32 * t >= P::at(x) ? x : i;
+    const int sel = t - P::at(i) / 32;         // byte of the word
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f16x2 s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(vs[2 * e][i] | vs[2 * e + 1][i] << 8,
+                                                               1.0f, false);
+      const uint32_t a = low_nibbles(v[2 * e][i], v[2 * e + 1][i] << 4);
+      const uint32_t b = low_nibbles(v[2 * e][i] >> 4, v[2 * e + 1][i]);
+      even[e] = sel == 0 ? dequant2<0>(a, s) : sel == 1 ? dequant2<1>(a, s)
+                : sel == 2 ? dequant2<2>(a, s) : dequant2<3>(a, s);
+      odd[e] = sel == 0 ? dequant2<0>(b, s) : sel == 1 ? dequant2<1>(b, s)
+               : sel == 2 ? dequant2<2>(b, s) : dequant2<3>(b, s);
+    }
+  }
+};
+
+// Tokens of one step of a wave: 64 of an NVFP4 cache of up to 128 values, else 32 (the
+// K and V of a step are held in registers).
+template <bool kNVFP4, int D>
+constexpr int kSub = kNVFP4 && D <= 128 ? 2 : 1;
+// Waves per SIMD that the registers are shared out for.
+template <bool kNVFP4, int D>
+constexpr int kMinWaves = !kNVFP4 && D > 160 ? 1 : 2;
+constexpr float kSlack = 8.0f;    // see the rescaling below
+
+template <bool kNVFP4, int D>
+__global__ __launch_bounds__(kThreads, (kMinWaves<kNVFP4, D>)) void paged_decode_kernel(Plan p) {
   constexpr int kSteps = D / 32;               // 32-value steps of the first product
   constexpr int kTiles = D / 16;               // 16-row tiles of the second
   constexpr int kPad = D + 4;
+  constexpr int N = kSub<kNVFP4, D>;
   using P = Pieces<D>;
   __shared__ __attribute__((aligned(16))) float so[kWaves][kHeads][kPad];
   __shared__ float sm[kWaves][kHeads], sl[kWaves][kHeads];
   const DecodeArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
-  const int chunk = chunk_tokens(p, lane, 32 * kWaves);
+  const int chunk = chunk_tokens(p, lane);
   const Item it = find_item(p, lane, chunk, blockIdx.x);
   if (it.b < 0) return;
   const int per = a.c.heads * p.groups;
@@ -249,117 +415,89 @@ __global__ __launch_bounds__(kThreads) void paged_decode_kernel(Plan p) {
   for (int i = 0; i < kTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
   float m = -INFINITY, l = 0.0f;
 
-  for (int t0 = begin + 32 * wave; t0 < end; t0 += 32 * kWaves) {
-    // rows of this lane's K tokens and V tokens; lanes of an absent page read row 0 (of a
-    // cache with at least one page) and are masked
-    const int gk = t0 + 8 * (r >> 2), gv = t0 + 8 * q;
-    const int64_t rk = gk < end ? group_row(p, table, head, gk) : -1;
-    const int64_t rv = gv < end ? group_row(p, table, head, gv) : -1;
-    const int64_t krow = rk < 0 ? 0 : rk + (r & 3), vrow = max(rv, (int64_t)0);
-    f32x4 s[2];
-    u32x4 vt[kTiles];                          // V^T: tile i, tokens 8 q .. 8 q + 7
-    uint32_t seen = 0;                         // bit e: token gv + e is visible
+  // Pipeline of a wave's steps: page ids two steps ahead, K one step ahead from the end of
+  // the first product, V from the end of the second.
+  constexpr int kStride = 32 * N * kWaves;
+  Raw<kNVFP4, D> raw[N];
+  Group gk[N], gv[N];
+  bool v_held[N];
+  auto find = [&](int t) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) seen |= (uint32_t)(rv >= 0 && gv + e >= rg.first && gv + e < end) << e;
-    const bool all = __all(seen == 0xffu);
-    if constexpr (kNVFP4) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint8_t* kp = a.c.k + (krow + 4 * u) * (D / 2);
-        const uint8_t* sp = a.c.ks + (krow + 4 * u) * (D / 16);
-        s[u] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < P::count; ++i) {
-          constexpr int kN[3] = {4, 2, 1};
-          const int n = P::size(i) == 128 ? kN[0] : P::size(i) == 64 ? kN[1] : kN[2];
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(kp + P::at(i) / 2 + P::size(i) / 8 * q);
-#pragma unroll
-          for (int j = 0; j < n; ++j) {
-            const int d = P::at(i) + P::size(i) / 4 * q + 8 * j;
-            s[u] = mfma<true>(dequant8(w[j], e4m3_pair(sp[d / 16])), qf[P::at(i) / 32 + j], s[u]);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < P::count; ++i) {
-        const int per16 = P::size(i) / 16;     // values of a lane and row: 8, 4 or 2
-        uint32_t h[8][4];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t row = vrow + e;
-          const int d = P::at(i) + per16 * r;
-          const uint8_t* w = a.c.v + row * (D / 2) + d / 2;
-          uint32_t sb = a.c.vs[row * (D / 16) + d / 16];
-          if (!all && !((seen >> e) & 1)) sb = 0;
-          const f16x2 sc = e4m3_pair(sb);
-          const uint32_t word = per16 == 8 ? *reinterpret_cast<const uint32_t*>(w)
-                                : per16 == 4 ? *reinterpret_cast<const uint16_t*>(w) : *w;
-          const u32x4 x = dequant8(word, sc);
-          h[e][0] = x.x; h[e][1] = x.y; h[e][2] = x.z; h[e][3] = x.w;
-        }
-#pragma unroll
-        for (int c = 0; c < per16 / 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            vt[P::at(i) / 16 + 2 * c][e] = __builtin_amdgcn_perm(h[2 * e + 1][c], h[2 * e][c], 0x05040100u);
-            vt[P::at(i) / 16 + 2 * c + 1][e] = __builtin_amdgcn_perm(h[2 * e + 1][c], h[2 * e][c], 0x07060302u);
-          }
-      }
-    } else {
-      const uint16_t* kb = reinterpret_cast<const uint16_t*>(a.c.k);
-      const uint16_t* vb = reinterpret_cast<const uint16_t*>(a.c.v);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint16_t* kp = kb + (krow + 4 * u) * D + 8 * q;
-        s[u] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j)
-          s[u] = mfma<false>(*reinterpret_cast<const u32x4*>(kp + 32 * j), qf[j], s[u]);
-      }
-#pragma unroll
-      for (int i = 0; i < P::count; ++i) {
-        const int per16 = P::size(i) / 16;
-        uint32_t h[8][4];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint16_t* w = vb + (vrow + e) * D + P::at(i) + per16 * r;
-          if (per16 == 8) {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(w);
-            h[e][0] = x.x; h[e][1] = x.y; h[e][2] = x.z; h[e][3] = x.w;
-          } else if (per16 == 4) {
-            const u32x2 x = *reinterpret_cast<const u32x2*>(w);
-            h[e][0] = x.x; h[e][1] = x.y;
-          } else {
-            h[e][0] = *reinterpret_cast<const uint32_t*>(w);
-          }
-        }
-        if (!all) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int c = 0; c < per16 / 2; ++c) h[e][c] = (seen >> e) & 1 ? h[e][c] : 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < per16 / 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            vt[P::at(i) / 16 + 2 * c][e] = __builtin_amdgcn_perm(h[2 * e + 1][c], h[2 * e][c], 0x05040100u);
-            vt[P::at(i) / 16 + 2 * c + 1][e] = __builtin_amdgcn_perm(h[2 * e + 1][c], h[2 * e][c], 0x07060302u);
-          }
-      }
+    for (int n = 0; n < N; ++n) {
+      gk[n] = find_group(p, table, t + 32 * n + 8 * (r >> 2), end);
+      gv[n] = find_group(p, table, t + 32 * n + 8 * q, end);
     }
+  };
+  auto load_k = [&]() {
+#pragma unroll
+    for (int n = 0; n < N; ++n) raw[n].load_k(a.c, row_of(p, gk[n], head) + (r & 3), q);
+  };
+  auto load_v = [&](const Group (&g)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) raw[n].load_v(a.c, row_of(p, g[n], head), r);
+  };
+  int t = begin + 32 * N * wave;
+  if (t < end) {
+    find(t);
+    load_k();
+    load_v(gv);
+#pragma unroll
+    for (int n = 0; n < N; ++n) v_held[n] = held(p, gv[n]);
+    find(t + kStride);
+  }
+  for (; t < end; t += kStride) {
+    uint32_t seen[N];                          // bit e: token e of the lane is visible
+    bool all = true;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int tok = t + 32 * n + 8 * q;      // visible: tokens first .. end - 1 of the 8
+      const int lo = min(max(rg.first - tok, 0), 8), hi = min(max(end - tok, 0), 8);
+      seen[n] = v_held[n] ? (0xffu >> (8 - hi)) & (0xffu << lo) & 0xffu : 0u;
+      all = all && seen[n] == 0xffu;
+    }
+    all = __all(all);
 
-    // scores in powers of two, masked; running maximum and weights
-    float w[8], top = -INFINITY;
+    // scores in powers of two
+    float w[N][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[e] = s[e >> 2][e & 3] * cs;
-      if (!all && !((seen >> e) & 1)) w[e] = -INFINITY;
-      top = fmaxf(top, w[e]);
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) s = mfma<kNVFP4>(raw[n].k_step(u, j), qf[j], s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[n][4 * u + i] = s[i] * cs;
+      }
+    // the next step's page ids have arrived: its K, and the ids after it
+    const bool more = t + kStride < end;       // the same for every lane
+    Group next_v[N];
+    if (more) {
+      load_k();
+#pragma unroll
+      for (int n = 0; n < N; ++n) next_v[n] = gv[n];
+      find(t + 2 * kStride);
     }
-    top = max_over_groups(top);
-    if (__any(top > m)) {
-      const float m2 = fmaxf(m, top);
+    if (!all) {
+      asm volatile("");                        // a branch, not selects in every step
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        raw[n].mask_v(seen[n]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[n][e] = (seen[n] >> e) & 1 ? w[n][e] : -INFINITY;
+      }
+    }
+    // Rescaling.  m is a common reference of a head's four lanes rather than the exact
+    // maximum: it moves only when a score is more than 2^kSlack above it, so that most
+    // steps need neither the exchange between the lanes nor the products with o.  Weights
+    // are then at most 2^kSlack, well inside half precision.
+    float top = w[0][0];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, w[n][e]);
+    if (__any(top > m + kSlack)) {
+      const float m2 = fmaxf(m, max_over_groups(top));
       const float f = m2 == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
       m = m2;
       l *= f;
@@ -367,27 +505,45 @@ __global__ __launch_bounds__(kThreads) void paged_decode_kernel(Plan p) {
       for (int i = 0; i < kTiles; ++i) o[i] *= f;
     }
     const float m0 = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[e] = __builtin_amdgcn_exp2f(w[e] - m0);
-      l += w[e];
-    }
     // weights of the second product: half precision (11 bits) beside exact half-precision
     // V; beside bf16 V as the sum of two bf16 (16 bits), since one would round the weights
     // to 8 bits
-    u32x4 hi;
+    u32x4 hi[N], lo[N];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      hi[e] = kNVFP4 ? pack_f16x2(w[2 * e], w[2 * e + 1]) : pack_bf16x2(w[2 * e], w[2 * e + 1]);
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) o[i] = mfma<kNVFP4>(vt[i], hi, o[i]);
-    if constexpr (!kNVFP4) {
-      u32x4 lo;
+      for (int e = 0; e < 8; ++e) {
+        w[n][e] = __builtin_amdgcn_exp2f(w[n][e] - m0);
+        l += w[n][e];
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        lo[e] = pack_bf16x2(w[2 * e] - bf16_lo(hi[e]), w[2 * e + 1] - bf16_hi(hi[e]));
+      for (int e = 0; e < 4; ++e) {
+        const float x = w[n][2 * e], y = w[n][2 * e + 1];
+        if constexpr (kNVFP4) {
+          hi[n][e] = pack_f16x2(x, y);
+        } else {
+          hi[n][e] = pack_bf16x2(x, y);
+          lo[n][e] = pack_bf16x2(x - bf16_lo(hi[n][e]), y - bf16_hi(hi[n][e]));
+        }
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) o[i] = mfma<false>(vt[i], lo, o[i]);
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        u32x4 even, odd;
+        raw[n].v_tiles(i, even, odd);
+        o[2 * i] = mfma<kNVFP4>(even, hi[n], o[2 * i]);
+        o[2 * i + 1] = mfma<kNVFP4>(odd, hi[n], o[2 * i + 1]);
+        if constexpr (!kNVFP4) {
+          o[2 * i] = mfma<false>(even, lo[n], o[2 * i]);
+          o[2 * i + 1] = mfma<false>(odd, lo[n], o[2 * i + 1]);
+        }
+      }
+    if (more) {
+      load_v(next_v);
+#pragma unroll
+      for (int n = 0; n < N; ++n) v_held[n] = held(p, next_v[n]);
     }
   }
 
@@ -447,7 +603,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Plan p) {
   const DecodeArgs& a = p.a;
   const int lane = threadIdx.x & 63;
   const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int chunk = chunk_tokens(p, lane, 32 * kWaves);
+  const int chunk = chunk_tokens(p, lane);
   const int n = chunks_of(range_of(p, a.lens[b]), chunk);
   if (n == 1) return;
   const int per = a.c.heads * p.groups;
