@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;   // work-items of one launch
 constexpr int kMinPage = 16, kMaxPage = 4096;
 constexpr int kMaxHeadDim = 256;
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;   // of one sequence
@@ -32,6 +33,7 @@ fos_status check_wlinear(const fos::WLinearArgs& a, int out_dtype) {
   if (a.x_stride < 0 || (a.M > 1 && (a.x_stride < a.K || a.x_stride > kMaxElems / a.M)))
     return FOS_E_SHAPE;
   if (a.M == 0) return FOS_OK;
+  if (fos::wlinear_threads(a) > kMaxThreads) return FOS_E_SHAPE;
   if (!a.x || !a.wd || !a.ws || !a.y || (!a.mx && !a.wt)) return FOS_E_NULL;
   if (!aligned(a.x, 16) || (a.M > 1 && a.x_stride % 8) || !aligned(a.wd, 16) ||
       !aligned(a.ws, 4) || (!a.mx && !aligned(a.wt, 4)) || (a.bias && !aligned(a.bias, 2)) ||

@@ -18,6 +18,7 @@ struct WLinearArgs {
   int64_t M, N, K;
   bool mx, f32_out;
 };
+int64_t wlinear_threads(const WLinearArgs& a);   // work-items of the launch
 hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s);
 
 // Paged key-value cache: [page][kv head][token of the page][value].
