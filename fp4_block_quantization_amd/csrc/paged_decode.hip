@@ -167,6 +167,13 @@ template <int kSel>
 __device__ __forceinline__ uint32_t dequant2(uint32_t w, f16x2 s) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, kSel) * s);
 }
+// The two E4M3 scales in the low or high half of w.
+__device__ __forceinline__ f16x2 scale_pair(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
+}
+__device__ __forceinline__ f16x2 scale_pair_hi(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
+}
 // The nibbles selected by 0x0f0f0f0f from x, the others from y.
 __device__ __forceinline__ uint32_t low_nibbles(uint32_t x, uint32_t y) {
   return (x & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
@@ -186,53 +193,51 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
 }
 
-// Page id of the group of 8 tokens that starts at `tok` (a group never crosses a page)
-// and the group's first row in the page; id -1 past `end`.
-struct Group {
-  int id, off;
-};
-__device__ __forceinline__ Group find_group(const Plan& p, const int32_t* table, int tok, int end) {
-  const uint32_t g = (uint32_t)tok >> 3;
-  const int page = (int)((g * p.page_magic) >> 36);
-  Group x;
-  x.id = tok < end ? table[page] : -1;
-  x.off = tok - page * p.a.c.page_size;
-  return x;
-}
-__device__ __forceinline__ bool held(const Plan& p, const Group& x) {
-  return (uint32_t)x.id < (uint32_t)p.a.c.num_pages;   // num_pages < 2^31
-}
-// The group's first row in the cache; row 0 for a page that is not held (what is read
-// there is masked).
-__device__ __forceinline__ int64_t row_of(const Plan& p, const Group& x, int head) {
-  return held(p, x) ? ((int64_t)x.id * p.a.c.heads + head) * p.a.c.page_size + x.off : 0;
-}
+// K and V of one step of a wave (kTokens tokens), on their way from memory to the
+// operands.  A load instruction whose neighbouring lanes sit in different rows costs the
+// address unit a line per lane, so what an operand wants row by row (K, and everything of
+// an NVFP4 cache: its rows are short) is loaded in memory order, 16 bytes per lane, and
+// goes through the wave's own piece of LDS.  Loads stay in registers until the next step.
+//
+// 16-byte units of a row are stored at (unit ^ key): with the key of the row below, the 16
+// rows of an operand read start in different banks.
+__host__ __device__ constexpr int pow2_part(int n) { return n & -n; }
 
-// K and V of 32 tokens as one lane loads them: K rows as A operand rows, V rows of the
-// lane's 8 tokens.
 template <bool kNVFP4, int D>
-struct Raw;
+struct Step;
+
 template <int D>
-struct Raw<false, D> {
+struct Step<false, D> {
   using P = Pieces<D>;
-  u32x4 k[2][D / 32];
-  uint32_t v[8][D / 32];
-  __device__ __forceinline__ void load_k(const KVCacheArgs& c, int64_t row, int q) {
-    const uint16_t* base = reinterpret_cast<const uint16_t*>(c.k) + row * D + 8 * q;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j)
-        k[u][j] = *reinterpret_cast<const u32x4*>(base + 4 * u * D + 32 * j);
+  static constexpr int kTokens = 32;
+  static constexpr int kUnits = D / 8;               // 16-byte units of a K row
+  static constexpr int kLoads = D / 16;              // units of a lane: 32 * kUnits / 64
+  static constexpr int kLds = kTokens * D * 2;       // K
+  u32x4 kr[kLoads];
+  uint32_t v[8][D / 32];                             // V: rows of the lane's 8 tokens
+  static __device__ __forceinline__ int key(int row) {
+    return ((row >> 3) << 2 | (row & 3)) & (pow2_part(kUnits) - 1);
   }
-  __device__ __forceinline__ void load_v(const KVCacheArgs& c, int64_t row, int r) {
-    const uint16_t* base = reinterpret_cast<const uint16_t*>(c.v) + row * D;
+  __device__ __forceinline__ void load(const KVCacheArgs& c, uint32_t row8, int lane) {
+    const u32x4* kb = reinterpret_cast<const u32x4*>(c.k);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = lane + 64 * i, row = at / kUnits, u = at % kUnits;
+      const uint32_t r8 = __shfl(row8, row >> 3);
+      kr[i] = kb[((uint64_t)r8 * 8 + (row & 7)) * kUnits + u];
+    }
+  }
+  // V of the next step, once this one's is used
+  __device__ __forceinline__ void load_late(const KVCacheArgs& c, uint32_t row8, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+    const uint16_t* vb =
+        reinterpret_cast<const uint16_t*>(c.v) + (uint64_t)__shfl(row8, q) * (8 * D);
 #pragma unroll
     for (int i = 0; i < P::count; ++i) {
       const int n = P::size(i) / 16, at = P::at(i) / 32;   // values of the lane; its dwords
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint16_t* w = base + P::at(i) + n * r + e * D;
+        const uint16_t* w = vb + P::at(i) + n * r + e * D;
         if (n == 8) {
           const u32x4 x = *reinterpret_cast<const u32x4*>(w);
           v[e][at] = x.x; v[e][at + 1] = x.y; v[e][at + 2] = x.z; v[e][at + 3] = x.w;
@@ -245,123 +250,196 @@ struct Raw<false, D> {
       }
     }
   }
-  __device__ __forceinline__ u32x4 k_step(int u, int j) const { return k[u][j]; }
-  __device__ __forceinline__ void mask_v(uint32_t seen) {
+  __device__ __forceinline__ void stage(uint8_t* lds, int lane) {
+    u32x4* l = reinterpret_cast<u32x4*>(lds);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = lane + 64 * i, row = at / kUnits, u = at % kUnits;
+      l[row * kUnits + (u ^ key(row))] = kr[i];
+    }
+  }
+  // Scores of 16 tokens: operand rows r = tokens 8 (r / 4) + 4 u + r % 4.
+  __device__ __forceinline__ f32x4 scores(const uint8_t* lds, const u32x4 (&qf)[D / 32], int,
+                                          int u, int r, int q) const {
+    const int row = 8 * (r >> 2) + 4 * u + (r & 3);
+    const u32x4* l = reinterpret_cast<const u32x4*>(lds) + row * kUnits;
+    f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) s = mfma<false>(l[(4 * j + q) ^ key(row)], qf[j], s);
+    return s;
+  }
+  __device__ __forceinline__ void mask_v(uint8_t*, const uint32_t* seen, int) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) v[e][i] = (seen >> e) & 1 ? v[e][i] : 0u;
+      for (int i = 0; i < D / 32; ++i) v[e][i] = (seen[0] >> e) & 1 ? v[e][i] : 0u;
   }
-  // Tiles 2 i and 2 i + 1 of V^T: two values of each of the 8 tokens.
-  __device__ __forceinline__ void v_tiles(int i, u32x4& even, u32x4& odd) const {
+  // o += V^T P^T: tiles 2 i and 2 i + 1 take two values of each of the 8 tokens.
+  __device__ __forceinline__ void accumulate(const uint8_t*, f32x4 (&o)[D / 16], int,
+                                             const u32x4& hi, const u32x4& lo, int, int) const {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      even[e] = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x05040100u);
-      odd[e] = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x07060302u);
-    }
-  }
-};
-template <int D>
-struct Raw<true, D> {
-  using P = Pieces<D>;
-  uint32_t k[2][D / 32];           // 8 nibbles of each step
-  uint32_t ks[2][P::count];        // one or two block scales of each piece
-  uint32_t v[8][P::count];         // 8, 4 or 2 nibbles
-  uint32_t vs[8][P::count];        // their block scale
-  __device__ __forceinline__ void load_k(const KVCacheArgs& c, int64_t row, int q) {
-    const uint8_t* base = c.k + row * (D / 2);
-    const uint8_t* sbase = c.ks + row * (D / 16);
+    for (int i = 0; i < D / 32; ++i) {
+      u32x4 even, odd;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < P::count; ++i) {
-        const int n = P::size(i) / 32, at = P::at(i) / 32;
-        const uint8_t* w = base + 4 * u * (D / 2) + P::at(i) / 2 + 4 * n * q;
-        const uint8_t* sp = sbase + 4 * u * (D / 16) + P::at(i) / 16;
-        if (n == 4) {
-          const u32x4 x = *reinterpret_cast<const u32x4*>(w);
-          k[u][at] = x.x; k[u][at + 1] = x.y; k[u][at + 2] = x.z; k[u][at + 3] = x.w;
-          ks[u][i] = *reinterpret_cast<const uint16_t*>(sp + 2 * q);
-        } else if (n == 2) {
-          const u32x2 x = *reinterpret_cast<const u32x2*>(w);
-          k[u][at] = x.x; k[u][at + 1] = x.y;
-          ks[u][i] = sp[q];
-        } else {
-          k[u][at] = *reinterpret_cast<const uint32_t*>(w);
-          ks[u][i] = sp[q / 2];
-        }
+      for (int e = 0; e < 4; ++e) {
+        even[e] = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x05040100u);
+        odd[e] = __builtin_amdgcn_perm(v[2 * e + 1][i], v[2 * e][i], 0x07060302u);
       }
-  }
-  __device__ __forceinline__ void load_v(const KVCacheArgs& c, int64_t row, int r) {
-    const uint8_t* base = c.v + row * (D / 2);
-    const uint8_t* sbase = c.vs + row * (D / 16);
-#pragma unroll
-    for (int i = 0; i < P::count; ++i) {
-      const int n = P::size(i) / 16;
-      const uint8_t* w = base + P::at(i) / 2 + n * r / 2;
-      const uint8_t* sp = sbase + (P::at(i) + n * r) / 16;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint8_t* we = w + e * (D / 2);
-        v[e][i] = n == 8 ? *reinterpret_cast<const uint32_t*>(we)
-                  : n == 4 ? *reinterpret_cast<const uint16_t*>(we) : *we;
-        vs[e][i] = sp[e * (D / 16)];
-      }
-    }
-  }
-  __device__ __forceinline__ u32x4 k_step(int u, int j) const {
-    int i = 0;
-#pragma unroll
-    for (int x = 1; x < P::count; ++x) i = 32 * j >= P::at(x) ? x : i;
-    const int in = j - P::at(i) / 32;          // step of the piece
-    const f16x2 s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(ks[u][i], 1.0f, false);
-    const _Float16 x = in >= 2 ? s.y : s.x;
-    return dequant8(k[u][j], f16x2{x, x});
-  }
-  __device__ __forceinline__ void mask_v(uint32_t seen) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-#pragma unroll
-      for (int i = 0; i < P::count; ++i) vs[e][i] = (seen >> e) & 1 ? vs[e][i] : 0u;
-  }
-  // The nibbles of two tokens are brought together (four tokens' worth of bit selects for
-  // eight conversions), so that one conversion gives two tokens of one d.
-  __device__ __forceinline__ void v_tiles(int t, u32x4& even, u32x4& odd) const {
-    int i = 0;
-#pragma unroll
-    for (int x = 1; x < P::count; ++x) i = 32 * t >= P::at(x) ? x : i;
-    const int sel = t - P::at(i) / 32;         // byte of the word
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const f16x2 s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(vs[2 * e][i] | vs[2 * e + 1][i] << 8,
-                                                               1.0f, false);
-      const uint32_t a = low_nibbles(v[2 * e][i], v[2 * e + 1][i] << 4);
-      const uint32_t b = low_nibbles(v[2 * e][i] >> 4, v[2 * e + 1][i]);
-      even[e] = sel == 0 ? dequant2<0>(a, s) : sel == 1 ? dequant2<1>(a, s)
-                : sel == 2 ? dequant2<2>(a, s) : dequant2<3>(a, s);
-      odd[e] = sel == 0 ? dequant2<0>(b, s) : sel == 1 ? dequant2<1>(b, s)
-               : sel == 2 ? dequant2<2>(b, s) : dequant2<3>(b, s);
+      o[2 * i] = mfma<false>(even, hi, o[2 * i]);
+      o[2 * i + 1] = mfma<false>(odd, hi, o[2 * i + 1]);
+      o[2 * i] = mfma<false>(even, lo, o[2 * i]);
+      o[2 * i + 1] = mfma<false>(odd, lo, o[2 * i + 1]);
     }
   }
 };
 
-// Tokens of one step of a wave: 64 of an NVFP4 cache of up to 128 values, else 32 (the
-// K and V of a step are held in registers).
-template <bool kNVFP4, int D>
-constexpr int kSub = kNVFP4 && D <= 128 ? 2 : 1;
-// Waves per SIMD that the registers are shared out for.
-template <bool kNVFP4, int D>
-constexpr int kMinWaves = !kNVFP4 && D > 160 ? 1 : 2;
+template <int D>
+struct Step<true, D> {
+  using P = Pieces<D>;
+  static constexpr int kTokens = 64;
+  static constexpr int kRow = D / 2;                 // bytes of a row
+  static constexpr int kUnits = D / 32;              // its 16-byte units, and those of a lane
+  static constexpr int kBlocks = D / 16;             // its block scales
+  static constexpr int kV = kTokens * kRow, kKS = 2 * kV, kVS = kKS + kTokens * kBlocks;
+  static constexpr int kLds = kVS + kTokens * kBlocks;
+  u32x4 kr[kUnits], vr[kUnits];
+  uint16_t ksr[kBlocks / 2], vsr[kBlocks / 2];       // of row `lane`
+  static __device__ __forceinline__ int key(int row) { return (row >> 3) & 3 & (pow2_part(kUnits) - 1); }
+  __device__ __forceinline__ void load(const KVCacheArgs& c, uint32_t row8, int lane) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int at = lane + 64 * i, row = at / kUnits, u = at % kUnits;
+      const uint64_t g = ((uint64_t)__shfl(row8, row >> 3) * 8 + (row & 7)) * kUnits + u;
+      kr[i] = reinterpret_cast<const u32x4*>(c.k)[g];
+      vr[i] = reinterpret_cast<const u32x4*>(c.v)[g];
+    }
+    const uint64_t g = ((uint64_t)__shfl(row8, lane >> 3) * 8 + (lane & 7)) * kBlocks;
+    __builtin_memcpy(ksr, __builtin_assume_aligned(c.ks + g, pow2_part(kBlocks)), kBlocks);
+    __builtin_memcpy(vsr, __builtin_assume_aligned(c.vs + g, pow2_part(kBlocks)), kBlocks);
+  }
+  __device__ __forceinline__ void load_late(const KVCacheArgs&, uint32_t, int) {}
+  // K scales as they are ([token][block]); V scales by block ([block][token]), so that a
+  // lane reads the scales of its 8 tokens at once.
+  __device__ __forceinline__ void stage(uint8_t* lds, int lane) {
+    u32x4* l = reinterpret_cast<u32x4*>(lds);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int at = lane + 64 * i, row = at / kUnits, u = at % kUnits;
+      l[row * kUnits + (u ^ key(row))] = kr[i];
+      l[kV / 16 + row * kUnits + (u ^ key(row))] = vr[i];
+    }
+    __builtin_memcpy(__builtin_assume_aligned(lds + kKS + lane * kBlocks, pow2_part(kBlocks)), ksr,
+                     kBlocks);
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+      lds[kVS + i * kTokens + lane] = (uint8_t)(vsr[i / 2] >> (8 * (i % 2)));
+  }
+  __device__ __forceinline__ f32x4 scores(const uint8_t* lds, const u32x4 (&qf)[D / 32], int n,
+                                          int u, int r, int q) const {
+    const int row = 32 * n + 8 * (r >> 2) + 4 * u + (r & 3);
+    const uint8_t* l = lds + row * kRow;
+    const uint8_t* sp = lds + kKS + row * kBlocks;
+    f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < P::count; ++i) {
+      const int steps = P::size(i) / 32, j0 = P::at(i) / 32;
+      // the lane's 4 * steps bytes of the piece: in unit j0 + steps q / 4
+      const uint8_t* w = l + 16 * ((j0 + steps * q / 4) ^ key(row)) + (4 * steps * q) % 16;
+      uint32_t word[4];
+      f16x2 sc;
+      if (steps == 4) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(w);
+        word[0] = x.x; word[1] = x.y; word[2] = x.z; word[3] = x.w;
+        sc = scale_pair(*reinterpret_cast<const uint16_t*>(sp + 2 * j0 + 2 * q));
+      } else if (steps == 2) {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(w);
+        word[0] = x.x; word[1] = x.y;
+        sc = scale_pair(sp[2 * j0 + q]);
+      } else {
+        word[0] = *reinterpret_cast<const uint32_t*>(w);
+        sc = scale_pair(sp[2 * j0 + q / 2]);
+      }
+#pragma unroll
+      for (int j = 0; j < steps; ++j) {
+        const _Float16 x = j >= 2 ? sc.y : sc.x;
+        s = mfma<true>(dequant8(word[j], f16x2{x, x}), qf[j0 + j], s);
+      }
+    }
+    return s;
+  }
+  __device__ __forceinline__ void mask_v(uint8_t* lds, const uint32_t* seen, int lane) {
+    // lane r < 8 of group q holds the mask of groups q and 4 + q of 8 tokens: each of the
+    // group's 16 lanes clears the scales of one token and half
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int tok = 32 * n + 8 * (lane >> 4) + (lane & 7);
+      if ((lane & 8) == 0 && !((seen[n] >> (lane & 7)) & 1)) {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) lds[kVS + i * kTokens + tok] = 0;
+      }
+    }
+  }
+  // The nibbles of two tokens are brought together (four bit selects for eight
+  // conversions), so that one conversion gives two tokens of one d.
+  __device__ __forceinline__ void accumulate(const uint8_t* lds, f32x4 (&o)[D / 16], int n,
+                                             const u32x4& hi, const u32x4&, int r, int q) const {
+    const int tok = 32 * n + 8 * q;                  // one key for the group's 8 rows
+#pragma unroll
+    for (int i = 0; i < P::count; ++i) {
+      const int bytes = P::size(i) / 32;             // of the lane and token: 4, 2 or 1
+      const int b = P::at(i) / 2 + bytes * r;
+      const uint8_t* w = lds + kV + tok * kRow + 16 * ((b / 16) ^ key(tok)) + b % 16;
+      const u32x2 sb = *reinterpret_cast<const u32x2*>(lds + kVS + (b / 8) * kTokens + tok);
+      uint32_t lo[4], up[4];
+      f16x2 sc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t x, y;
+        if (bytes == 4) {
+          x = *reinterpret_cast<const uint32_t*>(w + 2 * e * kRow);
+          y = *reinterpret_cast<const uint32_t*>(w + (2 * e + 1) * kRow);
+        } else if (bytes == 2) {
+          x = *reinterpret_cast<const uint16_t*>(w + 2 * e * kRow);
+          y = *reinterpret_cast<const uint16_t*>(w + (2 * e + 1) * kRow);
+        } else {
+          x = w[2 * e * kRow];
+          y = w[(2 * e + 1) * kRow];
+        }
+        lo[e] = low_nibbles(x, y << 4);
+        up[e] = low_nibbles(x >> 4, y);
+        sc[e] = e & 1 ? scale_pair_hi(sb[e / 2]) : scale_pair(sb[e / 2]);
+      }
+#pragma unroll
+      for (int j = 0; j < bytes; ++j) {
+        u32x4 even, odd;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          even[e] = j == 0 ? dequant2<0>(lo[e], sc[e]) : j == 1 ? dequant2<1>(lo[e], sc[e])
+                    : j == 2 ? dequant2<2>(lo[e], sc[e]) : dequant2<3>(lo[e], sc[e]);
+          odd[e] = j == 0 ? dequant2<0>(up[e], sc[e]) : j == 1 ? dequant2<1>(up[e], sc[e])
+                   : j == 2 ? dequant2<2>(up[e], sc[e]) : dequant2<3>(up[e], sc[e]);
+        }
+        const int t = P::at(i) / 16 + 2 * j;
+        o[t] = mfma<true>(even, hi, o[t]);
+        o[t + 1] = mfma<true>(odd, hi, o[t + 1]);
+      }
+    }
+  }
+};
+
 constexpr float kSlack = 8.0f;    // see the rescaling below
 
 template <bool kNVFP4, int D>
-__global__ __launch_bounds__(kThreads, (kMinWaves<kNVFP4, D>)) void paged_decode_kernel(Plan p) {
+__global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void paged_decode_kernel(Plan p) {
   constexpr int kSteps = D / 32;               // 32-value steps of the first product
   constexpr int kTiles = D / 16;               // 16-row tiles of the second
   constexpr int kPad = D + 4;
-  constexpr int N = kSub<kNVFP4, D>;
   using P = Pieces<D>;
-  __shared__ __attribute__((aligned(16))) float so[kWaves][kHeads][kPad];
+  using S = Step<kNVFP4, D>;
+  constexpr int N = S::kTokens / 32;
+  constexpr int kJoin = kHeads * kPad * 4;     // bytes of a wave's o
+  // the waves' pieces during the steps, their o after them
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * (S::kLds > kJoin ? S::kLds : kJoin)];
   __shared__ float sm[kWaves][kHeads], sl[kWaves][kHeads];
   const DecodeArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -407,7 +485,17 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<kNVFP4, D>)) void paged_decode
         const float x = ldexpf(bf16_lo(raw[j][i]), -e), y = ldexpf(bf16_hi(raw[j][i]), -e);
         qf[j][i] = kNVFP4 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
       }
-    cs = ldexpf(a.scale * kLog2e * (kNVFP4 ? a.c.kt[0] : 1.0f), e);
+    // the sign of the scale goes into the queries: cs >= 0, and the maximum can be taken
+    // before the scale (a scale of 0 as queries of 0: -inf * 0 is not -inf)
+    const float full = ldexpf(a.scale * kLog2e * (kNVFP4 ? a.c.kt[0] : 1.0f), e);
+    cs = full == 0.0f ? 1.0f : fabsf(full);
+    if (!(full > 0.0f)) {
+      const uint32_t flip = full < 0.0f ? 0x80008000u : 0u, keep = full < 0.0f ? ~0u : 0u;
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[j][i] = (qf[j][i] & keep) ^ flip;
+    }
   }
 
   f32x4 o[kTiles];
@@ -415,77 +503,70 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<kNVFP4, D>)) void paged_decode
   for (int i = 0; i < kTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
   float m = -INFINITY, l = 0.0f;
 
-  // Pipeline of a wave's steps: page ids two steps ahead, K one step ahead from the end of
-  // the first product, V from the end of the second.
-  constexpr int kStride = 32 * N * kWaves;
-  Raw<kNVFP4, D> raw[N];
-  Group gk[N], gv[N];
-  bool v_held[N];
-  auto find = [&](int t) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      gk[n] = find_group(p, table, t + 32 * n + 8 * (r >> 2), end);
-      gv[n] = find_group(p, table, t + 32 * n + 8 * q, end);
-    }
+  // Pipeline of a wave's steps: page ids two steps ahead, K and V one.  Lane i (mod 8)
+  // looks up the page of group i (mod groups) of 8 tokens (a group never crosses a page).
+  constexpr int kGroups = S::kTokens / 8, kStride = S::kTokens * kWaves;
+  uint8_t* mine = lds + wave * S::kLds;
+  S step;
+  int id, page;                                // of the step after the one being loaded
+  auto look_up = [&](int t) {
+    const int tok = t + 8 * (lane % kGroups);
+    page = (int)((((uint32_t)tok >> 3) * p.page_magic) >> 36);
+    id = tok < end ? table[page] : -1;
   };
-  auto load_k = [&]() {
-#pragma unroll
-    for (int n = 0; n < N; ++n) raw[n].load_k(a.c, row_of(p, gk[n], head) + (r & 3), q);
+  uint32_t held = 0, next_held = 0;            // bit i: group i's page is held
+  uint32_t row8 = 0;
+  auto load = [&](int t) {
+    const bool in = (uint32_t)id < (uint32_t)a.c.num_pages;
+    // rows of the cache in groups of 8 (fewer than 2^32); where no page is held row 0 is
+    // read and masked
+    const int off = t + 8 * (lane % kGroups) - page * a.c.page_size;
+    row8 = in ? ((uint32_t)id * a.c.heads + head) * ((uint32_t)a.c.page_size >> 3) +
+                               ((uint32_t)off >> 3) : 0u;
+    next_held = (uint32_t)__ballot(in);
+    step.load(a.c, row8, lane);
   };
-  auto load_v = [&](const Group (&g)[N]) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) raw[n].load_v(a.c, row_of(p, g[n], head), r);
-  };
-  int t = begin + 32 * N * wave;
+  int t = begin + S::kTokens * wave;
   if (t < end) {
-    find(t);
-    load_k();
-    load_v(gv);
-#pragma unroll
-    for (int n = 0; n < N; ++n) v_held[n] = held(p, gv[n]);
-    find(t + kStride);
+    look_up(t);
+    load(t);
+    step.load_late(a.c, row8, lane);
+    look_up(t + kStride);
   }
   for (; t < end; t += kStride) {
-    uint32_t seen[N];                          // bit e: token e of the lane is visible
+    step.stage(mine, lane);
+    held = next_held;
+    if (t + kStride < end) {
+      load(t + kStride);
+      look_up(t + 2 * kStride);
+    }
+    uint32_t seen[N];                          // bit e: token e of the lane's 8 is visible
     bool all = true;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int tok = t + 32 * n + 8 * q;      // visible: tokens first .. end - 1 of the 8
       const int lo = min(max(rg.first - tok, 0), 8), hi = min(max(end - tok, 0), 8);
-      seen[n] = v_held[n] ? (0xffu >> (8 - hi)) & (0xffu << lo) & 0xffu : 0u;
+      seen[n] = (held >> (4 * n + q)) & 1 ? (0xffu >> (8 - hi)) & (0xffu << lo) & 0xffu : 0u;
       all = all && seen[n] == 0xffu;
     }
     all = __all(all);
 
-    // scores in powers of two
-    float w[N][8];
+    float w[N][8];                             // scores, before cs
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        f32x4 s = {0, 0, 0, 0};
+        const f32x4 s = step.scores(mine, qf, n, u, r, q);
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) s = mfma<kNVFP4>(raw[n].k_step(u, j), qf[j], s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[n][4 * u + i] = s[i] * cs;
+        for (int i = 0; i < 4; ++i) w[n][4 * u + i] = s[i];
       }
-    // the next step's page ids have arrived: its K, and the ids after it
-    const bool more = t + kStride < end;       // the same for every lane
-    Group next_v[N];
-    if (more) {
-      load_k();
-#pragma unroll
-      for (int n = 0; n < N; ++n) next_v[n] = gv[n];
-      find(t + 2 * kStride);
-    }
     if (!all) {
       asm volatile("");                        // a branch, not selects in every step
+      step.mask_v(mine, seen, lane);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        raw[n].mask_v(seen[n]);
+      for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[n][e] = (seen[n] >> e) & 1 ? w[n][e] : -INFINITY;
-      }
     }
     // Rescaling.  m is a common reference of a head's four lanes rather than the exact
     // maximum: it moves only when a score is more than 2^kSlack above it, so that most
@@ -496,6 +577,7 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<kNVFP4, D>)) void paged_decode
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, w[n][e]);
+    top *= cs;
     if (__any(top > m + kSlack)) {
       const float m2 = fmaxf(m, max_over_groups(top));
       const float f = m2 == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
@@ -508,44 +590,29 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<kNVFP4, D>)) void paged_decode
     // weights of the second product: half precision (11 bits) beside exact half-precision
     // V; beside bf16 V as the sum of two bf16 (16 bits), since one would round the weights
     // to 8 bits
-    u32x4 hi[N], lo[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
+      u32x4 hi, lo;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        w[n][e] = __builtin_amdgcn_exp2f(w[n][e] - m0);
+        w[n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(w[n][e], cs, -m0));
         l += w[n][e];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = w[n][2 * e], y = w[n][2 * e + 1];
         if constexpr (kNVFP4) {
-          hi[n][e] = pack_f16x2(x, y);
+          hi[e] = pack_f16x2(x, y);
         } else {
-          hi[n][e] = pack_bf16x2(x, y);
-          lo[n][e] = pack_bf16x2(x - bf16_lo(hi[n][e]), y - bf16_hi(hi[n][e]));
+          hi[e] = pack_bf16x2(x, y);
+          lo[e] = pack_bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
         }
       }
+      step.accumulate(mine, o, n, hi, lo, r, q);
     }
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        u32x4 even, odd;
-        raw[n].v_tiles(i, even, odd);
-        o[2 * i] = mfma<kNVFP4>(even, hi[n], o[2 * i]);
-        o[2 * i + 1] = mfma<kNVFP4>(odd, hi[n], o[2 * i + 1]);
-        if constexpr (!kNVFP4) {
-          o[2 * i] = mfma<false>(even, lo[n], o[2 * i]);
-          o[2 * i + 1] = mfma<false>(odd, lo[n], o[2 * i + 1]);
-        }
-      }
-    if (more) {
-      load_v(next_v);
-#pragma unroll
-      for (int n = 0; n < N; ++n) v_held[n] = held(p, next_v[n]);
-    }
+    if (t + kStride < end) step.load_late(a.c, row8, lane);
   }
+  __syncthreads();                             // the pieces of LDS take the waves' o
 
   // join the waves
   l = sum_over_groups(l);
@@ -553,6 +620,7 @@ __global__ __launch_bounds__(kThreads, (kMinWaves<kNVFP4, D>)) void paged_decode
     sm[wave][r] = m;
     sl[wave][r] = l;
   }
+  float(*so)[kHeads][kPad] = reinterpret_cast<float(*)[kHeads][kPad]>(lds);
   if (r < rows) {
 #pragma unroll
     for (int i = 0; i < P::count; ++i) {
