@@ -307,10 +307,18 @@ struct Step<true, D> {
   static constexpr int kRow = D / 2;                 // bytes of a row
   static constexpr int kUnits = D / 32;              // its 16-byte units, and those of a lane
   static constexpr int kBlocks = D / 16;             // its block scales
-  static constexpr int kV = kTokens * kRow, kKS = 2 * kV, kVS = kKS + kTokens * kBlocks;
+  // LDS: K, V, their scales as in memory, V's scales by block
+  static constexpr int kV = kTokens * kRow, kKS = 2 * kV, kVR = kKS + kTokens * kBlocks;
+  static constexpr int kVS = kVR + kTokens * kBlocks;
   static constexpr int kLds = kVS + kTokens * kBlocks;
   u32x4 kr[kUnits], vr[kUnits];
-  uint16_t ksr[kBlocks / 2], vsr[kBlocks / 2];       // of row `lane`
+  // Block scales: 8 rows are kUnits units (rows alone may start at any even byte, and loads
+  // off their alignment take several times as long: 18 us with aligned loads against 33
+  // with 6-byte ones, 24 x 12 heads x 1000 tokens of 96 values).  K's and V's in one load
+  // where both have the lanes.
+  static constexpr int kScaleUnits = 8 * kUnits;     // of K, and of V
+  static constexpr bool kOneLoad = 2 * kScaleUnits <= 64;
+  u32x4 sr[kOneLoad ? 1 : 2];
   static __device__ __forceinline__ int key(int row) { return (row >> 3) & 3 & (pow2_part(kUnits) - 1); }
   __device__ __forceinline__ void load(const KVCacheArgs& c, uint32_t row8, int lane) {
 #pragma unroll
@@ -320,9 +328,16 @@ struct Step<true, D> {
       kr[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c.k) + g);
       vr[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c.v) + g);
     }
-    const uint64_t g = ((uint64_t)__shfl(row8, lane >> 3) * 8 + (lane & 7)) * kBlocks;
-    __builtin_memcpy(ksr, __builtin_assume_aligned(c.ks + g, pow2_part(kBlocks)), kBlocks);
-    __builtin_memcpy(vsr, __builtin_assume_aligned(c.vs + g, pow2_part(kBlocks)), kBlocks);
+    const int at = kOneLoad ? lane % kScaleUnits : lane;
+    const uint64_t g = (uint64_t)__shfl(row8, at / kUnits) * kUnits + at % kUnits;
+    if constexpr (kOneLoad) {
+      if (lane < 2 * kScaleUnits)
+        sr[0] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>(lane < kScaleUnits ? c.ks : c.vs) + g);
+    } else if (lane < kScaleUnits) {
+      sr[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c.ks) + g);
+      sr[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c.vs) + g);
+    }
   }
   __device__ __forceinline__ void load_late(const KVCacheArgs&, uint32_t, int) {}
   // K scales as they are ([token][block]); V scales by block ([block][token]), so that a
@@ -335,11 +350,19 @@ struct Step<true, D> {
       l[row * kUnits + (u ^ key(row))] = kr[i];
       l[kV / 16 + row * kUnits + (u ^ key(row))] = vr[i];
     }
-    __builtin_memcpy(__builtin_assume_aligned(lds + kKS + lane * kBlocks, pow2_part(kBlocks)), ksr,
-                     kBlocks);
+    if constexpr (kOneLoad) {
+      if (lane < 2 * kScaleUnits) l[kKS / 16 + lane] = sr[0];
+    } else if (lane < kScaleUnits) {
+      l[kKS / 16 + lane] = sr[0];
+      l[kKS / 16 + kScaleUnits + lane] = sr[1];
+    }
+    // transpose V's: a lane takes a token
+    const uint16_t* sp = reinterpret_cast<const uint16_t*>(lds + kVR + lane * kBlocks);
+    uint16_t row[kBlocks / 2];
+    __builtin_memcpy(row, __builtin_assume_aligned(sp, pow2_part(kBlocks)), kBlocks);
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i)
-      lds[kVS + i * kTokens + lane] = (uint8_t)(vsr[i / 2] >> (8 * (i % 2)));
+      lds[kVS + i * kTokens + lane] = (uint8_t)(row[i / 2] >> (8 * (i % 2)));
   }
   __device__ __forceinline__ f32x4 scores(const uint8_t* lds, const u32x4 (&qf)[D / 32], int n,
                                           int u, int r, int q) const {
@@ -451,6 +474,7 @@ __global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void 
   const DecodeArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
+  const float kt0 = kNVFP4 ? a.c.kt[0] : 1.0f, vt0 = kNVFP4 ? a.c.vt[0] : 1.0f;
   const Item it = find_item(p, blockIdx.x, 0);
   if (it.b < 0) return;
   const int head = it.hg / p.groups, g0 = (it.hg % p.groups) * kHeads;
@@ -526,7 +550,7 @@ __global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void 
       }
     // the sign of the scale goes into the queries: cs >= 0, and the maximum can be taken
     // before the scale (a scale of 0 as queries of 0: -inf * 0 is not -inf)
-    const float full = ldexpf(a.scale * kLog2e * (kNVFP4 ? a.c.kt[0] : 1.0f), e);
+    const float full = ldexpf(a.scale * kLog2e * kt0, e);
     cs = full == 0.0f ? 1.0f : fabsf(full);
     if (!(full > 0.0f)) {
       const uint32_t flip = full < 0.0f ? 0x80008000u : 0u, keep = full < 0.0f ? ~0u : 0u;
@@ -643,7 +667,6 @@ __global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void 
   }
   __syncthreads();
   const bool whole = it.count == 1;
-  const float vt0 = kNVFP4 ? a.c.vt[0] : 1.0f;
   float* part = static_cast<float*>(a.ws) + (int64_t)blockIdx.x * part_stride(p);
   for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
     const int g = i / (D / 2), d = 2 * (i % (D / 2));
