@@ -17,6 +17,7 @@ constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;   // work-items of one l
 constexpr int kMinPage = 16, kMaxPage = 4096;
 constexpr int kMaxHeadDim = 256;
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;   // of one sequence
+constexpr int64_t kMaxBatchTokens = (int64_t)1 << 38;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -184,10 +185,12 @@ size_t fos_paged_decode_workspace_bytes(int64_t num_seqs, int64_t num_q_heads,
                                         int64_t num_kv_heads, int64_t head_dim) {
   if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads ||
       head_dim < 1 || head_dim > kMaxHeadDim || num_q_heads >= kMaxDim || num_seqs >= kMaxDim ||
-      num_seqs * num_q_heads >= kMaxDim)
+      num_seqs * num_q_heads >= kMaxDim || !fos::decode_heads_ok(num_q_heads, num_kv_heads))
     return 0;
   return fos::decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim);
 }
+
+size_t fos_paged_decode_counter_bytes(void) { return fos::decode_counter_bytes(); }
 
 fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64_t q_stride,
                             int64_t num_seqs, int64_t num_q_heads, const int32_t* block_table,
@@ -205,9 +208,10 @@ fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64
   if (num_seqs > 1 && (q_stride < width || table_stride < pages_per_seq ||
                        q_stride > kMaxElems / num_seqs || table_stride > kMaxElems / num_seqs))
     return FOS_E_SHAPE;
-  if (num_seqs * num_q_heads > fos::kMaxGrid ||
-      fos::decode_items(num_seqs, num_q_heads, cache->num_kv_heads) > fos::kMaxGrid)
-    return FOS_E_SHAPE;
+  // the device counts steps of 256 tokens of all sequences in 32 bits
+  const int64_t cap = pages_per_seq * cache->page_size;
+  if (num_seqs > 0 && cap > kMaxBatchTokens / num_seqs) return FOS_E_SHAPE;
+  if (!fos::decode_heads_ok(num_q_heads, cache->num_kv_heads)) return FOS_E_SHAPE;
   if (window < 0 || !std::isfinite(softmax_scale)) return FOS_E_FLAGS;
   if (num_seqs == 0) return FOS_OK;
   if (!q_bf16 || !seq_lens || !out_bf16 || (pages_per_seq > 0 && !block_table)) return FOS_E_NULL;

@@ -19,11 +19,14 @@
 // group supplies to the second product.  The weights go from one product into the
 // other without leaving their lane, and the running statistics of a head are per lane.
 //
-// Split.  Every workgroup takes one chunk of one sequence's tokens for one kv head.  The
-// chunk length is set on the device from the lengths themselves (all tokens over the
-// wanted number of workgroups), so that ragged batches stay balanced and the host needs
-// no length.  A sequence of several chunks leaves partial (m, l, o) that a second kernel
-// joins; the order of every sum depends on the lengths alone.
+// Split.  The steps (256 tokens) of all sequences form one list, and for every kv head
+// the workgroups that the GPU holds at once take equal runs of it: all start together and
+// all are done together, however ragged the lengths are.  The lengths are read on the
+// device; the host needs none.  Workgroups of the same run and neighbouring heads are
+// neighbours: they read the same pages at the same time.  A run covers parts of one or
+// more sequences.  A sequence that fell to several runs leaves partial (m, l, o) in the
+// workspace, and the last workgroup to finish joins them in their order: no second
+// launch, nobody waits, and the order of every sum depends on the lengths alone.
 #include "serving.hpp"
 
 namespace fos {
@@ -33,9 +36,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kHeads = 16;            // query heads per workgroup: columns of the products
-constexpr int kTargetItems = 1024;    // chunks wanted over the whole batch
-constexpr int kChunkStep = 64 * kWaves;   // tokens of a chunk: a multiple of this,
-constexpr int kMinSteps = 2;          //   at least this many times
+constexpr int kStepTokens = 64 * kWaves;   // a step of a workgroup
+constexpr int kCUs = 256;
+constexpr int kMaxPerCU = 3;          // workgroups that a CU holds, at most
+constexpr int kMaxSegments = 65536;   // (sequence, head group) segments of one launch
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -53,9 +57,14 @@ struct Plan {
   // x / d = (x * page_magic) >> 36 for d = page_size / 8 (at most 512) and x < 2^27:
   // page_magic = ceil(2^36 / d) is too large by less than 1, x * (less than d) < 2^36
   uint64_t page_magic;
+  int runs;                // per head group
+  uint32_t* arrived;       // per segment: workgroups done with it, 0 between launches
+  float* parts;
 };
 
-// Partial results: per chunk m[rows], l[rows], o[rows][dim].
+// Partial results: (m, l)[rows], o[rows][dim].  Run i of a head group leaves the one of
+// sequence b at i + b: along the list one of the two grows from each to the next, so the
+// places are distinct, and those of a sequence lie in a row.
 __device__ __forceinline__ int64_t part_stride(const Plan& p) {
   return (int64_t)p.rows * (p.a.c.dim + 2);
 }
@@ -84,53 +93,71 @@ __device__ __forceinline__ int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31
   return v;
 }
-__device__ __forceinline__ int steps_of(const Range& r) {            // at most 2^22
-  return (r.last - r.base + kChunkStep - 1) / kChunkStep;
+// Steps of a sequence of this length for one head, at most 2^22; an empty one takes a
+// step to write its zeros.
+__device__ __forceinline__ int steps_of(const Plan& p, int len) {
+  const Range r = range_of(p, len);
+  return max(1, (r.last - r.base + kStepTokens - 1) / kStepTokens);
 }
-__device__ __forceinline__ int chunks_of(const Range& r, int chunk) {
-  return max(1, (steps_of(r) + chunk - 1) / chunk);   // an empty sequence writes its zeros
-}
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// One work item: chunk `chunk` (of `count`, `steps` steps each) of sequence b for head
-// group hg; `first` is the sequence's first item.  b < 0 past the last item.  Every lane
-// of the wave gets the same answer.
-struct Item {
-  int b, chunk, hg, count, steps, first, len;
+// A workgroup's run [pos, end) of the list of steps, and its current sequence: steps
+// [at, at + steps) of the list are sequence b, `len` tokens.  The API keeps the list below
+// 2^31.  Every lane of a wave holds the same values, but for sum and upto: lane i's share
+// of the sequences, i * each and on.
+struct Run {
+  int each, sum, upto, len0;
+  int share, pos, end;
+  int b, len, steps, at;
 };
-// Item `want`, or (with want < 0) the first item of sequence `of`.
-__device__ __forceinline__ Item find_item(const Plan& p, int want, int of) {
-  const int lane = threadIdx.x & 63, per = p.a.c.heads * p.groups, B = p.a.B;
-  // steps of a chunk: all steps over the wanted number of items
-  int len = lane < B ? p.a.lens[lane] : 0;
-  int64_t total = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) {
-    const int x = b0 == 0 ? len : b0 + lane < B ? p.a.lens[b0 + lane] : 0;
-    total += __builtin_amdgcn_readlane(wave_scan(steps_of(range_of(p, x))), 63);
-  }
-  Item it;
-  it.steps = (int)min(max((total * per + kTargetItems - 1) / kTargetItems, (int64_t)kMinSteps),
-                      (int64_t)1 << 22);   // never more than the longest sequence has
-  int before = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) {
-    if (b0) len = b0 + lane < B ? p.a.lens[b0 + lane] : 0;
-    const int n = b0 + lane < B ? chunks_of(range_of(p, len), it.steps) * per : 0;
-    const int upto = wave_scan(n), start = before + upto - n;
-    const uint64_t hit = __ballot(want >= 0 ? want >= start && want < start + n : b0 + lane == of);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      it.b = b0 + l;
-      it.first = __builtin_amdgcn_readlane(start, l);
-      it.len = __builtin_amdgcn_readlane(len, l);
-      it.count = __builtin_amdgcn_readlane(n, l) / per;
-      const int in = want >= 0 ? want - it.first : 0;
-      it.chunk = in / per;
-      it.hg = in - it.chunk * per;
-      return it;
+__device__ __forceinline__ void begin_run(const Plan& p, Run& u, int run) {
+  const int lane = threadIdx.x & 63, B = p.a.B;
+  u.each = (B + 63) >> 6;
+  u.sum = u.len0 = 0;
+  for (int i = 0; i < u.each; ++i) {
+    const int b = lane * u.each + i;
+    if (b < B) {
+      u.len0 = p.a.lens[b];
+      u.sum += steps_of(p, u.len0);
     }
-    before += __builtin_amdgcn_readlane(upto, 63);
   }
-  it.b = -1;
-  return it;
+  u.upto = wave_scan(u.sum);
+  const uint32_t total = (uint32_t)__builtin_amdgcn_readlane(u.upto, 63);
+  u.share = scalar((int)((total + p.runs - 1) / (uint32_t)p.runs));
+  // unsigned: runs * share is below 2^31 + runs
+  const uint32_t pos = (uint32_t)run * (uint32_t)u.share;
+  u.pos = (int)min(pos, total);
+  u.end = (int)min(pos + (uint32_t)u.share, total);
+}
+// The sequence at u.pos.
+__device__ __forceinline__ void find_sequence(const Plan& p, Run& u) {
+  const int lane = threadIdx.x & 63, y = u.pos;
+  int start = u.upto - u.sum;
+  const int l = __ffsll((unsigned long long)__ballot(y >= start && y < u.upto)) - 1;
+  start = __builtin_amdgcn_readlane(start, l);
+  if (u.each == 1) {
+    u.b = l;
+    u.len = __builtin_amdgcn_readlane(u.len0, l);
+    u.steps = __builtin_amdgcn_readlane(u.sum, l);
+  } else {
+    for (int i = 0; i < u.each; i += 64) {
+      const int b = l * u.each + i + lane;
+      const bool in = i + lane < u.each && b < p.a.B;
+      const int len = in ? p.a.lens[b] : 0, n = in ? steps_of(p, len) : 0;
+      const int upto = start + wave_scan(n);
+      const uint64_t hit = __ballot(y >= upto - n && y < upto);
+      if (hit) {
+        const int k = __ffsll((unsigned long long)hit) - 1;
+        u.b = l * u.each + i + k;
+        u.len = __builtin_amdgcn_readlane(len, k);
+        u.steps = __builtin_amdgcn_readlane(n, k);
+        start = __builtin_amdgcn_readlane(upto - n, k);
+        break;
+      }
+      start = __builtin_amdgcn_readlane(upto, 63);
+    }
+  }
+  u.at = start;
 }
 
 // ---- one wave's pieces -------------------------------------------------------------
@@ -459,8 +486,74 @@ struct Step<true, D> {
 
 constexpr float kSlack = 8.0f;    // see the rescaling below
 
+// Partial results pass from one workgroup to another on any XCD, each with an L2 of its
+// own.  A release and an acquire fence at that scope write back and invalidate a whole L2
+// (262 us instead of 92 for 32 sequences of up to 8192 tokens); instead the few values
+// that are passed are themselves accessed at device scope, as relaxed atomics of 8 bytes:
+// the stores write through to memory and the loads read from there.  What orders them is
+// that every thread waits until its stores are done (wait_stores), then the barrier, and
+// only then one thread counts the workgroup: who reads the full count reads after all
+// the stores.
+__device__ __forceinline__ void store_shared(float* p, f32x2 v) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 load_shared(const float* p) {
+  return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p),
+                                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ void wait_stores() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Joins the `count` partials of a segment, in order, and writes its outputs: each thread
+// takes four values of a head, eight partials at a time.
+template <int D>
+__device__ __forceinline__ void join_partials(const Plan& p, const float* all, int count, int rows,
+                                              int64_t hrow0, float vt0) {
+  constexpr int kBatch = 8;
+  const int64_t step = part_stride(p);
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+    const int g = i / (D / 4), d = 4 * (i % (D / 4));
+    float m = -INFINITY, l = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    for (int c = 0; c < count; c += kBatch) {
+      f32x2 ml[kBatch], x[kBatch], y[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float* part = all + min(c + k, count - 1) * step;
+        ml[k] = load_shared(part + 2 * g);
+        x[k] = load_shared(part + 2 * p.rows + g * D + d);
+        y[k] = load_shared(part + 2 * p.rows + g * D + d + 2);
+      }
+      float m2 = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) m2 = fmaxf(m2, ml[k].x);
+      if (m2 == -INFINITY) continue;             // nothing seen so far
+      const float f = __builtin_amdgcn_exp2f(m - m2);
+      m = m2;
+      l *= f;
+      o *= f;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = c + k < count ? __builtin_amdgcn_exp2f(ml[k].x - m) : 0.0f;
+        l += w * ml[k].y;
+        o += w * f32x4{x[k].x, x[k].y, y[k].x, y[k].y};
+      }
+    }
+    const float n = l > 0.0f ? vt0 / l : 0.0f;
+    *reinterpret_cast<u32x2*>(p.a.out + (hrow0 + g) * D + d) =
+        u32x2{pack_bf16x2(o[0] * n, o[1] * n), pack_bf16x2(o[2] * n, o[3] * n)};
+    if (d == 0 && p.a.lse) p.a.lse[hrow0 + g] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
+// Workgroups that a CU holds at once: what the registers of a step leave room for.
 template <bool kNVFP4, int D>
-__global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void paged_decode_kernel(Plan p) {
+constexpr int kPerCU = kNVFP4 ? (D <= 64 ? 3 : D <= 192 ? 2 : 1) : (D <= 64 ? 3 : D <= 128 ? 2 : 1);
+
+template <bool kNVFP4, int D>
+__global__ __launch_bounds__(kThreads, (kPerCU<kNVFP4, D>)) void paged_decode_kernel(Plan p) {
   constexpr int kSteps = D / 32;               // 32-value steps of the first product
   constexpr int kTiles = D / 16;               // 16-row tiles of the second
   constexpr int kPad = D + 4;
@@ -471,19 +564,25 @@ __global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void 
   // the waves' pieces during the steps, their o after them
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * (S::kLds > kJoin ? S::kLds : kJoin)];
   __shared__ float sm[kWaves][kHeads], sl[kWaves][kHeads];
+  __shared__ uint32_t before_me;
   const DecodeArgs& a = p.a;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, q = lane >> 4;
   const float kt0 = kNVFP4 ? a.c.kt[0] : 1.0f, vt0 = kNVFP4 ? a.c.vt[0] : 1.0f;
-  const Item it = find_item(p, blockIdx.x, 0);
-  if (it.b < 0) return;
-  const int head = it.hg / p.groups, g0 = (it.hg % p.groups) * kHeads;
+  const int per = a.c.heads * p.groups, hg = blockIdx.x % per;
+  const int head = hg / p.groups, g0 = (hg % p.groups) * kHeads;
   const int rows = min(kHeads, a.G - g0);
-  const Range rg = range_of(p, it.len);
-  // at most 2^30 tokens: no overflow
-  const int begin = rg.base + it.chunk * it.steps * kChunkStep;
-  const int end = (int)min((int64_t)rg.last, (int64_t)begin + (int64_t)it.steps * kChunkStep);
-  const int32_t* table = a.table + it.b * a.table_stride;
+  Run run;
+  begin_run(p, run, blockIdx.x / per);
+  for (; run.pos < run.end; __syncthreads()) {
+  find_sequence(p, run);
+  const Range rg = range_of(p, run.len);
+  // this workgroup's tokens of the sequence (at most 2^30, and a step more)
+  const int steps = min(run.at + run.steps, run.end) - run.pos;
+  const int begin = rg.base + (run.pos - run.at) * kStepTokens;
+  const int end = min(rg.last, begin + steps * kStepTokens);
+  const bool whole = steps == run.steps;
+  const int32_t* table = a.table + run.b * a.table_stride;
 
   // Pipeline of a wave's steps: page ids two steps ahead, K and V one.  Lane i (mod 8)
   // looks up the page of group i (mod groups) of 8 tokens (a group never crosses a page).
@@ -510,7 +609,7 @@ __global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void 
   };
   int t = begin + S::kTokens * wave;
   look_up(t);
-  const uint16_t* qrow = a.q + it.b * a.q_stride + (int64_t)(head * a.G + g0 + r) * D;
+  const uint16_t* qrow = a.q + run.b * a.q_stride + (int64_t)(head * a.G + g0 + r) * D;
   u32x4 raw[kSteps];
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
@@ -666,8 +765,9 @@ __global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void 
     }
   }
   __syncthreads();
-  const bool whole = it.count == 1;
-  float* part = static_cast<float*>(a.ws) + (int64_t)blockIdx.x * part_stride(p);
+  float* parts = p.parts + ((int64_t)hg * (p.runs + a.B) + run.b) * part_stride(p);
+  float* part = parts + (int64_t)(blockIdx.x / per) * part_stride(p);
+  const int64_t hrow0 = (int64_t)run.b * a.Hq + head * a.G + g0;
   for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
     const int g = i / (D / 2), d = 2 * (i % (D / 2));
     float mm = sm[0][g];
@@ -681,113 +781,103 @@ __global__ __launch_bounds__(kThreads, (D > (kNVFP4 ? 192 : 128) ? 1 : 2)) void 
       x += f * so[w][g][d];
       y += f * so[w][g][d + 1];
     }
-    const int64_t hrow = (int64_t)it.b * a.Hq + head * a.G + g0 + g;
     if (whole) {
       const float n = ll > 0.0f ? vt0 / ll : 0.0f;
-      *reinterpret_cast<uint32_t*>(a.out + hrow * D + d) = pack_bf16x2(x * n, y * n);
-      if (d == 0 && a.lse) a.lse[hrow] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+      *reinterpret_cast<uint32_t*>(a.out + (hrow0 + g) * D + d) = pack_bf16x2(x * n, y * n);
+      if (d == 0 && a.lse) a.lse[hrow0 + g] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
     } else {
-      *reinterpret_cast<float2*>(part + 2 * p.rows + g * D + d) = make_float2(x, y);
-      if (d == 0) {
-        part[g] = mm;
-        part[p.rows + g] = ll;
-      }
+      store_shared(part + 2 * p.rows + g * D + d, f32x2{x, y});
+      if (d == 0) store_shared(part + 2 * g, f32x2{mm, ll});
     }
+  }
+  if (!whole) {
+    const int first = scalar((uint32_t)run.at / (uint32_t)run.share);
+    const int count = scalar((uint32_t)(run.at + run.steps - 1) / (uint32_t)run.share) - first + 1;
+    uint32_t* arrived = p.arrived + (int64_t)run.b * per + hg;
+    wait_stores();                             // each thread's own, before the barrier
+    __syncthreads();
+    if (threadIdx.x == 0)
+      before_me = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if ((int)before_me == count - 1) {
+      join_partials<D>(p, parts + first * part_stride(p), count, rows, hrow0, vt0);
+      if (threadIdx.x == 0)
+        __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  run.pos += steps;
   }
 }
 
-// One workgroup per sequence and query head: joins the partials of its chunks.
-__global__ __launch_bounds__(kThreads) void join_kernel(Plan p) {
-  __shared__ float so[kThreads][4];
-  __shared__ float sl[kThreads];
-  const DecodeArgs& a = p.a;
-  const int lane = threadIdx.x & 63;
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const Item it = find_item(p, -1, b);
-  const int n = it.count;
-  if (n == 1) return;
-  const int per = a.c.heads * p.groups;
-  const int hk = h / a.G, g = h % a.G, hg = hk * p.groups + g / kHeads, row = g % kHeads;
-  const float* part = static_cast<const float*>(a.ws) + (int64_t)(it.first + hg) * part_stride(p);
-  const int64_t step = per * part_stride(p);        // from chunk to chunk
-  const int D = a.c.dim, quads = D / 4;              // threads of one partial: 8 to 64
-  const int slots = kThreads / quads, t = threadIdx.x % quads, slot = threadIdx.x / quads;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 64) m = fmaxf(m, part[i * step + row]);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-  float l = 0.0f;
-  f32x4 o = {0, 0, 0, 0};
-  if (slot < slots && m > -INFINITY) {
-    for (int i = slot; i < n; i += slots) {
-      const float mi = part[i * step + row];
-      const float f = __builtin_amdgcn_exp2f(mi - m);   // 0 for a chunk that saw nothing
-      l += f * part[i * step + p.rows + row];
-      const float2* src = reinterpret_cast<const float2*>(part + i * step + 2 * p.rows + row * D + 4 * t);
-      const float2 x = src[0], y = src[1];
-      o += f * f32x4{x.x, x.y, y.x, y.y};
-    }
-  }
-  sl[threadIdx.x] = l;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) so[threadIdx.x][k] = o[k];
-  __syncthreads();
-  if (slot != 0) return;
-  for (int s = 1; s < slots; ++s) {
-    l += sl[s * quads + t];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] += so[s * quads + t][k];
-  }
-  const float v = l > 0.0f ? (a.c.nvfp4 ? a.c.vt[0] : 1.0f) / l : 0.0f;
-  const int64_t hrow = (int64_t)b * a.Hq + h;
-  *reinterpret_cast<u32x2*>(a.out + hrow * D + 4 * t) =
-      u32x2{pack_bf16x2(o[0] * v, o[1] * v), pack_bf16x2(o[2] * v, o[3] * v)};
-  if (t == 0 && a.lse) a.lse[hrow] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+// `steps`: of one head at most, by the table's capacity.
+template <bool kNVFP4, int D>
+void launch(Plan& p, int64_t steps, hipStream_t s) {
+  const int per = p.a.c.heads * p.groups;
+  p.runs = (int)max(min((int64_t)(kPerCU<kNVFP4, D> * kCUs / per), steps), (int64_t)1);
+  paged_decode_kernel<kNVFP4, D><<<(uint32_t)(p.runs * per), kThreads, 0, s>>>(p);
 }
-
 template <bool kNVFP4>
-void launch_dim(const Plan& p, uint32_t grid, hipStream_t s) {
+void launch_dim(Plan& p, int64_t steps, hipStream_t s) {
   switch (p.a.c.dim) {
-    case 32: paged_decode_kernel<kNVFP4, 32><<<grid, kThreads, 0, s>>>(p); break;
-    case 64: paged_decode_kernel<kNVFP4, 64><<<grid, kThreads, 0, s>>>(p); break;
-    case 96: paged_decode_kernel<kNVFP4, 96><<<grid, kThreads, 0, s>>>(p); break;
-    case 128: paged_decode_kernel<kNVFP4, 128><<<grid, kThreads, 0, s>>>(p); break;
-    case 160: paged_decode_kernel<kNVFP4, 160><<<grid, kThreads, 0, s>>>(p); break;
-    case 192: paged_decode_kernel<kNVFP4, 192><<<grid, kThreads, 0, s>>>(p); break;
-    case 224: paged_decode_kernel<kNVFP4, 224><<<grid, kThreads, 0, s>>>(p); break;
-    default: paged_decode_kernel<kNVFP4, 256><<<grid, kThreads, 0, s>>>(p); break;
+    case 32: return launch<kNVFP4, 32>(p, steps, s);
+    case 64: return launch<kNVFP4, 64>(p, steps, s);
+    case 96: return launch<kNVFP4, 96>(p, steps, s);
+    case 128: return launch<kNVFP4, 128>(p, steps, s);
+    case 160: return launch<kNVFP4, 160>(p, steps, s);
+    case 192: return launch<kNVFP4, 192>(p, steps, s);
+    case 224: return launch<kNVFP4, 224>(p, steps, s);
+    default: return launch<kNVFP4, 256>(p, steps, s);
   }
 }
+
+// Segments of one sequence, and the sequences of one launch.
+int64_t segments_of(int64_t Hq, int64_t heads) {
+  return heads * ((Hq / heads + kHeads - 1) / kHeads);
+}
+int64_t launch_seqs(int64_t B, int64_t per) { return min(B, kMaxSegments / per); }
 
 }  // namespace
 
-int64_t decode_items(int64_t B, int64_t Hq, int64_t heads) {
-  const int64_t G = Hq / heads;
-  return kTargetItems + B * heads * ((G + kHeads - 1) / kHeads);
-}
+bool decode_heads_ok(int64_t Hq, int64_t heads) { return segments_of(Hq, heads) <= kMaxSegments; }
+
+size_t decode_counter_bytes() { return sizeof(uint32_t) * kMaxSegments; }
 
 size_t decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim) {
-  const int64_t G = Hq / heads;
-  return sizeof(float) * (size_t)(decode_items(B, Hq, heads) * (G < kHeads ? G : kHeads) * (dim + 2));
+  const int64_t G = Hq / heads, per = segments_of(Hq, heads);
+  const int64_t runs = max(kMaxPerCU * kCUs / per, (int64_t)1);
+  const int64_t parts = (runs + launch_seqs(B, per)) * per;
+  return decode_counter_bytes() +
+         sizeof(float) * (size_t)(parts * (G < kHeads ? G : kHeads) * (dim + 2));
 }
 
-hipError_t launch_paged_decode(const DecodeArgs& a, hipStream_t s) {
+hipError_t launch_paged_decode(const DecodeArgs& args, hipStream_t s) {
   Plan p;
-  p.a = a;
+  p.a = args;
+  const DecodeArgs& a = p.a;
   p.groups = (a.G + kHeads - 1) / kHeads;
   p.rows = a.G < kHeads ? a.G : kHeads;
   const uint64_t d = a.c.page_size / 8;
   p.page_magic = (((uint64_t)1 << 36) + d - 1) / d;
-  // chunks: at most kTargetItems and one more for every sequence and head group, and
-  // no more than the table's tokens give
-  const int64_t cap = (int64_t)a.pages_per_seq * a.c.page_size;
-  const int64_t heads = (int64_t)a.B * a.c.heads * p.groups;
-  const int64_t least = (int64_t)kMinSteps * kChunkStep, most = (cap + least - 1) / least;
-  const int64_t items = min(kTargetItems + heads, heads * max(most, (int64_t)1));
-  if (a.c.nvfp4) launch_dim<true>(p, (uint32_t)items, s);
-  else launch_dim<false>(p, (uint32_t)items, s);
-  if (most > 1) join_kernel<<<(uint32_t)((int64_t)a.B * a.Hq), kThreads, 0, s>>>(p);
-  return hipGetLastError();
+  p.arrived = static_cast<uint32_t*>(a.ws);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + decode_counter_bytes());
+  const int64_t per = (int64_t)a.c.heads * p.groups, B = args.B, seqs = launch_seqs(B, per);
+  for (int64_t b = 0; b < B; b += seqs) {
+    p.a.B = (int)min(seqs, B - b);
+    p.a.q = args.q + b * args.q_stride;
+    p.a.table = args.table + b * args.table_stride;
+    p.a.lens = args.lens + b;
+    p.a.out = args.out + b * args.Hq * args.c.dim;
+    p.a.lse = args.lse ? args.lse + b * args.Hq : nullptr;
+    // the table's capacity bounds the steps (a visible range starts at a multiple of 8
+    // tokens, so it never takes a step more)
+    const int64_t cap = (int64_t)a.pages_per_seq * a.c.page_size;
+    const int64_t steps = p.a.B * max((cap + kStepTokens - 1) / kStepTokens, (int64_t)1);
+    if (a.c.nvfp4) launch_dim<true>(p, steps, s);
+    else launch_dim<false>(p, steps, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fos

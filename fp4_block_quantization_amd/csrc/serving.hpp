@@ -56,8 +56,10 @@ struct DecodeArgs {
   float* lse;              // [B][Hq] or null
   void* ws;
 };
-// Workgroups of the decode launch at most.
-int64_t decode_items(int64_t B, int64_t Hq, int64_t heads);
+// Whether the head layout has few enough segments, and the bytes at the start of the
+// workspace that are 0 between launches.
+bool decode_heads_ok(int64_t Hq, int64_t heads);
+size_t decode_counter_bytes();
 size_t decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim);
 hipError_t launch_paged_decode(const DecodeArgs& a, hipStream_t s);
 

@@ -89,6 +89,7 @@ def _load() -> ctypes.CDLL:
         "fos_kv_append": ([cachep, ctypes.c_int, P, I64, P, I64, P, I64, P], ctypes.c_int),
         "fos_kv_gather": ([cachep, P, I64, P, I64, P, I64, P], ctypes.c_int),
         "fos_paged_decode_workspace_bytes": ([I64, I64, I64, I64], SZ),
+        "fos_paged_decode_counter_bytes": ([], SZ),
         "fos_paged_decode": ([cachep, P, I64, I64, I64, P, I64, I64, P, ctypes.c_float, I64, P, P,
                               P, SZ, P], ctypes.c_int),
     }
@@ -717,13 +718,14 @@ _decode_workspaces = {}
 
 
 def _decode_workspace(device: torch.device, stream: int, need: int) -> torch.Tensor:
-    """Scratch of paged_decode for one stream.  It grows by powers of two, and an outgrown
+    """Scratch of paged_decode for one stream, its counters cleared.  It grows by powers of two, and an outgrown
     one is kept: a captured graph may hold its address."""
     key = (device.index, stream)
     held = _decode_workspaces.setdefault(key, [])
     if not held or held[-1].numel() < need:
-        held.append(torch.empty(1 << max(need - 1, 4095).bit_length(), dtype=torch.uint8,
-                                device=device))
+        ws = torch.empty(1 << (need - 1).bit_length(), dtype=torch.uint8, device=device)
+        ws[:int(_lib.fos_paged_decode_counter_bytes())].zero_()
+        held.append(ws)
     return held[-1]
 
 

@@ -479,6 +479,11 @@ fos_status fos_kv_gather(const fos_kv_cache* cache, const int64_t* slots, int64_
 size_t fos_paged_decode_workspace_bytes(int64_t num_seqs, int64_t num_q_heads,
                                         int64_t num_kv_heads, int64_t head_dim);
 
+/* Bytes at the start of that workspace that must be 0 when a workspace is first used
+ * (262144; counters of finished workgroups).  Every call leaves them 0, so one clearing
+ * serves all later calls of any sizes, also replayed from a graph. */
+size_t fos_paged_decode_counter_bytes(void);
+
 /* Attention of one new token per sequence over its pages of the cache.  Sequence b
  * holds seq_lens[b] tokens (the new one included, once appended); token j is row
  * j % page_size of page block_table[b][j / page_size].  Query head h reads kv head
@@ -498,9 +503,12 @@ size_t fos_paged_decode_workspace_bytes(int64_t num_seqs, int64_t num_q_heads,
  *   out_bf16 [num_seqs][num_q_heads][head_dim] contiguous; lse fp32
  *   [num_seqs][num_q_heads] or NULL (natural logarithm).
  *   q_bf16 16-byte aligned with q_stride % 8 == 0 (for num_seqs > 1), out_bf16
- *   16-byte aligned; pages_per_seq * page_size at most 2^30.
+ *   16-byte aligned; pages_per_seq * page_size at most 2^30, and at most
+ *   2^38 / num_seqs; at most 65536 kv heads (times ceil(query heads per kv head / 16)).
  *   workspace: device scratch, 256-byte aligned, at least
- *   fos_paged_decode_workspace_bytes(...) bytes; calls that may overlap need their own.
+ *   fos_paged_decode_workspace_bytes(...) bytes, its first
+ *   fos_paged_decode_counter_bytes() bytes 0 before its first use; calls that may
+ *   overlap need their own.
  * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS (also a negative window or
  * a softmax_scale that is not finite), FOS_E_WORKSPACE, FOS_E_HIP. */
 fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64_t q_stride,
