@@ -2,16 +2,11 @@
 //   y[m][n] = t * sum_k x[m][k] E(w[n][k]) D(s[n][k / block]) + bias[n].
 // The weight is read once; its bytes bound the call (x and y are small beside it).
 //
-// Matrix form, on the 16x16x32 bf16 instruction: A = 16 weight rows, B = 16 activation
-// rows, so a weight is converted to bf16 once for up to 64 activation rows.  E2M1 x E4M3
-// has at most 6 significant bits and E2M1 x 2^e two: both are exact in bf16, products
-// are exact in fp32, and every sum is fp32.  y is rounded once.
-//
-// A wave walks the inner dimension in chunks of 128.  For each weight row (r = lane % 16)
-// its four lanes (q = lane / 16) read 16 contiguous bytes each, and exchange them so that
-// in step j lane q holds the values k = 32 j + 8 q .. + 7: then the activation's loads
-// are 64 contiguous bytes per row as well.  The waves of a workgroup share its output
-// tile and split the inner dimension; they join in LDS in a fixed order.
+// Matrix form: E2M1 x E4M3 has at most 6 significant bits and E2M1 x 2^e two, so weights
+// are exact in bf16, products are exact in fp32, and every sum is fp32; y is rounded once.
+// Two kernels, by the number of activation rows: up to 8 on 4x4x4 products, where a lane
+// keeps a weight row to itself, and more on 16x16x32 tiles, where a weight is converted
+// once for up to 64 activation rows.
 #include "serving.hpp"
 
 namespace fos {
@@ -23,10 +18,8 @@ constexpr int kChunk = 128;   // values of the inner dimension per wave and step
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-// Weight rows are K / 2 bytes apart: 8-byte alignment (K % 16 == 0), scales any.
+// Weight rows are K / 2 bytes apart: 8-byte alignment (K % 16 == 0).
 typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
-typedef uint32_t u32x2_a1 __attribute__((ext_vector_type(2), aligned(1)));
-typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -55,48 +48,49 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return kMX ? __uint_as_float(byte << 23) : e4m3_decode(byte & 0x7fu);
 }
 
-// One chunk of one weight row as its four lanes load it: word j of lane q is 16 q + 4 j
-// bytes into the chunk.
-template <bool kMX>
-struct RawW {
-  u32x4 w;
-  u32x2 s;      // NVFP4: the chunk's 8 block scales; MXFP4: its 4 in s.x
-};
-
-// 4x4 exchange of words between the lanes q = 0..3 of a row: word j of lane q becomes
-// word q of lane j.
-__device__ __forceinline__ u32x4 exchange(u32x4 w) {
-  auto a = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
-  auto b = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
-  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  return u32x4{c[0], c[1], d[0], d[1]};
-}
-
-template <bool kMX, int NT, int MT, int KW>
-__global__ __launch_bounds__(64 * KW) void wlinear_kernel(WLinearArgs a) {
-  // chunks in flight per wave: their x must fit the registers too
-  constexpr int U = MT == 1 ? (KW > 8 ? 2 : 4) : MT == 2 ? 2 : 1;
+// ---- more activation rows: 16x16x32 tiles -------------------------------------------
+// A wave takes 16 NT weight rows (A operand) by 16 MT activation rows (B operand) and walks
+// the inner dimension in chunks of 128; the waves of a workgroup share the tile and split
+// the inner dimension.  Lane (r = lane % 16, q = lane / 16) supplies to step j of a chunk
+// the values 32 q + 8 j .. + 7 of row r: 16 contiguous bytes of a weight row.  Loaded like
+// that, neighbouring lanes would sit in different rows and cost the address unit a line
+// each (18.8 us at 16 x 12288 x 4096), so weights and activations are loaded in memory
+// order and go through the wave's own LDS.  16-byte units are stored at (unit ^ key of the
+// row), so that the 16 rows of an operand are read from different banks.
+template <bool kMX, bool kEven, int NT, int MT, int KW>
+__global__ __launch_bounds__(64 * KW) void wlinear_tile_kernel(WLinearArgs a) {
+  constexpr int U = MT <= 2 ? 2 : 1;           // consecutive chunks in flight
   constexpr int kBlock = kMX ? 32 : 16;
   constexpr int kTileN = 16 * NT, kTileM = 16 * MT;
-  __shared__ f32x4 sums[KW][NT * MT][64];
+  struct Lds {
+    u32x4 w[NT][16][4];                        // [row][unit of 32 values]
+    u32x4 x[MT][16][16];                       // [row][unit of 8 values]
+    uint16_t s[NT][16][4];                     // [row][32 values]: their one or two scales
+  };
+  constexpr int kSums = NT * MT * 64 * sizeof(f32x4);
+  constexpr int kBytes = sizeof(Lds) > kSums ? sizeof(Lds) : kSums;
+  __shared__ __attribute__((aligned(16))) uint8_t mem[KW][kBytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  Lds& l = *reinterpret_cast<Lds*>(mem[wave]);
   // activation tiles of the same weight rows are neighbours
   const uint32_t tiles_m = (uint32_t)((a.M + kTileM - 1) / kTileM);
   const int64_t n0 = (int64_t)(blockIdx.x / tiles_m) * kTileN;
   const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * kTileM;
-  const int chunks = (int)(a.K / kChunk);      // whole ones
+  const int K = (int)a.K, chunks = K / kChunk;   // whole ones
+  const float t = kMX ? 1.0f : a.wt[0];
+  const int rows_m = (int)min((int64_t)kTileM, a.M - m0);
+  // loads in memory order: four lanes to a weight row, 16 to an activation row; rows past
+  // N and M read the last row again
+  const int wr = lane >> 2, wu = lane & 3, xr0 = lane >> 4, xu = lane & 15;
   const uint8_t* wp[NT];
   const uint8_t* sp[NT];
-  const uint16_t* xp[MT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {               // rows past N read the last row again
-    const int64_t row = min(n0 + 16 * n + r, a.N - 1);
-    wp[n] = a.wd + row * (a.K / 2);
-    sp[n] = a.ws + row * (a.K / kBlock);
+  for (int n = 0; n < NT; ++n) {
+    const int64_t row = min(n0 + 16 * n + wr, a.N - 1);
+    wp[n] = a.wd + row * (K / 2) + 16 * wu;
+    sp[n] = a.ws + row * (K / kBlock) + 32 / kBlock * wu;
   }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) xp[m] = a.x + min(m0 + 16 * m + r, a.M - 1) * a.x_stride + 8 * q;
+  const uint16_t* xp = a.x + m0 * a.x_stride + 8 * xu;
 
   f32x4 acc[NT][MT];
 #pragma unroll
@@ -104,92 +98,109 @@ __global__ __launch_bounds__(64 * KW) void wlinear_kernel(WLinearArgs a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{0, 0, 0, 0};
 
-  RawW<kMX> raw[U][NT];
-  auto load_w = [&](int c) {
+  auto multiply = [&](const u32x4 (&w)[NT], const uint32_t (&sb)[NT], const u32x4 (&x)[4 * MT]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int cu = min(c + KW * u, chunks - 1);      // past the end: not used
+    for (int n = 0; n < NT; ++n) {
+      l.w[n][wr][wu ^ (wr >> 2)] = w[n];
+      l.s[n][wr][wu] = (uint16_t)sb[n];
+    }
+#pragma unroll
+    for (int m = 0; m < 4 * MT; ++m) {
+      const int row = 4 * (m & 3) + xr0;
+      l.x[m >> 2][row][xu ^ row] = x[m];
+    }
+    u32x4 wf[NT];
+    uint32_t sf[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      wf[n] = l.w[n][r][q ^ (r >> 2)];
+      sf[n] = l.s[n][r][q];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4 xf[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xf[m] = l.x[m][r][(4 * q + j) ^ r];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        raw[u][n].w = *reinterpret_cast<const u32x4_a8*>(wp[n] + (int64_t)cu * (kChunk / 2) + 16 * q);
-        const uint8_t* s = sp[n] + (int64_t)cu * (kChunk / kBlock);
-        if constexpr (kMX) raw[u][n].s.x = *reinterpret_cast<const u32_a1*>(s);
-        else raw[u][n].s = *reinterpret_cast<const u32x2_a1*>(s);
+        const float d = scale_value<kMX>((kMX || j < 2 ? sf[n] : sf[n] >> 8) & 0xff);
+        const u32x4 e = dequant8<kMX>(wf[n][j], d);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = mfma(e, xf[m], acc[n][m]);
       }
     }
   };
-  if (wave < chunks) load_w(wave);
-  for (int c = wave; c < chunks; c += KW * U) {
-    u32x4 xf[U][MT][4];
+
+  for (int c = wave * U; c < chunks; c += KW * U) {
+    u32x4 w[U][NT], x[U][4 * MT];
+    uint32_t sb[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int cu = min(c + KW * u, chunks - 1);
+      if (c + u >= chunks) break;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NT; ++n) {
+        w[u][n] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4_a8*>(wp[n] + (c + u) * (kChunk / 2)));
+        const uint8_t* s = sp[n] + (c + u) * (kChunk / kBlock);
+        if constexpr (kMX) sb[u][n] = s[0];
+        else if constexpr (kEven) sb[u][n] = *reinterpret_cast<const uint16_t*>(s);
+        else sb[u][n] = s[0] | (uint32_t)s[1] << 8;
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          xf[u][m][j] = *reinterpret_cast<const u32x4*>(xp[m] + (int64_t)cu * kChunk + 32 * j);
+      for (int m = 0; m < 4 * MT; ++m) {
+        const int row = min(4 * m + xr0, rows_m - 1);
+        x[u][m] = *reinterpret_cast<const u32x4*>(xp + row * a.x_stride + (c + u) * kChunk);
+      }
     }
-    RawW<kMX> cur[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) cur[u][n] = raw[u][n];
-    if (c + KW * U < chunks) load_w(c + KW * U);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c + KW * u >= chunks) break;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const u32x4 w = exchange(cur[u][n].w);
-        // block scales of this lane's steps: NVFP4 byte 2 j + q / 2, MXFP4 byte j
-        const uint32_t s0 = kMX ? cur[u][n].s.x : cur[u][n].s.x >> (8 * (q >> 1));
-        const uint32_t s1 = kMX ? cur[u][n].s.x >> 16 : cur[u][n].s.y >> (8 * (q >> 1));
-        const uint32_t sb[4] = {s0 & 0xff, (kMX ? s0 >> 8 : s0 >> 16) & 0xff, s1 & 0xff,
-                                (kMX ? s1 >> 8 : s1 >> 16) & 0xff};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 wf = dequant8<kMX>(w[j], scale_value<kMX>(sb[j]));
-#pragma unroll
-          for (int m = 0; m < MT; ++m) acc[n][m] = mfma(wf, xf[u][m][j], acc[n][m]);
-        }
-      }
-    }
+      if (c + u < chunks) multiply(w[u], sb[u], x[u]);
   }
-  // the last K % 128 values, in the layout of the steps; what lies past K is zero
-  if (chunks % KW == wave && a.K % kChunk) {
+  if (K % kChunk && chunks / U % KW == wave) {
+    // the last chunk; past K everything is zero (K % 16 == 0: a lane may hold half)
+    const int left = K - chunks * kChunk;
+    u32x4 w[NT], x[4 * MT];
+    uint32_t sb[NT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t k = (int64_t)chunks * kChunk + 32 * j + 8 * q;
-      const bool in = k < a.K;
-      u32x4 xf[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        xf[m] = in ? *reinterpret_cast<const u32x4*>(xp[m] + (k - 8 * q)) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t w = in ? *reinterpret_cast<const uint32_t*>(wp[n] + k / 2) : 0u;
-        const uint32_t s = in ? sp[n][k / kBlock] : 0u;
-        const u32x4 wf = dequant8<kMX>(w, scale_value<kMX>(s));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[n][m] = mfma(wf, xf[m], acc[n][m]);
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t* s4 = reinterpret_cast<const uint32_t*>(wp[n] + chunks * (kChunk / 2));
+      const uint8_t* s = sp[n] + chunks * (kChunk / kBlock);
+      w[n] = u32x4{0, 0, 0, 0};
+      sb[n] = 0;
+      if (32 * wu + 16 <= left) {
+        w[n].x = s4[0];
+        w[n].y = s4[1];
+        sb[n] = s[0];
+      }
+      if (32 * wu + 32 <= left) {
+        w[n].z = s4[2];
+        w[n].w = s4[3];
+        if (!kMX) sb[n] |= (uint32_t)s[1] << 8;
       }
     }
+#pragma unroll
+    for (int m = 0; m < 4 * MT; ++m) {
+      const int row = min(4 * m + xr0, rows_m - 1);
+      x[m] = u32x4{0, 0, 0, 0};
+      if (8 * xu < left)
+        x[m] = *reinterpret_cast<const u32x4*>(xp + row * a.x_stride + chunks * kChunk);
+    }
+    multiply(w, sb, x);
   }
 
   // join: rows n0 + 16 n + 4 q + i, column m0 + 16 m + r
+  f32x4(*sums)[64] = reinterpret_cast<f32x4(*)[64]>(mem[wave]);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) sums[wave][n * MT + m][lane] = acc[n][m];
+    for (int m = 0; m < MT; ++m) sums[n * MT + m][lane] = acc[n][m];
   __syncthreads();
-  const float t = kMX ? 1.0f : a.wt[0];
   for (int i = threadIdx.x; i < NT * MT * 64; i += 64 * KW) {
-    const int tile = i >> 6, l = i & 63;
-    f32x4 v = sums[0][tile][l];
+    const int tile = i >> 6, ln = i & 63;
+    f32x4 v = reinterpret_cast<f32x4(*)[64]>(mem[0])[tile][ln];
 #pragma unroll
-    for (int w = 1; w < KW; ++w) v += sums[w][tile][l];
-    const int64_t n = n0 + 16 * (tile / MT) + 4 * (l >> 4), m = m0 + 16 * (tile % MT) + (l & 15);
+    for (int w = 1; w < KW; ++w) v += reinterpret_cast<f32x4(*)[64]>(mem[w])[tile][ln];
+    const int64_t n = n0 + 16 * (tile / MT) + 4 * (ln >> 4), m = m0 + 16 * (tile % MT) + (ln & 15);
     if (m >= a.M) continue;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -203,17 +214,194 @@ __global__ __launch_bounds__(64 * KW) void wlinear_kernel(WLinearArgs a) {
   }
 }
 
+// ---- few activation rows: M <= 8 ---------------------------------------------------
+// On the 4x4x4 instruction, 16 independent 4x4 products: a quad of lanes takes four weight
+// rows (its columns) over the same 32 values of the inner dimension and four activation
+// rows.  Each lane keeps the sums of its own weight row, so a block's scale multiplies the
+// block's four sums instead of its 16 weights, and E2M1 enters as it is: about one VALU
+// instruction per weight for up to four activation rows (a 16x16 tile takes two for any
+// number, and its operands cross lanes).
+//
+// A wave takes 16 weight rows (four to a lane) and walks the inner dimension 512 values
+// at a time; the waves of a workgroup share its rows and split the inner dimension.  The
+// activation comes in memory order and goes through the wave's own LDS.
+constexpr int kQuadStep = 512;
+
+// Sum over the lanes with the same lane % 4, in all of them.
+__device__ __forceinline__ float sum_over_quads(float v) {
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xf, 0xf, true));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, true));
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// MS: sets of four activation rows.  kEven: scale rows start at even bytes (K % 32 == 0),
+// so that a lane's two NVFP4 scales are one aligned load.
+template <bool kMX, bool kEven, int MS, int KW>
+__global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(WLinearArgs a) {
+  constexpr int kBlock = kMX ? 32 : 16;
+  constexpr int R = 4;                  // weight rows of a lane
+  constexpr int U = MS == 1 ? 2 : 1;    // steps in flight
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  __shared__ u32x4 xs[KW][4 * MS][64];
+  __shared__ float sums[KW][16][4 * MS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 3, g = lane >> 2;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int M = (int)a.M, K = (int)a.K, whole = K / kQuadStep;
+  const float t = kMX ? 1.0f : a.wt[0];
+  const uint8_t* wp[R];
+  const uint8_t* sp[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {         // rows past N read the last row again
+    const int64_t row = min(n0 + 4 * j + i, a.N - 1);
+    wp[j] = a.wd + row * (K / 2) + 16 * g;
+    sp[j] = a.ws + row * (K / kBlock) + 32 / kBlock * g;
+  }
+  f32x4 acc[MS][R];
+#pragma unroll
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int j = 0; j < R; ++j) acc[m][j] = f32x4{0, 0, 0, 0};
+
+  // The products of one step: w, sb the lane's weights and scales, x row m's unit `lane`.
+  // Unit u of row m lies at u ^ (m % 4) in LDS: the four rows of a quad read from different
+  // banks.  Rows past M are whatever LDS holds: they only reach sums that are not used.
+  auto multiply = [&](const u32x4 (&w)[R], const uint32_t (&sb)[R], const u32x4 (&xr)[4 * MS]) {
+#pragma unroll
+    for (int m = 0; m < 4 * MS; ++m)
+      if (m < M) xs[wave][m][lane ^ (m & 3)] = xr[m];
+    u32x4 x[MS][4];
+#pragma unroll
+    for (int m = 0; m < MS; ++m)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[m][u] = xs[wave][4 * m + i][(4 * g + u) ^ i];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+#pragma unroll
+      for (int b = 0; b < 32 / kBlock; ++b) {
+        f32x4 part[MS];
+#pragma unroll
+        for (int m = 0; m < MS; ++m) part[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int u = b * kBlock / 8; u < (b + 1) * kBlock / 8; ++u) {   // 8 values each
+          const u32x4 e = dequant8<true>(w[j][u], 1.0f);
+#pragma unroll
+          for (int m = 0; m < MS; ++m) {
+            part[m] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+                __builtin_bit_cast(s16x4, u32x2{x[m][u].x, x[m][u].y}),
+                __builtin_bit_cast(s16x4, u32x2{e.x, e.y}), part[m], 0, 0, 0);
+            part[m] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+                __builtin_bit_cast(s16x4, u32x2{x[m][u].z, x[m][u].w}),
+                __builtin_bit_cast(s16x4, u32x2{e.z, e.w}), part[m], 0, 0, 0);
+          }
+        }
+        const float d = scale_value<kMX>((sb[j] >> (8 * b)) & 0xff);
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[m][j][c] = __builtin_fmaf(part[m][c], d, acc[m][j][c]);
+      }
+    }
+  };
+
+  for (int s = wave; s < whole; s += KW * U) {
+    u32x4 w[U][R], xr[U][4 * MS];
+    uint32_t sb[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int su = s + KW * u;
+      if (su >= whole) break;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        w[u][j] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4_a8*>(wp[j] + su * (kQuadStep / 2)));
+        const uint8_t* q = sp[j] + su * (kQuadStep / kBlock);
+        if constexpr (kMX) sb[u][j] = q[0];
+        else if constexpr (kEven) sb[u][j] = *reinterpret_cast<const uint16_t*>(q);
+        else sb[u][j] = q[0] | (uint32_t)q[1] << 8;
+      }
+#pragma unroll
+      for (int m = 0; m < 4 * MS; ++m)
+        if (m < M) xr[u][m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + su * kQuadStep)[lane];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + KW * u < whole) multiply(w[u], sb[u], xr[u]);
+  }
+  if (K % kQuadStep && whole % KW == wave) {
+    // the last step; past K everything is zero (K % 16 == 0: a lane may hold half)
+    const int left = K - whole * kQuadStep;
+    u32x4 w[R], xr[4 * MS];
+    uint32_t sb[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(wp[j] + whole * (kQuadStep / 2));
+      const uint8_t* qs = sp[j] + whole * (kQuadStep / kBlock);
+      w[j] = u32x4{0, 0, 0, 0};
+      sb[j] = 0;
+      if (32 * g + 16 <= left) {
+        w[j].x = q[0];
+        w[j].y = q[1];
+        sb[j] = qs[0];
+      }
+      if (32 * g + 32 <= left) {
+        w[j].z = q[2];
+        w[j].w = q[3];
+        if (!kMX) sb[j] |= (uint32_t)qs[1] << 8;
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 4 * MS; ++m) {
+      xr[m] = u32x4{0, 0, 0, 0};
+      if (m < M && 8 * lane < left)
+        xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + whole * kQuadStep)[lane];
+    }
+    multiply(w, sb, xr);
+  }
+
+#pragma unroll
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float v = sum_over_quads(acc[m][j][c]);
+        if (g == 0) sums[wave][4 * j + i][4 * m + c] = v;
+      }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 16 * M; e += 64 * KW) {
+    const int n = e & 15, m = e >> 4;
+    if (n0 + n >= a.N) continue;
+    float v = sums[0][n][m];
+#pragma unroll
+    for (int w = 1; w < KW; ++w) v += sums[w][n][m];
+    v *= t;
+    if (a.bias) v += bf16_lo(a.bias[n0 + n]);
+    const int64_t at = m * a.N + n0 + n;
+    if (a.f32_out) static_cast<float*>(a.y)[at] = v;
+    else static_cast<uint16_t*>(a.y)[at] = (uint16_t)pack_bf16x2(v, v);
+  }
+}
+
 // Tile and split for a shape: 16 NT weight rows, 16 MT activation rows, KW waves.
+// MT 0 and -1: the quad kernel with one or two sets of four activation rows.
 struct Shape {
   int nt, mt, kw;
 };
 Shape shape_of(const WLinearArgs& a) {
-  const bool few = a.N < 16 * 512;             // weight rows for fewer than 512 workgroups of 16
-  if (a.M <= 16) return few ? Shape{1, 1, 16} : Shape{1, 1, 4};
+  if (a.M <= 8) {
+    const bool wide = a.N >= 16 * 512;
+    return Shape{1, a.M <= 4 ? 0 : -1, wide ? 4 : 8};
+  }
+  const bool few = a.N < 16 * 512;
+  if (a.M <= 16) return few ? Shape{1, 1, 8} : Shape{2, 1, 4};
   if (a.M <= 32) return few ? Shape{1, 2, 8} : Shape{2, 2, 4};
-  return few ? Shape{1, 4, 8} : Shape{2, 4, 4};
+  return few ? Shape{2, 4, 8} : Shape{4, 4, 4};
 }
 int64_t tiles_of(const WLinearArgs& a, const Shape& h) {
+  if (h.mt <= 0) return (a.N + 15) / 16;
   return ((a.N + 16 * h.nt - 1) / (16 * h.nt)) * ((a.M + 16 * h.mt - 1) / (16 * h.mt));
 }
 
@@ -221,8 +409,19 @@ template <int NT, int MT, int KW>
 bool launch_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
   if (h.nt != NT || h.mt != MT || h.kw != KW) return false;
   const uint32_t grid = (uint32_t)tiles_of(a, h);
-  if (a.mx) wlinear_kernel<true, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
-  else wlinear_kernel<false, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
+  if (a.mx) wlinear_tile_kernel<true, true, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
+  else if (a.K % 32 == 0) wlinear_tile_kernel<false, true, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
+  else wlinear_tile_kernel<false, false, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
+  return true;
+}
+
+template <int MS, int KW>
+bool launch_quad_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
+  if (h.mt != 1 - MS || h.kw != KW) return false;
+  const uint32_t grid = (uint32_t)tiles_of(a, h);
+  if (a.mx) wlinear_quad_kernel<true, true, MS, KW><<<grid, 64 * KW, 0, s>>>(a);
+  else if (a.K % 32 == 0) wlinear_quad_kernel<false, true, MS, KW><<<grid, 64 * KW, 0, s>>>(a);
+  else wlinear_quad_kernel<false, false, MS, KW><<<grid, 64 * KW, 0, s>>>(a);
   return true;
 }
 
@@ -235,9 +434,11 @@ int64_t wlinear_threads(const WLinearArgs& a) {
 
 hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s) {
   const Shape h = shape_of(a);
-  (void)(launch_if<1, 1, 16>(a, h, s) || launch_if<1, 1, 4>(a, h, s) ||
+  (void)(launch_quad_if<1, 4>(a, h, s) || launch_quad_if<1, 8>(a, h, s) ||
+         launch_quad_if<2, 4>(a, h, s) || launch_quad_if<2, 8>(a, h, s) ||
+         launch_if<1, 1, 8>(a, h, s) || launch_if<2, 1, 4>(a, h, s) ||
          launch_if<1, 2, 8>(a, h, s) || launch_if<2, 2, 4>(a, h, s) ||
-         launch_if<1, 4, 8>(a, h, s) || launch_if<2, 4, 4>(a, h, s));
+         launch_if<2, 4, 8>(a, h, s) || launch_if<4, 4, 4>(a, h, s));
   return hipGetLastError();
 }
 
