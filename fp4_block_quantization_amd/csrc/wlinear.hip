@@ -43,9 +43,15 @@ __device__ __forceinline__ u32x4 dequant8(uint32_t w, float d) {
                  pack_bf16x2(c.x * d, c.y * d), pack_bf16x2(e.x * d, e.y * d)};
   }
 }
+// The scales of 32 values: two E4M3 bytes, or one E8M0 byte (2^-127 is subnormal in fp32).
 template <bool kMX>
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  return kMX ? __uint_as_float(byte << 23) : e4m3_decode(byte & 0x7fu);
+__device__ __forceinline__ f32x2 scale_values(uint32_t w) {
+  if constexpr (kMX) {
+    const float d = __uint_as_float(max(w << 23, 0x400000u));
+    return f32x2{d, d};
+  } else {
+    return __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+  }
 }
 
 // ---- more activation rows: 16x16x32 tiles -------------------------------------------
@@ -58,8 +64,7 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 // order and go through the wave's own LDS.  16-byte units are stored at (unit ^ key of the
 // row), so that the 16 rows of an operand are read from different banks.
 template <bool kMX, bool kEven, int NT, int MT, int KW>
-__global__ __launch_bounds__(64 * KW) void wlinear_tile_kernel(WLinearArgs a) {
-  constexpr int U = MT <= 2 ? 2 : 1;           // consecutive chunks in flight
+__global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a) {
   constexpr int kBlock = kMX ? 32 : 16;
   constexpr int kTileN = 16 * NT, kTileM = 16 * MT;
   struct Lds {
@@ -76,7 +81,7 @@ __global__ __launch_bounds__(64 * KW) void wlinear_tile_kernel(WLinearArgs a) {
   const uint32_t tiles_m = (uint32_t)((a.M + kTileM - 1) / kTileM);
   const int64_t n0 = (int64_t)(blockIdx.x / tiles_m) * kTileN;
   const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * kTileM;
-  const int K = (int)a.K, chunks = K / kChunk;   // whole ones
+  const int K = (int)a.K, chunks = (K + kChunk - 1) / kChunk;
   const float t = kMX ? 1.0f : a.wt[0];
   const int rows_m = (int)min((int64_t)kTileM, a.M - m0);
   // loads in memory order: four lanes to a weight row, 16 to an activation row; rows past
@@ -98,7 +103,46 @@ __global__ __launch_bounds__(64 * KW) void wlinear_tile_kernel(WLinearArgs a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{0, 0, 0, 0};
 
-  auto multiply = [&](const u32x4 (&w)[NT], const uint32_t (&sb)[NT], const u32x4 (&x)[4 * MT]) {
+  // one chunk on its way; the registers are refilled as soon as it is staged
+  u32x4 w[NT], x[4 * MT];
+  uint32_t sb[NT];
+  auto load = [&](int c) {
+    const int left = K - c * kChunk;
+    if (left >= kChunk) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        w[n] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4_a8*>(wp[n] + c * (kChunk / 2)));
+        const uint8_t* s = sp[n] + c * (kChunk / kBlock);
+        if constexpr (kMX) sb[n] = s[0];
+        else if constexpr (kEven) sb[n] = *reinterpret_cast<const uint16_t*>(s);
+        else sb[n] = s[0] | (uint32_t)s[1] << 8;
+      }
+#pragma unroll
+      for (int m = 0; m < 4 * MT; ++m) {
+        const int row = min(4 * m + xr0, rows_m - 1);
+        x[m] = *reinterpret_cast<const u32x4*>(xp + row * a.x_stride + c * kChunk);
+      }
+    } else {
+      // past K everything is zero (K % 16 == 0: a lane may hold half of its 32 weights)
+      const bool half = 32 * wu + 16 <= left, full = 32 * wu + 32 <= left;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(wp[n] + c * (kChunk / 2));
+        const uint8_t* s = sp[n] + c * (kChunk / kBlock);
+        w[n] = u32x4{half ? p[0] : 0u, half ? p[1] : 0u, full ? p[2] : 0u, full ? p[3] : 0u};
+        sb[n] = (half ? s[0] : 0u) | (!kMX && full ? (uint32_t)s[1] << 8 : 0u);
+      }
+#pragma unroll
+      for (int m = 0; m < 4 * MT; ++m) {
+        const int row = min(4 * m + xr0, rows_m - 1);
+        x[m] = u32x4{0, 0, 0, 0};
+        if (8 * xu < left)
+          x[m] = *reinterpret_cast<const u32x4*>(xp + row * a.x_stride + c * kChunk);
+      }
+    }
+  };
+  auto stage = [&]() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       l.w[n][wr][wu ^ (wr >> 2)] = w[n];
@@ -109,83 +153,38 @@ __global__ __launch_bounds__(64 * KW) void wlinear_tile_kernel(WLinearArgs a) {
       const int row = 4 * (m & 3) + xr0;
       l.x[m >> 2][row][xu ^ row] = x[m];
     }
+  };
+  auto multiply = [&]() {
     u32x4 wf[NT];
-    uint32_t sf[NT];
+    f32x2 sf[NT];                              // of the lane's first and last 16 values
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       wf[n] = l.w[n][r][q ^ (r >> 2)];
-      sf[n] = l.s[n][r][q];
+      sf[n] = scale_values<kMX>(l.s[n][r][q]);
     }
+    u32x4 xf[4][MT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4 xf[MT];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xf[m] = l.x[m][r][(4 * q + j) ^ r];
+      for (int m = 0; m < MT; ++m) xf[j][m] = l.x[m][r][(4 * q + j) ^ r];
+    // every read is on its way before the first product (left alone, the scheduler reads
+    // each operand right before its product and waits for it)
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float d = scale_value<kMX>((kMX || j < 2 ? sf[n] : sf[n] >> 8) & 0xff);
-        const u32x4 e = dequant8<kMX>(wf[n][j], d);
+        const u32x4 e = dequant8<kMX>(wf[n][j], j < 2 ? sf[n].x : sf[n].y);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[n][m] = mfma(e, xf[m], acc[n][m]);
+        for (int m = 0; m < MT; ++m) acc[n][m] = mfma(e, xf[j][m], acc[n][m]);
       }
-    }
   };
 
-  for (int c = wave * U; c < chunks; c += KW * U) {
-    u32x4 w[U][NT], x[U][4 * MT];
-    uint32_t sb[U][NT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c + u >= chunks) break;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        w[u][n] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4_a8*>(wp[n] + (c + u) * (kChunk / 2)));
-        const uint8_t* s = sp[n] + (c + u) * (kChunk / kBlock);
-        if constexpr (kMX) sb[u][n] = s[0];
-        else if constexpr (kEven) sb[u][n] = *reinterpret_cast<const uint16_t*>(s);
-        else sb[u][n] = s[0] | (uint32_t)s[1] << 8;
-      }
-#pragma unroll
-      for (int m = 0; m < 4 * MT; ++m) {
-        const int row = min(4 * m + xr0, rows_m - 1);
-        x[u][m] = *reinterpret_cast<const u32x4*>(xp + row * a.x_stride + (c + u) * kChunk);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c + u < chunks) multiply(w[u], sb[u], x[u]);
-  }
-  if (K % kChunk && chunks / U % KW == wave) {
-    // the last chunk; past K everything is zero (K % 16 == 0: a lane may hold half)
-    const int left = K - chunks * kChunk;
-    u32x4 w[NT], x[4 * MT];
-    uint32_t sb[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint32_t* s4 = reinterpret_cast<const uint32_t*>(wp[n] + chunks * (kChunk / 2));
-      const uint8_t* s = sp[n] + chunks * (kChunk / kBlock);
-      w[n] = u32x4{0, 0, 0, 0};
-      sb[n] = 0;
-      if (32 * wu + 16 <= left) {
-        w[n].x = s4[0];
-        w[n].y = s4[1];
-        sb[n] = s[0];
-      }
-      if (32 * wu + 32 <= left) {
-        w[n].z = s4[2];
-        w[n].w = s4[3];
-        if (!kMX) sb[n] |= (uint32_t)s[1] << 8;
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < 4 * MT; ++m) {
-      const int row = min(4 * m + xr0, rows_m - 1);
-      x[m] = u32x4{0, 0, 0, 0};
-      if (8 * xu < left)
-        x[m] = *reinterpret_cast<const u32x4*>(xp + row * a.x_stride + chunks * kChunk);
-    }
-    multiply(w, sb, x);
+  if (wave < chunks) load(wave);
+  for (int c = wave; c < chunks; c += KW) {
+    stage();
+    if (c + KW < chunks) load(c + KW);
+    multiply();
   }
 
   // join: rows n0 + 16 n + 4 q + i, column m0 + 16 m + r
@@ -249,7 +248,7 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
   __shared__ float sums[KW][16][4 * MS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 3, g = lane >> 2;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int M = (int)a.M, K = (int)a.K, whole = K / kQuadStep;
+  const int M = (int)a.M, K = (int)a.K, steps = (K + kQuadStep - 1) / kQuadStep;
   const float t = kMX ? 1.0f : a.wt[0];
   const uint8_t* wp[R];
   const uint8_t* sp[R];
@@ -279,6 +278,7 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
       for (int u = 0; u < 4; ++u) x[m][u] = xs[wave][4 * m + i][(4 * g + u) ^ i];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
+      const f32x2 sf = scale_values<kMX>(sb[j]);
 #pragma unroll
       for (int b = 0; b < 32 / kBlock; ++b) {
         f32x4 part[MS];
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
                 __builtin_bit_cast(s16x4, u32x2{e.z, e.w}), part[m], 0, 0, 0);
           }
         }
-        const float d = scale_value<kMX>((sb[j] >> (8 * b)) & 0xff);
+        const float d = b ? sf.y : sf.x;
 #pragma unroll
         for (int m = 0; m < MS; ++m)
 #pragma unroll
@@ -306,59 +306,48 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
     }
   };
 
-  for (int s = wave; s < whole; s += KW * U) {
-    u32x4 w[U][R], xr[U][4 * MS];
-    uint32_t sb[U][R];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int su = s + KW * u;
-      if (su >= whole) break;
+  auto load = [&](int s, u32x4 (&w)[R], uint32_t (&sb)[R], u32x4 (&xr)[4 * MS]) {
+    const int left = K - s * kQuadStep;
+    if (left >= kQuadStep) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        w[u][j] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4_a8*>(wp[j] + su * (kQuadStep / 2)));
-        const uint8_t* q = sp[j] + su * (kQuadStep / kBlock);
-        if constexpr (kMX) sb[u][j] = q[0];
-        else if constexpr (kEven) sb[u][j] = *reinterpret_cast<const uint16_t*>(q);
-        else sb[u][j] = q[0] | (uint32_t)q[1] << 8;
+        w[j] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4_a8*>(wp[j] + s * (kQuadStep / 2)));
+        const uint8_t* q = sp[j] + s * (kQuadStep / kBlock);
+        if constexpr (kMX) sb[j] = q[0];
+        else if constexpr (kEven) sb[j] = *reinterpret_cast<const uint16_t*>(q);
+        else sb[j] = q[0] | (uint32_t)q[1] << 8;
       }
 #pragma unroll
       for (int m = 0; m < 4 * MS; ++m)
-        if (m < M) xr[u][m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + su * kQuadStep)[lane];
+        if (m < M) xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + s * kQuadStep)[lane];
+    } else {
+      // past K everything is zero (K % 16 == 0: a lane may hold half of its 32 weights)
+      const bool half = 32 * g + 16 <= left, full = 32 * g + 32 <= left;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(wp[j] + s * (kQuadStep / 2));
+        const uint8_t* q = sp[j] + s * (kQuadStep / kBlock);
+        w[j] = u32x4{half ? p[0] : 0u, half ? p[1] : 0u, full ? p[2] : 0u, full ? p[3] : 0u};
+        sb[j] = (half ? q[0] : 0u) | (!kMX && full ? (uint32_t)q[1] << 8 : 0u);
+      }
+#pragma unroll
+      for (int m = 0; m < 4 * MS; ++m) {
+        xr[m] = u32x4{0, 0, 0, 0};
+        if (m < M && 8 * lane < left)
+          xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + s * kQuadStep)[lane];
+      }
     }
+  };
+  for (int s = wave; s < steps; s += KW * U) {
+    u32x4 w[U][R], xr[U][4 * MS];
+    uint32_t sb[U][R];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (s + KW * u < whole) multiply(w[u], sb[u], xr[u]);
-  }
-  if (K % kQuadStep && whole % KW == wave) {
-    // the last step; past K everything is zero (K % 16 == 0: a lane may hold half)
-    const int left = K - whole * kQuadStep;
-    u32x4 w[R], xr[4 * MS];
-    uint32_t sb[R];
+      if (s + KW * u < steps) load(s + KW * u, w[u], sb[u], xr[u]);
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(wp[j] + whole * (kQuadStep / 2));
-      const uint8_t* qs = sp[j] + whole * (kQuadStep / kBlock);
-      w[j] = u32x4{0, 0, 0, 0};
-      sb[j] = 0;
-      if (32 * g + 16 <= left) {
-        w[j].x = q[0];
-        w[j].y = q[1];
-        sb[j] = qs[0];
-      }
-      if (32 * g + 32 <= left) {
-        w[j].z = q[2];
-        w[j].w = q[3];
-        if (!kMX) sb[j] |= (uint32_t)qs[1] << 8;
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < 4 * MS; ++m) {
-      xr[m] = u32x4{0, 0, 0, 0};
-      if (m < M && 8 * lane < left)
-        xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + whole * kQuadStep)[lane];
-    }
-    multiply(w, sb, xr);
+    for (int u = 0; u < U; ++u)
+      if (s + KW * u < steps) multiply(w[u], sb[u], xr[u]);
   }
 
 #pragma unroll
@@ -391,14 +380,11 @@ struct Shape {
   int nt, mt, kw;
 };
 Shape shape_of(const WLinearArgs& a) {
-  if (a.M <= 8) {
-    const bool wide = a.N >= 16 * 512;
-    return Shape{1, a.M <= 4 ? 0 : -1, wide ? 4 : 8};
-  }
-  const bool few = a.N < 16 * 512;
-  if (a.M <= 16) return few ? Shape{1, 1, 8} : Shape{2, 1, 4};
-  if (a.M <= 32) return few ? Shape{1, 2, 8} : Shape{2, 2, 4};
-  return few ? Shape{2, 4, 8} : Shape{4, 4, 4};
+  const int64_t tiles = (a.N + 15) / 16;
+  if (a.M <= 4) return Shape{1, 0, tiles >= 512 ? 4 : 8};
+  const int nt = (int)min(max((tiles + 64) / 256, (int64_t)1), (int64_t)3);
+  const int mt = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+  return Shape{nt, mt, mt == 4 ? 4 : 8};
 }
 int64_t tiles_of(const WLinearArgs& a, const Shape& h) {
   if (h.mt <= 0) return (a.N + 15) / 16;
@@ -436,9 +422,9 @@ hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s) {
   const Shape h = shape_of(a);
   (void)(launch_quad_if<1, 4>(a, h, s) || launch_quad_if<1, 8>(a, h, s) ||
          launch_quad_if<2, 4>(a, h, s) || launch_quad_if<2, 8>(a, h, s) ||
-         launch_if<1, 1, 8>(a, h, s) || launch_if<2, 1, 4>(a, h, s) ||
-         launch_if<1, 2, 8>(a, h, s) || launch_if<2, 2, 4>(a, h, s) ||
-         launch_if<2, 4, 8>(a, h, s) || launch_if<4, 4, 4>(a, h, s));
+         launch_if<1, 1, 8>(a, h, s) || launch_if<2, 1, 8>(a, h, s) || launch_if<3, 1, 8>(a, h, s) ||
+         launch_if<1, 2, 8>(a, h, s) || launch_if<2, 2, 8>(a, h, s) || launch_if<3, 2, 8>(a, h, s) ||
+         launch_if<1, 4, 4>(a, h, s) || launch_if<2, 4, 4>(a, h, s) || launch_if<3, 4, 4>(a, h, s));
   return hipGetLastError();
 }
 
