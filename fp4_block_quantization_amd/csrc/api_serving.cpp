@@ -190,7 +190,7 @@ size_t fos_paged_decode_workspace_bytes(int64_t num_seqs, int64_t num_q_heads,
   return fos::decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim);
 }
 
-size_t fos_paged_decode_counter_bytes(void) { return fos::decode_counter_bytes(); }
+size_t fos_paged_decode_counter_bytes(void) { return fos::kCounterBytes; }
 
 fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64_t q_stride,
                             int64_t num_seqs, int64_t num_q_heads, const int32_t* block_table,

@@ -37,15 +37,10 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kHeads = 16;            // query heads per workgroup: columns of the products
 constexpr int kStepTokens = 64 * kWaves;   // a step of a workgroup
-constexpr int kCUs = 256;
 constexpr int kMaxPerCU = 3;          // workgroups that a CU holds, at most
-constexpr int kMaxSegments = 65536;   // (sequence, head group) segments of one launch
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -486,26 +481,6 @@ struct Step<true, D> {
 
 constexpr float kSlack = 8.0f;    // see the rescaling below
 
-// Partial results pass from one workgroup to another on any XCD, each with an L2 of its
-// own.  A release and an acquire fence at that scope write back and invalidate a whole L2
-// (262 us instead of 92 for 32 sequences of up to 8192 tokens); instead the few values
-// that are passed are themselves accessed at device scope, as relaxed atomics of 8 bytes:
-// the stores write through to memory and the loads read from there.  What orders them is
-// that every thread waits until its stores are done (wait_stores), then the barrier, and
-// only then one thread counts the workgroup: who reads the full count reads after all
-// the stores.
-__device__ __forceinline__ void store_shared(float* p, f32x2 v) {
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v),
-                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ f32x2 load_shared(const float* p) {
-  return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p),
-                                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-}
-__device__ __forceinline__ void wait_stores() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-}
-
 // Joins the `count` partials of a segment, in order, and writes its outputs: each thread
 // takes four values of a head, eight partials at a time.
 template <int D>
@@ -794,15 +769,9 @@ __global__ __launch_bounds__(kThreads, (kPerCU<kNVFP4, D>)) void paged_decode_ke
     const int first = scalar((uint32_t)run.at / (uint32_t)run.share);
     const int count = scalar((uint32_t)(run.at + run.steps - 1) / (uint32_t)run.share) - first + 1;
     uint32_t* arrived = p.arrived + (int64_t)run.b * per + hg;
-    wait_stores();                             // each thread's own, before the barrier
-    __syncthreads();
-    if (threadIdx.x == 0)
-      before_me = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if ((int)before_me == count - 1) {
+    if (last_to_finish(arrived, count, before_me)) {
       join_partials<D>(p, parts + first * part_stride(p), count, rows, hrow0, vt0);
-      if (threadIdx.x == 0)
-        __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      reset_counter(arrived);
     }
   }
   run.pos += steps;
@@ -834,19 +803,17 @@ void launch_dim(Plan& p, int64_t steps, hipStream_t s) {
 int64_t segments_of(int64_t Hq, int64_t heads) {
   return heads * ((Hq / heads + kHeads - 1) / kHeads);
 }
-int64_t launch_seqs(int64_t B, int64_t per) { return min(B, kMaxSegments / per); }
+int64_t launch_seqs(int64_t B, int64_t per) { return min(B, kCounters / per); }
 
 }  // namespace
 
-bool decode_heads_ok(int64_t Hq, int64_t heads) { return segments_of(Hq, heads) <= kMaxSegments; }
-
-size_t decode_counter_bytes() { return sizeof(uint32_t) * kMaxSegments; }
+bool decode_heads_ok(int64_t Hq, int64_t heads) { return segments_of(Hq, heads) <= kCounters; }
 
 size_t decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim) {
   const int64_t G = Hq / heads, per = segments_of(Hq, heads);
   const int64_t runs = max(kMaxPerCU * kCUs / per, (int64_t)1);
   const int64_t parts = (runs + launch_seqs(B, per)) * per;
-  return decode_counter_bytes() +
+  return kCounterBytes +
          sizeof(float) * (size_t)(parts * (G < kHeads ? G : kHeads) * (dim + 2));
 }
 
@@ -859,7 +826,7 @@ hipError_t launch_paged_decode(const DecodeArgs& args, hipStream_t s) {
   const uint64_t d = a.c.page_size / 8;
   p.page_magic = (((uint64_t)1 << 36) + d - 1) / d;
   p.arrived = static_cast<uint32_t*>(a.ws);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + decode_counter_bytes());
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounterBytes);
   const int64_t per = (int64_t)a.c.heads * p.groups, B = args.B, seqs = launch_seqs(B, per);
   for (int64_t b = 0; b < B; b += seqs) {
     p.a.B = (int)min(seqs, B - b);

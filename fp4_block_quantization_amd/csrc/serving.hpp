@@ -6,6 +6,53 @@
 
 namespace fos {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kCUs = 256;
+
+// The workspace of the attention starts with counters of finished workgroups, 0 between
+// launches; what is behind them is scratch.
+constexpr int kCounters = 65536;
+constexpr size_t kCounterBytes = sizeof(uint32_t) * kCounters;
+
+// Partial results pass from one workgroup to another on any XCD, each with an L2 of its
+// own.  A release and an acquire fence at that scope write back and invalidate a whole L2
+// (paged attention of 32 sequences of up to 8192 tokens: 262 us instead of 89); instead the few values
+// that are passed are themselves accessed at device scope, as relaxed atomics of 8 bytes:
+// the stores write through to memory and the loads read from there.  What orders them is
+// that every thread waits until its stores are done (wait_stores), then the barrier, and
+// only then one thread counts the workgroup: who reads the full count reads after all
+// the stores.
+__device__ __forceinline__ void store_shared(float* p, f32x2 v) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 load_shared(const float* p) {
+  return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p),
+                                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ void wait_stores() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Counts this workgroup as done with the work behind `counter`, once every thread's
+// store_shared so far is done; true, for all threads, in the last of `count` workgroups
+// (which has to put the counter back to 0 with reset_counter).  `before` is in LDS.
+__device__ __forceinline__ bool last_to_finish(uint32_t* counter, int count, uint32_t& before) {
+  wait_stores();                               // each thread's own, before the barrier
+  __syncthreads();
+  if (threadIdx.x == 0)
+    before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return (int)before == count - 1;
+}
+__device__ __forceinline__ void reset_counter(uint32_t* counter) {
+  if (threadIdx.x == 0)
+    __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Weight-only linear: y[m][n] = t * sum_k x[m][k] deq(w)[n][k] (+ bias[n]).
 struct WLinearArgs {
   const uint16_t* x;       // bf16, row m at x + m * x_stride
@@ -56,10 +103,8 @@ struct DecodeArgs {
   float* lse;              // [B][Hq] or null
   void* ws;
 };
-// Whether the head layout has few enough segments, and the bytes at the start of the
-// workspace that are 0 between launches.
+// Whether the head layout has few enough segments.
 bool decode_heads_ok(int64_t Hq, int64_t heads);
-size_t decode_counter_bytes();
 size_t decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim);
 hipError_t launch_paged_decode(const DecodeArgs& a, hipStream_t s);
 

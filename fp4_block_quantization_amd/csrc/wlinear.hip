@@ -4,7 +4,7 @@
 //
 // Matrix form: E2M1 x E4M3 has at most 6 significant bits and E2M1 x 2^e two, so weights
 // are exact in bf16, products are exact in fp32, and every sum is fp32; y is rounded once.
-// Two kernels, by the number of activation rows: up to 8 on 4x4x4 products, where a lane
+// Two kernels, by the number of activation rows: up to 4 on 4x4x4 products, where a lane
 // keeps a weight row to itself, and more on 16x16x32 tiles, where a weight is converted
 // once for up to 64 activation rows.
 #include "serving.hpp"
@@ -15,9 +15,6 @@ namespace {
 
 constexpr int kChunk = 128;   // values of the inner dimension per wave and step
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // Weight rows are K / 2 bytes apart: 8-byte alignment (K % 16 == 0).
 typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -162,22 +159,26 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
       wf[n] = l.w[n][r][q ^ (r >> 2)];
       sf[n] = scale_values<kMX>(l.s[n][r][q]);
     }
-    u32x4 xf[4][MT];
+    // the reads of J steps are on their way before their first product (left alone, the
+    // scheduler reads each operand right before its product and waits for it)
+    constexpr int J = MT <= 2 ? 4 : 1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j0 = 0; j0 < 4; j0 += J) {
+      u32x4 xf[J][MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xf[j][m] = l.x[m][r][(4 * q + j) ^ r];
-    // every read is on its way before the first product (left alone, the scheduler reads
-    // each operand right before its product and waits for it)
-    __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < J; ++j)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+        for (int m = 0; m < MT; ++m) xf[j][m] = l.x[m][r][(4 * q + j0 + j) ^ r];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const u32x4 e = dequant8<kMX>(wf[n][j], j < 2 ? sf[n].x : sf[n].y);
+      for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[n][m] = mfma(e, xf[j][m], acc[n][m]);
-      }
+        for (int n = 0; n < NT; ++n) {
+          const u32x4 e = dequant8<kMX>(wf[n][j0 + j], j0 + j < 2 ? sf[n].x : sf[n].y);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[n][m] = mfma(e, xf[j][m], acc[n][m]);
+        }
+    }
   };
 
   if (wave < chunks) load(wave);
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
   }
 }
 
-// ---- few activation rows: M <= 8 ---------------------------------------------------
+// ---- few activation rows: M <= 4 ---------------------------------------------------
 // On the 4x4x4 instruction, 16 independent 4x4 products: a quad of lanes takes four weight
 // rows (its columns) over the same 32 values of the inner dimension and four activation
 // rows.  Each lane keeps the sums of its own weight row, so a block's scale multiplies the
@@ -236,16 +237,16 @@ __device__ __forceinline__ float sum_over_quads(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// MS: sets of four activation rows.  kEven: scale rows start at even bytes (K % 32 == 0),
+// kEven: scale rows start at even bytes (K % 32 == 0),
 // so that a lane's two NVFP4 scales are one aligned load.
-template <bool kMX, bool kEven, int MS, int KW>
-__global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(WLinearArgs a) {
+template <bool kMX, bool kEven, int KW>
+__global__ __launch_bounds__(64 * KW, 3) void wlinear_quad_kernel(WLinearArgs a) {
   constexpr int kBlock = kMX ? 32 : 16;
   constexpr int R = 4;                  // weight rows of a lane
-  constexpr int U = MS == 1 ? 2 : 1;    // steps in flight
+  constexpr int U = 2;                  // steps in flight
   typedef short s16x4 __attribute__((ext_vector_type(4)));
-  __shared__ u32x4 xs[KW][4 * MS][64];
-  __shared__ float sums[KW][16][4 * MS];
+  __shared__ u32x4 xs[KW][4][64];
+  __shared__ float sums[KW][16][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 3, g = lane >> 2;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int M = (int)a.M, K = (int)a.K, steps = (K + kQuadStep - 1) / kQuadStep;
@@ -258,55 +259,44 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
     wp[j] = a.wd + row * (K / 2) + 16 * g;
     sp[j] = a.ws + row * (K / kBlock) + 32 / kBlock * g;
   }
-  f32x4 acc[MS][R];
+  f32x4 acc[R];
 #pragma unroll
-  for (int m = 0; m < MS; ++m)
-#pragma unroll
-    for (int j = 0; j < R; ++j) acc[m][j] = f32x4{0, 0, 0, 0};
+  for (int j = 0; j < R; ++j) acc[j] = f32x4{0, 0, 0, 0};
 
   // The products of one step: w, sb the lane's weights and scales, x row m's unit `lane`.
   // Unit u of row m lies at u ^ (m % 4) in LDS: the four rows of a quad read from different
   // banks.  Rows past M are whatever LDS holds: they only reach sums that are not used.
-  auto multiply = [&](const u32x4 (&w)[R], const uint32_t (&sb)[R], const u32x4 (&xr)[4 * MS]) {
+  auto multiply = [&](const u32x4 (&w)[R], const uint32_t (&sb)[R], const u32x4 (&xr)[4]) {
 #pragma unroll
-    for (int m = 0; m < 4 * MS; ++m)
+    for (int m = 0; m < 4; ++m)
       if (m < M) xs[wave][m][lane ^ (m & 3)] = xr[m];
-    u32x4 x[MS][4];
+    u32x4 x[4];
 #pragma unroll
-    for (int m = 0; m < MS; ++m)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) x[m][u] = xs[wave][4 * m + i][(4 * g + u) ^ i];
+    for (int u = 0; u < 4; ++u) x[u] = xs[wave][i][(4 * g + u) ^ i];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const f32x2 sf = scale_values<kMX>(sb[j]);
 #pragma unroll
       for (int b = 0; b < 32 / kBlock; ++b) {
-        f32x4 part[MS];
-#pragma unroll
-        for (int m = 0; m < MS; ++m) part[m] = f32x4{0, 0, 0, 0};
+        f32x4 part = {0, 0, 0, 0};
 #pragma unroll
         for (int u = b * kBlock / 8; u < (b + 1) * kBlock / 8; ++u) {   // 8 values each
           const u32x4 e = dequant8<true>(w[j][u], 1.0f);
-#pragma unroll
-          for (int m = 0; m < MS; ++m) {
-            part[m] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
-                __builtin_bit_cast(s16x4, u32x2{x[m][u].x, x[m][u].y}),
-                __builtin_bit_cast(s16x4, u32x2{e.x, e.y}), part[m], 0, 0, 0);
-            part[m] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
-                __builtin_bit_cast(s16x4, u32x2{x[m][u].z, x[m][u].w}),
-                __builtin_bit_cast(s16x4, u32x2{e.z, e.w}), part[m], 0, 0, 0);
-          }
+          part = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+              __builtin_bit_cast(s16x4, u32x2{x[u].x, x[u].y}),
+              __builtin_bit_cast(s16x4, u32x2{e.x, e.y}), part, 0, 0, 0);
+          part = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+              __builtin_bit_cast(s16x4, u32x2{x[u].z, x[u].w}),
+              __builtin_bit_cast(s16x4, u32x2{e.z, e.w}), part, 0, 0, 0);
         }
         const float d = b ? sf.y : sf.x;
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[m][j][c] = __builtin_fmaf(part[m][c], d, acc[m][j][c]);
+        for (int c = 0; c < 4; ++c) acc[j][c] = __builtin_fmaf(part[c], d, acc[j][c]);
       }
     }
   };
 
-  auto load = [&](int s, u32x4 (&w)[R], uint32_t (&sb)[R], u32x4 (&xr)[4 * MS]) {
+  auto load = [&](int s, u32x4 (&w)[R], uint32_t (&sb)[R], u32x4 (&xr)[4]) {
     const int left = K - s * kQuadStep;
     if (left >= kQuadStep) {
 #pragma unroll
@@ -319,7 +309,7 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
         else sb[j] = q[0] | (uint32_t)q[1] << 8;
       }
 #pragma unroll
-      for (int m = 0; m < 4 * MS; ++m)
+      for (int m = 0; m < 4; ++m)
         if (m < M) xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + s * kQuadStep)[lane];
     } else {
       // past K everything is zero (K % 16 == 0: a lane may hold half of its 32 weights)
@@ -332,7 +322,7 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
         sb[j] = (half ? q[0] : 0u) | (!kMX && full ? (uint32_t)q[1] << 8 : 0u);
       }
 #pragma unroll
-      for (int m = 0; m < 4 * MS; ++m) {
+      for (int m = 0; m < 4; ++m) {
         xr[m] = u32x4{0, 0, 0, 0};
         if (m < M && 8 * lane < left)
           xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + s * kQuadStep)[lane];
@@ -340,7 +330,7 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
     }
   };
   for (int s = wave; s < steps; s += KW * U) {
-    u32x4 w[U][R], xr[U][4 * MS];
+    u32x4 w[U][R], xr[U][4];
     uint32_t sb[U][R];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -351,14 +341,12 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
   }
 
 #pragma unroll
-  for (int m = 0; m < MS; ++m)
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int j = 0; j < R; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float v = sum_over_quads(acc[m][j][c]);
-        if (g == 0) sums[wave][4 * j + i][4 * m + c] = v;
-      }
+    for (int c = 0; c < 4; ++c) {
+      const float v = sum_over_quads(acc[j][c]);
+      if (g == 0) sums[wave][4 * j + i][c] = v;
+    }
   __syncthreads();
   for (int e = threadIdx.x; e < 16 * M; e += 64 * KW) {
     const int n = e & 15, m = e >> 4;
@@ -374,20 +362,37 @@ __global__ __launch_bounds__(64 * KW, MS == 1 ? 3 : 2) void wlinear_quad_kernel(
   }
 }
 
-// Tile and split for a shape: 16 NT weight rows, 16 MT activation rows, KW waves.
-// MT 0 and -1: the quad kernel with one or two sets of four activation rows.
+// Kernel and tile for a shape: 16 NT weight rows by 16 MT activation rows (MT 0: the quad
+// kernel), KW waves.
 struct Shape {
   int nt, mt, kw;
 };
+int64_t tiles_of(const WLinearArgs& a, const Shape& h);
+
+// Up to 4 activation rows: the quad kernel (M = 4, 12288 x 4096: 9.1 us, a tile of one
+// activation set 9.6; M = 1: 7.9 us), with 4 waves where the weight rows alone give two
+// workgroups per CU.  More: the tile that is done first, by what one workgroup of each
+// takes at K = 4096 (us, measured) times the rounds of 256 workgroups.
 Shape shape_of(const WLinearArgs& a) {
-  const int64_t tiles = (a.N + 15) / 16;
-  if (a.M <= 4) return Shape{1, 0, tiles >= 512 ? 4 : 8};
-  const int nt = (int)min(max((tiles + 64) / 256, (int64_t)1), (int64_t)3);
-  const int mt = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-  return Shape{nt, mt, mt == 4 ? 4 : 8};
+  if (a.M <= 4) return Shape{1, 0, a.N >= 2 * 16 * kCUs ? 4 : 8};
+  constexpr struct {
+    Shape shape;
+    float us;
+  } kTiles[] = {{{1, 1, 8}, 3.3f}, {{2, 1, 8}, 5.0f}, {{3, 1, 8}, 7.5f},
+                {{2, 2, 4}, 7.9f}, {{3, 2, 4}, 10.0f}, {{3, 4, 4}, 17.4f}};
+  Shape best = kTiles[0].shape;
+  float least = INFINITY;
+  for (const auto& c : kTiles) {
+    const float us = c.us * (float)((tiles_of(a, c.shape) + kCUs - 1) / kCUs);
+    if (us < least) {
+      least = us;
+      best = c.shape;
+    }
+  }
+  return best;
 }
 int64_t tiles_of(const WLinearArgs& a, const Shape& h) {
-  if (h.mt <= 0) return (a.N + 15) / 16;
+  if (h.mt == 0) return (a.N + 15) / 16;
   return ((a.N + 16 * h.nt - 1) / (16 * h.nt)) * ((a.M + 16 * h.mt - 1) / (16 * h.mt));
 }
 
@@ -401,13 +406,13 @@ bool launch_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
   return true;
 }
 
-template <int MS, int KW>
+template <int KW>
 bool launch_quad_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
-  if (h.mt != 1 - MS || h.kw != KW) return false;
+  if (h.mt != 0 || h.kw != KW) return false;
   const uint32_t grid = (uint32_t)tiles_of(a, h);
-  if (a.mx) wlinear_quad_kernel<true, true, MS, KW><<<grid, 64 * KW, 0, s>>>(a);
-  else if (a.K % 32 == 0) wlinear_quad_kernel<false, true, MS, KW><<<grid, 64 * KW, 0, s>>>(a);
-  else wlinear_quad_kernel<false, false, MS, KW><<<grid, 64 * KW, 0, s>>>(a);
+  if (a.mx) wlinear_quad_kernel<true, true, KW><<<grid, 64 * KW, 0, s>>>(a);
+  else if (a.K % 32 == 0) wlinear_quad_kernel<false, true, KW><<<grid, 64 * KW, 0, s>>>(a);
+  else wlinear_quad_kernel<false, false, KW><<<grid, 64 * KW, 0, s>>>(a);
   return true;
 }
 
@@ -420,11 +425,9 @@ int64_t wlinear_threads(const WLinearArgs& a) {
 
 hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s) {
   const Shape h = shape_of(a);
-  (void)(launch_quad_if<1, 4>(a, h, s) || launch_quad_if<1, 8>(a, h, s) ||
-         launch_quad_if<2, 4>(a, h, s) || launch_quad_if<2, 8>(a, h, s) ||
-         launch_if<1, 1, 8>(a, h, s) || launch_if<2, 1, 8>(a, h, s) || launch_if<3, 1, 8>(a, h, s) ||
-         launch_if<1, 2, 8>(a, h, s) || launch_if<2, 2, 8>(a, h, s) || launch_if<3, 2, 8>(a, h, s) ||
-         launch_if<1, 4, 4>(a, h, s) || launch_if<2, 4, 4>(a, h, s) || launch_if<3, 4, 4>(a, h, s));
+  (void)(launch_quad_if<4>(a, h, s) || launch_quad_if<8>(a, h, s) || launch_if<1, 1, 8>(a, h, s) ||
+         launch_if<2, 1, 8>(a, h, s) || launch_if<3, 1, 8>(a, h, s) || launch_if<2, 2, 4>(a, h, s) ||
+         launch_if<3, 2, 4>(a, h, s) || launch_if<3, 4, 4>(a, h, s));
   return hipGetLastError();
 }
 
