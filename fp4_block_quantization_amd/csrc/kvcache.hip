@@ -13,99 +13,133 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Row (slot, head) of the cache, or -1.
-__device__ __forceinline__ int64_t cache_row(const KVCacheArgs& c, int64_t slot, int head) {
-  if (slot < 0 || slot >= c.num_pages * c.page_size) return -1;
-  const int64_t page = slot / c.page_size;
-  return (page * c.heads + head) * c.page_size + (slot - page * c.page_size);
+// Divisions of the index arithmetic as products with ceil(2^k / d): exact where the
+// dividend times d stays below 2^k.
+struct Div64 {                  // dividend < 2^40, d < 2^24
+  uint64_t magic;
+  explicit Div64(uint64_t d) : magic(~(uint64_t)0 / d + 1) {}
+  __device__ __forceinline__ uint64_t operator()(uint64_t x) const { return __umul64hi(x, magic); }
+};
+struct Div32 {                  // dividend * d < 2^32
+  uint32_t magic;
+  explicit Div32(uint32_t d) : magic(~(uint32_t)0 / d + 1) {}
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const { return __umulhi(x, magic); }
+};
+
+// One thread per kValues consecutive values of a row; blockIdx.y 0: K, 1: V.
+struct Plan {
+  KVRowsArgs a;
+  int64_t n;                    // threads of K
+  uint32_t per, units;          // threads of a token (fewer than 2^24), of a row
+  Div64 by_per, by_page;
+  Div32 by_units;
+  Plan(const KVRowsArgs& args, int values)
+      : a(args), n(args.T * args.c.heads * (args.c.dim / values)),
+        per((uint32_t)(args.c.heads * (args.c.dim / values))),
+        units((uint32_t)(args.c.dim / values)), by_per(per), by_page((uint64_t)args.c.page_size),
+        by_units(units) {}
+  dim3 grid() const { return dim3((uint32_t)((n + kThreads - 1) / kThreads), 2); }
+};
+
+// What a thread works on: unit `unit` (of per) of token tok, and its place in the cache in
+// units, or -1 for a slot outside it.
+struct Where {
+  int64_t tok, at;
+  uint32_t unit;
+};
+__device__ __forceinline__ Where locate(const Plan& p, int64_t i) {
+  Where w;
+  w.tok = (int64_t)p.by_per((uint64_t)i);
+  w.unit = (uint32_t)(i - w.tok * p.per);
+  const KVCacheArgs& c = p.a.c;
+  const int64_t slot = p.a.slots[w.tok];
+  w.at = -1;
+  if (slot >= 0 && slot < c.num_pages * c.page_size) {
+    const int64_t page = (int64_t)p.by_page((uint64_t)slot);
+    const uint32_t head = p.by_units(w.unit);
+    const int64_t row = (page * c.heads + head) * c.page_size + (slot - page * c.page_size);
+    w.at = row * p.units + (w.unit - head * p.units);
+  }
+  return w;
 }
 
-// One thread per 16 values of one row of K (blockIdx.y 0) or V (1).
+typedef u32x4 v4u;
+
+// 16 values: one block.  The input is loaded before the workgroup's table of scales is
+// built, and the rows are read once: non-temporal loads.
 template <bool k46>
-__global__ __launch_bounds__(kThreads) void append_nvfp4_kernel(KVRowsArgs a) {
+__global__ __launch_bounds__(kThreads) void append_nvfp4_kernel(Plan p) {
   __shared__ float2 tab[kScaleTableSize];
+  const KVRowsArgs& a = p.a;
   const bool is_v = blockIdx.y != 0;
   const float t = is_v ? a.c.vt[0] : a.c.kt[0];
+  const int64_t i = min((int64_t)blockIdx.x * kThreads + threadIdx.x, p.n - 1);
+  const Where w = locate(p, i);      // threads past the last do the last once more
+  const v4u* src = reinterpret_cast<const v4u*>((is_v ? a.v + w.tok * a.v_stride
+                                                      : a.k + w.tok * a.k_stride) + 16 * w.unit);
+  const v4u l0 = __builtin_nontemporal_load(src), l1 = __builtin_nontemporal_load(src + 1);
   build_scale_table(tab, t);
-  const int nb = a.c.dim / 16, per = nb * a.c.heads;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= a.T * per) return;
-  const int64_t tok = i / per;
-  const int r = (int)(i - tok * per);
-  const int64_t row = cache_row(a.c, a.slots[tok], r / nb);
-  if (row < 0) return;
-  const uint16_t* src = (is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) + 16 * r;
-  const uint4 w0 = reinterpret_cast<const uint4*>(src)[0];
-  const uint4 w1 = reinterpret_cast<const uint4*>(src)[1];
+  if (w.at < 0) return;
   float v[16];
-  unpack16(w0, w1, v);
+  unpack16(make_uint4(l0.x, l0.y, l0.z, l0.w), make_uint4(l1.x, l1.y, l1.z, l1.w), v);
   const uint32_t none[16] = {};
   const Cand c = quantize_block<k46, false>(v, tab, tab[128].x, tab[128].y, none);
-  const int64_t blk = row * nb + r % nb;
-  *reinterpret_cast<uint2*>((is_v ? a.c.v : a.c.k) + 8 * blk) = make_uint2(c.lo, c.hi);
-  (is_v ? a.c.vs : a.c.ks)[blk] = (uint8_t)c.s;
+  *reinterpret_cast<uint2*>((is_v ? a.c.v : a.c.k) + 8 * w.at) = make_uint2(c.lo, c.hi);
+  (is_v ? a.c.vs : a.c.ks)[w.at] = (uint8_t)c.s;
 }
 
-// One thread per 8 values.
-__global__ __launch_bounds__(kThreads) void append_bf16_kernel(KVRowsArgs a) {
+// 8 values.
+__global__ __launch_bounds__(kThreads) void append_bf16_kernel(Plan p) {
+  const KVRowsArgs& a = p.a;
   const bool is_v = blockIdx.y != 0;
-  const int nb = a.c.dim / 8, per = nb * a.c.heads;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= a.T * per) return;
-  const int64_t tok = i / per;
-  const int r = (int)(i - tok * per);
-  const int64_t row = cache_row(a.c, a.slots[tok], r / nb);
-  if (row < 0) return;
-  const uint16_t* src = (is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) + 8 * r;
-  reinterpret_cast<uint4*>(is_v ? a.c.v : a.c.k)[row * nb + r % nb] =
-      *reinterpret_cast<const uint4*>(src);
+  if (i >= p.n) return;
+  const Where w = locate(p, i);
+  if (w.at < 0) return;
+  const uint16_t* src = (is_v ? a.v + w.tok * a.v_stride : a.k + w.tok * a.k_stride) + 8 * w.unit;
+  reinterpret_cast<v4u*>(is_v ? a.c.v : a.c.k)[w.at] =
+      __builtin_nontemporal_load(reinterpret_cast<const v4u*>(src));
 }
 
-// One thread per 8 values.
+// 8 values.
 template <bool kNVFP4>
-__global__ __launch_bounds__(kThreads) void gather_kernel(KVRowsArgs a) {
+__global__ __launch_bounds__(kThreads) void gather_kernel(Plan p) {
+  const KVRowsArgs& a = p.a;
   const bool is_v = blockIdx.y != 0;
-  const int nb = a.c.dim / 8, per = nb * a.c.heads;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= a.T * per) return;
-  const int64_t tok = i / per;
-  const int r = (int)(i - tok * per);
-  const int64_t row = cache_row(a.c, a.slots[tok], r / nb);
-  uint4 o = make_uint4(0, 0, 0, 0);
-  if (row >= 0) {
-    const int64_t at = row * nb + r % nb;
+  if (i >= p.n) return;
+  const Where w = locate(p, i);
+  v4u o = {0, 0, 0, 0};
+  if (w.at >= 0) {
     if (kNVFP4) {
-      const uint32_t q = reinterpret_cast<const uint32_t*>(is_v ? a.c.v : a.c.k)[at];
-      const float d = e4m3_decode((is_v ? a.c.vs : a.c.ks)[at >> 1]) * (is_v ? a.c.vt[0] : a.c.kt[0]);
+      const uint32_t q = reinterpret_cast<const uint32_t*>(is_v ? a.c.v : a.c.k)[w.at];
+      const float d = e4m3_decode((is_v ? a.c.vs : a.c.ks)[w.at >> 1]) * (is_v ? a.c.vt[0] : a.c.kt[0]);
       const f32x2 e0 = cvt_pk_f32_fp4<0>(q), e1 = cvt_pk_f32_fp4<1>(q);
       const f32x2 e2 = cvt_pk_f32_fp4<2>(q), e3 = cvt_pk_f32_fp4<3>(q);
-      o = make_uint4(pack_bf16x2(e0.x * d, e0.y * d), pack_bf16x2(e1.x * d, e1.y * d),
-                     pack_bf16x2(e2.x * d, e2.y * d), pack_bf16x2(e3.x * d, e3.y * d));
+      o = v4u{pack_bf16x2(e0.x * d, e0.y * d), pack_bf16x2(e1.x * d, e1.y * d),
+              pack_bf16x2(e2.x * d, e2.y * d), pack_bf16x2(e3.x * d, e3.y * d)};
     } else {
-      o = reinterpret_cast<const uint4*>(is_v ? a.c.v : a.c.k)[at];
+      o = reinterpret_cast<const v4u*>(is_v ? a.c.v : a.c.k)[w.at];
     }
   }
-  uint16_t* dst = (is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride) + 8 * r;
-  *reinterpret_cast<uint4*>(dst) = o;
-}
-
-dim3 rows_grid(const KVRowsArgs& a, int values) {
-  const int64_t n = a.T * a.c.heads * (a.c.dim / values);
-  return dim3((uint32_t)((n + kThreads - 1) / kThreads), 2);
+  uint16_t* dst = (is_v ? a.v + w.tok * a.v_stride : a.k + w.tok * a.k_stride) + 8 * w.unit;
+  *reinterpret_cast<v4u*>(dst) = o;
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const KVRowsArgs& a, hipStream_t s) {
-  if (!a.c.nvfp4) append_bf16_kernel<<<rows_grid(a, 8), kThreads, 0, s>>>(a);
-  else if (a.four_over_six) append_nvfp4_kernel<true><<<rows_grid(a, 16), kThreads, 0, s>>>(a);
-  else append_nvfp4_kernel<false><<<rows_grid(a, 16), kThreads, 0, s>>>(a);
+  const Plan p(a, a.c.nvfp4 ? 16 : 8);
+  if (!a.c.nvfp4) append_bf16_kernel<<<p.grid(), kThreads, 0, s>>>(p);
+  else if (a.four_over_six) append_nvfp4_kernel<true><<<p.grid(), kThreads, 0, s>>>(p);
+  else append_nvfp4_kernel<false><<<p.grid(), kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_kv_gather(const KVRowsArgs& a, hipStream_t s) {
-  if (a.c.nvfp4) gather_kernel<true><<<rows_grid(a, 8), kThreads, 0, s>>>(a);
-  else gather_kernel<false><<<rows_grid(a, 8), kThreads, 0, s>>>(a);
+  const Plan p(a, 8);
+  if (a.c.nvfp4) gather_kernel<true><<<p.grid(), kThreads, 0, s>>>(p);
+  else gather_kernel<false><<<p.grid(), kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -11,6 +11,7 @@ device tensors; ``quantize`` / ``dequantize`` / ``qlinear_fwd`` allocate the out
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -536,8 +537,15 @@ def mx_qlinear_fwd(aq: MXFP4Tensor, bq: MXFP4Tensor, out: Optional[torch.Tensor]
 # These calls run once per layer and token, so their wrappers marshal raw addresses and
 # check no more than the library needs to stay inside its tensors.
 
+# The handle of a device's current stream; torch's own accessor where this build of torch
+# has it (0.1 us; building a Stream object for it takes 1.9 us of a call's 10).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(device.index)
 
 
 _OUT_CODE = {torch.float32: FOS_OUT_F32, torch.bfloat16: FOS_OUT_BF16}
@@ -714,6 +722,11 @@ def kv_gather(cache: PagedKVCache, slots: torch.Tensor) -> Tuple[torch.Tensor, t
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
+def _decode_need(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(_lib.fos_paged_decode_workspace_bytes(B, Hq, Hkv, D))
+
+
 _decode_workspaces = {}
 
 
@@ -764,8 +777,7 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
         raise ValueError("out must be a contiguous bf16 tensor of q's shape on the cache's device")
     lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
     stream = _raw_stream(dev)
-    need = _lib.fos_paged_decode_workspace_bytes(B, Hq, cache.num_kv_heads, D)
-    ws = _decode_workspace(dev, stream, need)
+    ws = _decode_workspace(dev, stream, _decode_need(B, Hq, cache.num_kv_heads, D))
     _check(_lib.fos_paged_decode(cache._ref, q.data_ptr(), s[0], B, Hq, block_table.data_ptr(),
                                  block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
                                  1.0 / math.sqrt(D) if scale is None else scale, int(window),
