@@ -66,7 +66,8 @@ __device__ __forceinline__ Where locate(const Plan& p, int64_t i) {
 typedef u32x4 v4u;
 
 // 16 values: one block.  The input is loaded before the workgroup's table of scales is
-// built, and the rows are read once: non-temporal loads.
+// built.  Cached loads: new rows come out of the projection before (8192 tokens of 8 heads
+// of 128, append and gather: 19.5 us, with non-temporal loads 22.9).
 template <bool k46>
 __global__ __launch_bounds__(kThreads) void append_nvfp4_kernel(Plan p) {
   __shared__ float2 tab[kScaleTableSize];
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(kThreads) void append_nvfp4_kernel(Plan p) {
   const Where w = locate(p, i);      // threads past the last do the last once more
   const v4u* src = reinterpret_cast<const v4u*>((is_v ? a.v + w.tok * a.v_stride
                                                       : a.k + w.tok * a.k_stride) + 16 * w.unit);
-  const v4u l0 = __builtin_nontemporal_load(src), l1 = __builtin_nontemporal_load(src + 1);
+  const v4u l0 = src[0], l1 = src[1];
   build_scale_table(tab, t);
   if (w.at < 0) return;
   float v[16];
@@ -97,8 +98,7 @@ __global__ __launch_bounds__(kThreads) void append_bf16_kernel(Plan p) {
   const Where w = locate(p, i);
   if (w.at < 0) return;
   const uint16_t* src = (is_v ? a.v + w.tok * a.v_stride : a.k + w.tok * a.k_stride) + 8 * w.unit;
-  reinterpret_cast<v4u*>(is_v ? a.c.v : a.c.k)[w.at] =
-      __builtin_nontemporal_load(reinterpret_cast<const v4u*>(src));
+  reinterpret_cast<v4u*>(is_v ? a.c.v : a.c.k)[w.at] = *reinterpret_cast<const v4u*>(src);
 }
 
 // 8 values.

@@ -108,8 +108,9 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
     if (left >= kChunk) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        w[n] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4_a8*>(wp[n] + c * (kChunk / 2)));
+        // cached: a chunk of a row is half a line, another wave reads the other half (with
+        // non-temporal loads 16.4 us instead of 12.7 at 61 x 4099 x 4112)
+        w[n] = *reinterpret_cast<const u32x4_a8*>(wp[n] + c * (kChunk / 2));
         const uint8_t* s = sp[n] + c * (kChunk / kBlock);
         if constexpr (kMX) sb[n] = s[0];
         else if constexpr (kEven) sb[n] = *reinterpret_cast<const uint16_t*>(s);
@@ -369,17 +370,19 @@ struct Shape {
 };
 int64_t tiles_of(const WLinearArgs& a, const Shape& h);
 
-// Up to 4 activation rows: the quad kernel (M = 4, 12288 x 4096: 9.1 us, a tile of one
-// activation set 9.6; M = 1: 7.9 us), with 4 waves where the weight rows alone give two
-// workgroups per CU.  More: the tile that is done first, by what one workgroup of each
-// takes at K = 4096 (us, measured) times the rounds of 256 workgroups.
+// The quad kernel for up to 2 activation rows, and up to 4 where the weight rows alone do
+// not give two workgroups per CU (1 x 12288 x 4096: 8.0 us, a tile 8.6; 4 x 4096 x 12288: 9.3,
+// a tile 9.6; 4 x 12288 x 4096: 9.1, a tile 8.6).  Otherwise the tile that is done first, by
+// what one workgroup of each takes at K = 4096 (us, measured) times the rounds of 256
+// workgroups.
 Shape shape_of(const WLinearArgs& a) {
-  if (a.M <= 4) return Shape{1, 0, a.N >= 2 * 16 * kCUs ? 4 : 8};
+  const bool wide = a.N >= 2 * 16 * kCUs;
+  if (a.M <= (wide ? 2 : 4)) return Shape{1, 0, wide ? 4 : 8};
   constexpr struct {
     Shape shape;
     float us;
-  } kTiles[] = {{{1, 1, 8}, 3.3f}, {{2, 1, 8}, 5.0f}, {{3, 1, 8}, 7.5f},
-                {{2, 2, 4}, 7.9f}, {{3, 2, 4}, 10.0f}, {{3, 4, 4}, 17.4f}};
+  } kTiles[] = {{{1, 1, 8}, 2.6f}, {{2, 1, 8}, 4.0f}, {{3, 1, 8}, 6.2f},
+                {{2, 2, 4}, 6.6f}, {{3, 2, 4}, 9.0f}, {{3, 4, 4}, 14.7f}};
   Shape best = kTiles[0].shape;
   float least = INFINITY;
   for (const auto& c : kTiles) {
