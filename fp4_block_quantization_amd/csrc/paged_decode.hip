@@ -504,22 +504,22 @@ __device__ __forceinline__ void join_partials(const Plan& p, const float* all, i
       float m2 = m;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) m2 = fmaxf(m2, ml[k].x);
-      if (m2 == -INFINITY) continue;             // nothing seen so far
-      const float f = __builtin_amdgcn_exp2f(m - m2);
+      const float m1 = m2 == -INFINITY ? 0.0f : m2;    // nothing seen so far: all weights 0
+      const float f = __builtin_amdgcn_exp2f(m - m1);
       m = m2;
       l *= f;
       o *= f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float w = c + k < count ? __builtin_amdgcn_exp2f(ml[k].x - m) : 0.0f;
+        const float w = c + k < count ? __builtin_amdgcn_exp2f(ml[k].x - m1) : 0.0f;
         l += w * ml[k].y;
         o += w * f32x4{x[k].x, x[k].y, y[k].x, y[k].y};
       }
     }
-    const float n = l > 0.0f ? vt0 / l : 0.0f;
+    const float n = l == 0.0f ? 0.0f : vt0 / l;      // a NaN sum stays one
     *reinterpret_cast<u32x2*>(p.a.out + (hrow0 + g) * D + d) =
         u32x2{pack_bf16x2(o[0] * n, o[1] * n), pack_bf16x2(o[2] * n, o[3] * n)};
-    if (d == 0 && p.a.lse) p.a.lse[hrow0 + g] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (d == 0 && p.a.lse) p.a.lse[hrow0 + g] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -757,9 +757,9 @@ __global__ __launch_bounds__(kThreads, (kPerCU<kNVFP4, D>)) void paged_decode_ke
       y += f * so[w][g][d + 1];
     }
     if (whole) {
-      const float n = ll > 0.0f ? vt0 / ll : 0.0f;
+      const float n = ll == 0.0f ? 0.0f : vt0 / ll;
       *reinterpret_cast<uint32_t*>(a.out + (hrow0 + g) * D + d) = pack_bf16x2(x * n, y * n);
-      if (d == 0 && a.lse) a.lse[hrow0 + g] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+      if (d == 0 && a.lse) a.lse[hrow0 + g] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     } else {
       store_shared(part + 2 * p.rows + g * D + d, f32x2{x, y});
       if (d == 0) store_shared(part + 2 * g, f32x2{mm, ll});

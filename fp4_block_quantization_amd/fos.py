@@ -730,21 +730,34 @@ def _decode_need(B: int, Hq: int, Hkv: int, D: int) -> int:
 _decode_workspaces = {}
 
 
-def _decode_workspace(device: torch.device, stream: int, need: int) -> torch.Tensor:
-    """Scratch of paged_decode for one stream, its counters cleared.  It grows by powers of two, and an outgrown
-    one is kept: a captured graph may hold its address."""
+def paged_decode_workspace(B: int, Hq: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
+    """A workspace for paged_decode of these sizes, its counters cleared (by work on the
+    current stream): what a captured graph passes as ``ws``."""
+    need = _decode_need(B, Hq, Hkv, D)
+    if need == 0:
+        raise ValueError("sizes that paged_decode does not take")
+    ws = torch.empty(1 << (need - 1).bit_length(), dtype=torch.uint8, device=device)
+    ws[:int(_lib.fos_paged_decode_counter_bytes())].zero_()
+    return ws
+
+
+def _decode_workspace(device: torch.device, stream: int, sizes) -> torch.Tensor:
+    """The current stream's scratch for paged_decode, grown by powers of two.  A captured
+    call gets one of its own, cleared in the graph: the graph may be replayed on another
+    stream, or later than the next eager call on this one."""
+    if torch.cuda.is_current_stream_capturing():
+        return paged_decode_workspace(*sizes, device=device)
     key = (device.index, stream)
-    held = _decode_workspaces.setdefault(key, [])
-    if not held or held[-1].numel() < need:
-        ws = torch.empty(1 << (need - 1).bit_length(), dtype=torch.uint8, device=device)
-        ws[:int(_lib.fos_paged_decode_counter_bytes())].zero_()
-        held.append(ws)
-    return held[-1]
+    ws = _decode_workspaces.get(key)
+    if ws is None or ws.numel() < _decode_need(*sizes):
+        ws = _decode_workspaces[key] = paged_decode_workspace(*sizes, device=device)
+    return ws
 
 
 def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor,
                  seq_lens: torch.Tensor, scale: Optional[float] = None, window: int = 0,
-                 return_lse: bool = False, out: Optional[torch.Tensor] = None):
+                 return_lse: bool = False, out: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None):
     """Attention of one new token per sequence over the paged cache.
 
     q: bf16 [B, query heads, head dim] (the sequence stride is free; query heads a
@@ -752,6 +765,8 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
     strided; an id outside the cache is a page no longer held, whose tokens are not
     visible.  seq_lens: int32 [B], the new token included.  scale: default
     1/sqrt(head dim).  window > 0: only the last ``window`` tokens are visible.
+    ``ws``: a ``paged_decode_workspace`` that no overlapping call uses; by default the
+    current stream's (in a graph capture a new one, cleared by every replay).
     Returns bf16 [B, query heads, head dim] (``out`` if given), and with
     ``return_lse`` also the fp32 [B, query heads] log-sum-exp of the scaled scores.
     Where nothing is visible the output is 0 and its lse -inf."""
@@ -777,7 +792,10 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
         raise ValueError("out must be a contiguous bf16 tensor of q's shape on the cache's device")
     lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
     stream = _raw_stream(dev)
-    ws = _decode_workspace(dev, stream, _decode_need(B, Hq, cache.num_kv_heads, D))
+    if ws is None:
+        ws = _decode_workspace(dev, stream, (B, Hq, cache.num_kv_heads, D))
+    elif ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on the cache's device")
     _check(_lib.fos_paged_decode(cache._ref, q.data_ptr(), s[0], B, Hq, block_table.data_ptr(),
                                  block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
                                  1.0 / math.sqrt(D) if scale is None else scale, int(window),

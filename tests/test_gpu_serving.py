@@ -549,3 +549,66 @@ def test_decode_replayed_from_a_graph(fos, fmt):
         want = fos.paged_decode(q, eager, table, lens)
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int16), want.view(torch.int16)), i
+
+
+@FMTS
+@pytest.mark.parametrize("L", [5, 300, 5000])
+def test_decode_keeps_a_nan(fos, fmt, L):
+    """A NaN query gives NaN in its head's output and lse, one sequence, few tokens or
+    many workgroups alike, and touches no other head."""
+    cache = new_cache(fos, fmt, 320, 16, 2, 64)
+    k, v = (W.random_bf16(L, 128, s, "normal").to(DEV).view(L, 2, 64) for s in (1, 2))
+    fos.kv_append(cache, k, v, torch.arange(L, device=DEV))
+    q = W.random_bf16(1, 256, 3, "normal").to(DEV).view(1, 4, 64)
+    args = (torch.arange(320, dtype=torch.int32, device=DEV)[None],
+            torch.tensor([L], dtype=torch.int32, device=DEV))
+    out, lse = fos.paged_decode(q, cache, *args, return_lse=True)
+    q[0, 1, 17] = float("nan")
+    got, got_lse = fos.paged_decode(q, cache, *args, return_lse=True)
+    assert got[0, 1].isnan().all() and got_lse[0, 1].isnan()
+    rest = [0, 2, 3]
+    assert torch.equal(got[0, rest], out[0, rest]) and torch.equal(got_lse[0, rest], lse[0, rest])
+
+
+def test_decode_captured_before_any_call(fos):
+    """A capture that is the first call of its stream, and whose graph is replayed only
+    after an eager call there, changes neither; a workspace of the caller's serves both."""
+    cache = new_cache(fos, "nvfp4", 320, 16, 2, 64)
+    L = 5000
+    k, v = (W.random_bf16(L, 128, s, "normal").to(DEV).view(L, 2, 64) for s in (1, 2))
+    fos.kv_append(cache, k, v, torch.arange(L, device=DEV))
+    q = W.random_bf16(1, 256, 3, "normal").to(DEV).view(1, 4, 64)
+    args = (torch.arange(320, dtype=torch.int32, device=DEV)[None],
+            torch.tensor([L], dtype=torch.int32, device=DEV))
+    want = fos.paged_decode(q, cache, *args)
+    own = fos.paged_decode_workspace(1, 4, 2, 64, DEV)
+    outs = [torch.zeros_like(want) for _ in range(3)]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        fos.paged_decode(q, cache, *args, out=outs[0])
+        fos.paged_decode(q, cache, *args, out=outs[1], ws=own)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fos.paged_decode(q, cache, *args, out=outs[2])
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        outs[0].zero_(), outs[1].zero_()
+        graph.replay()
+        eager = fos.paged_decode(q, cache, *args, ws=own)
+        torch.cuda.synchronize()
+        for o in (outs[0], outs[1], outs[2], eager):
+            assert torch.equal(o, want)
+
+
+def test_decode_refuses_a_workspace_that_is_too_small(fos):
+    cache = new_cache(fos, "bf16", 4, 16, 2, 64)
+    q = torch.ones(1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    args = (torch.zeros(1, 4, dtype=torch.int32, device=DEV),
+            torch.ones(1, dtype=torch.int32, device=DEV))
+    with pytest.raises(fos.FosError):
+        fos.paged_decode(q, cache, *args, ws=torch.zeros(4096, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        fos.paged_decode(q, cache, *args, ws=torch.zeros(4096, device=DEV))
+    with pytest.raises(ValueError):
+        fos.paged_decode_workspace(1, 3, 2, 64, DEV)
