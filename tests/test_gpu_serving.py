@@ -612,3 +612,17 @@ def test_decode_refuses_a_workspace_that_is_too_small(fos):
         fos.paged_decode(q, cache, *args, ws=torch.zeros(4096, device=DEV))
     with pytest.raises(ValueError):
         fos.paged_decode_workspace(1, 3, 2, 64, DEV)
+
+
+@pytest.mark.parametrize("m", [1, 3, 9, 33])
+def test_mx_wlinear_scale_ends(fos, m):
+    """The ends of E8M0's range: codes 0 (2^-127, below fp32's normal range) to 6, and
+    228 up to the largest whose products with E2M1 are finite."""
+    n, k = 64, 640
+    g = np.random.RandomState(m)
+    data = g.randint(0, 256, (n, k // 2)).astype(np.uint8)
+    for lo, hi, e in ((0, 7, 100), (228, 253, -100)):
+        scales = g.randint(lo, hi, (n, k // 32)).astype(np.uint8)
+        x = to_gpu_bf16(F.f32_to_bf16_bits(np.ldexp(g.randn(m, k), e).astype(np.float32)))
+        y = fos.mx_wlinear_fwd(x, fos.MXFP4Tensor(dev(data), dev(scales)), out_dtype=torch.float32)
+        check_linear(y, x, data, scales, None)
