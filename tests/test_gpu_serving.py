@@ -626,3 +626,15 @@ def test_mx_wlinear_scale_ends(fos, m):
         x = to_gpu_bf16(F.f32_to_bf16_bits(np.ldexp(g.randn(m, k), e).astype(np.float32)))
         y = fos.mx_wlinear_fwd(x, fos.MXFP4Tensor(dev(data), dev(scales)), out_dtype=torch.float32)
         check_linear(y, x, data, scales, None)
+
+
+@FMTS
+@pytest.mark.parametrize("short", [False, True])
+def test_decode_several_parts_per_sequence(fos, fmt, short):
+    """Batches whose sequences fall to a few workgroups each, of one length in steps or
+    with much shorter and empty ones between."""
+    g = np.random.RandomState(31)
+    lens = g.randint(1025, 1281, 20)
+    if short:
+        lens[[3, 7, 8, 19]] = 0, 1, 257, 40
+    run_decode(fos, fmt, 20, 8, 8, 128, 32, list(lens), seed=32)
