@@ -374,7 +374,9 @@ int64_t tiles_of(const WLinearArgs& a, const Shape& h);
 // not give two workgroups per CU (1 x 12288 x 4096: 8.0 us, a tile 8.6; 4 x 4096 x 12288: 9.3,
 // a tile 9.6; 4 x 12288 x 4096: 9.1, a tile 8.6).  Otherwise the tile that is done first, by
 // what one workgroup of each takes at K = 4096 (us, measured) times the rounds of 256
-// workgroups.
+// workgroups.  Eight waves on 32 activation rows take most of a CU's LDS: no other
+// workgroup runs beside them, so they are for one round (61 x 4099 x 4096: 10.2 us, four
+// waves 11.0; 24 x 8192 x 4096: 8.4 and 9.0; but two rounds, 64 x 16384 x 1024: 15.1 and 9.9).
 Shape shape_of(const WLinearArgs& a) {
   const bool wide = a.N >= 2 * 16 * kCUs;
   if (a.M <= (wide ? 2 : 4)) return Shape{1, 0, wide ? 4 : 8};
@@ -382,11 +384,14 @@ Shape shape_of(const WLinearArgs& a) {
     Shape shape;
     float us;
   } kTiles[] = {{{1, 1, 8}, 2.6f}, {{2, 1, 8}, 4.0f}, {{3, 1, 8}, 6.2f},
-                {{2, 2, 4}, 6.6f}, {{3, 2, 4}, 9.0f}, {{3, 4, 4}, 14.7f}};
+                {{2, 2, 8}, 6.2f}, {{2, 2, 4}, 6.6f}, {{3, 2, 8}, 8.5f},
+                {{3, 2, 4}, 9.0f}, {{3, 4, 4}, 14.7f}};
   Shape best = kTiles[0].shape;
   float least = INFINITY;
   for (const auto& c : kTiles) {
-    const float us = c.us * (float)((tiles_of(a, c.shape) + kCUs - 1) / kCUs);
+    const int64_t rounds = (tiles_of(a, c.shape) + kCUs - 1) / kCUs;
+    if (c.shape.mt == 2 && c.shape.kw == 8 && rounds > 1) continue;
+    const float us = c.us * (float)rounds;
     if (us < least) {
       least = us;
       best = c.shape;
@@ -428,9 +433,12 @@ int64_t wlinear_threads(const WLinearArgs& a) {
 
 hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s) {
   const Shape h = shape_of(a);
-  (void)(launch_quad_if<4>(a, h, s) || launch_quad_if<8>(a, h, s) || launch_if<1, 1, 8>(a, h, s) ||
-         launch_if<2, 1, 8>(a, h, s) || launch_if<3, 1, 8>(a, h, s) || launch_if<2, 2, 4>(a, h, s) ||
-         launch_if<3, 2, 4>(a, h, s) || launch_if<3, 4, 4>(a, h, s));
+  const bool launched =
+      launch_quad_if<4>(a, h, s) || launch_quad_if<8>(a, h, s) || launch_if<1, 1, 8>(a, h, s) ||
+      launch_if<2, 1, 8>(a, h, s) || launch_if<3, 1, 8>(a, h, s) || launch_if<2, 2, 8>(a, h, s) ||
+      launch_if<2, 2, 4>(a, h, s) || launch_if<3, 2, 8>(a, h, s) || launch_if<3, 2, 4>(a, h, s) ||
+      launch_if<3, 4, 4>(a, h, s);
+  if (!launched) return hipErrorInvalidConfiguration;
   return hipGetLastError();
 }
 

@@ -638,3 +638,18 @@ def test_decode_several_parts_per_sequence(fos, fmt, short):
     if short:
         lens[[3, 7, 8, 19]] = 0, 1, 257, 40
     run_decode(fos, fmt, 20, 8, 8, 128, 32, list(lens), seed=32)
+
+
+@pytest.mark.parametrize("m,n", [(2, 8200), (4, 300), (16, 2050), (9, 6000), (16, 8200), (250, 1000),
+                                 (17, 12300), (61, 4099), (33, 16400), (100, 6000)])
+@pytest.mark.parametrize("fmt,k", [("nvfp4", 1040), ("nvfp4", 2208), ("mxfp4", 2208)])
+def test_wlinear_many_weight_rows(fos, m, n, fmt, k):
+    """Sizes for which the GPU is filled with each of the tiles."""
+    data, scales, t, w = (nv_weight if fmt == "nvfp4" else mx_weight)(fos, n, k, m + n)
+    x = W.random_bf16(m, k, n, "normal").to(DEV)
+    run = fos.wlinear_fwd if fmt == "nvfp4" else fos.mx_wlinear_fwd
+    y = torch.full((m, n), float("nan"), dtype=torch.float32, device=DEV)
+    run(x, w, out_dtype=torch.float32, out=y)
+    rows = np.unique(np.concatenate([np.arange(0, n, 7), np.arange(max(0, n - 80), n)]))
+    check_linear(y, x, data, scales, t, rows=rows)
+    assert not y.isnan().any()
