@@ -324,8 +324,12 @@ struct Step<false, D> {
     const int row = 8 * (r >> 2) + 4 * u + (r & 3);
     const u32x4* l = reinterpret_cast<const u32x4*>(lds) + row * kUnits;
     f32x4 s = {0, 0, 0, 0};
+    u32x4 k[D / 32];                           // all on their way before the first product
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) s = mfma<false>(l[(4 * j + q) ^ key(row)], qf[j], s);
+    for (int j = 0; j < D / 32; ++j) k[j] = l[(4 * j + q) ^ key(row)];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) s = mfma<false>(k[j], qf[j], s);
     return s;
   }
   __device__ __forceinline__ void mask_v(uint8_t*, const uint32_t* seen, int) {
@@ -356,7 +360,7 @@ struct Step<false, D> {
 template <int D>
 struct Step<true, D> {
   using P = Pieces<D>;
-  static constexpr int kTokens = 64;
+  static constexpr int kTokens = 64, N = kTokens / 32;
   static constexpr int kRow = D / 2;                 // bytes of a row
   static constexpr int kUnits = D / 32;              // its 16-byte units, and those of a lane
   static constexpr int kBlocks = D / 16;             // its block scales
@@ -417,35 +421,74 @@ struct Step<true, D> {
     for (int i = 0; i < kBlocks; ++i)
       lds[kVS + i * kTokens + lane] = (uint8_t)(row[i / 2] >> (8 * (i % 2)));
   }
-  __device__ __forceinline__ f32x4 scores(const uint8_t* lds, const u32x4 (&qf)[D / 32], int n,
-                                          int u, int r, int q) const {
-    const int row = 32 * n + 8 * (r >> 2) + 4 * u + (r & 3);
+  // The operands of a step as they lie in LDS.  They are all read before the first product:
+  // left where they are used, every read is waited for, and with one or two waves on a SIMD
+  // little else runs meanwhile (24 x 12 heads x 1000 tokens of 96 values: 18.2 -> 17.0 us,
+  // 16 x 8 heads x 32768 of 128: 64.0 -> 61.7).
+  uint32_t kw[2 * N][D / 32], vw[N][P::count][8];
+  uint16_t ksc[2 * N][P::count];
+  u32x2 vsc[N][P::count];
+  // K of 16 tokens: operand rows r = tokens 8 (r / 4) + 4 u + r % 4 of the 32.
+  __device__ __forceinline__ void read_k(const uint8_t* lds, int n, int u, int r, int q) {
+    const int row = 32 * n + 8 * (r >> 2) + 4 * u + (r & 3), t = 2 * n + u;
     const uint8_t* l = lds + row * kRow;
     const uint8_t* sp = lds + kKS + row * kBlocks;
-    f32x4 s = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < P::count; ++i) {
       const int steps = P::size(i) / 32, j0 = P::at(i) / 32;
       // the lane's 4 * steps bytes of the piece: in unit j0 + steps q / 4
       const uint8_t* w = l + 16 * ((j0 + steps * q / 4) ^ key(row)) + (4 * steps * q) % 16;
-      uint32_t word[4];
-      f16x2 sc;
       if (steps == 4) {
         const u32x4 x = *reinterpret_cast<const u32x4*>(w);
-        word[0] = x.x; word[1] = x.y; word[2] = x.z; word[3] = x.w;
-        sc = scale_pair(*reinterpret_cast<const uint16_t*>(sp + 2 * j0 + 2 * q));
+        kw[t][j0] = x.x; kw[t][j0 + 1] = x.y; kw[t][j0 + 2] = x.z; kw[t][j0 + 3] = x.w;
+        ksc[t][i] = *reinterpret_cast<const uint16_t*>(sp + 2 * j0 + 2 * q);
       } else if (steps == 2) {
         const u32x2 x = *reinterpret_cast<const u32x2*>(w);
-        word[0] = x.x; word[1] = x.y;
-        sc = scale_pair(sp[2 * j0 + q]);
+        kw[t][j0] = x.x; kw[t][j0 + 1] = x.y;
+        ksc[t][i] = sp[2 * j0 + q];
       } else {
-        word[0] = *reinterpret_cast<const uint32_t*>(w);
-        sc = scale_pair(sp[2 * j0 + q / 2]);
+        kw[t][j0] = *reinterpret_cast<const uint32_t*>(w);
+        ksc[t][i] = sp[2 * j0 + q / 2];
       }
+    }
+  }
+  // V of the lane's 8 tokens of the 32.
+  __device__ __forceinline__ void read_v(const uint8_t* lds, int n, int r, int q) {
+    const int tok = 32 * n + 8 * q;                  // one key for the group's 8 rows
 #pragma unroll
-      for (int j = 0; j < steps; ++j) {
+    for (int i = 0; i < P::count; ++i) {
+      const int bytes = P::size(i) / 32;             // of the lane and token: 4, 2 or 1
+      const int b = P::at(i) / 2 + bytes * r;
+      const uint8_t* w = lds + kV + tok * kRow + 16 * ((b / 16) ^ key(tok)) + b % 16;
+      vsc[n][i] = *reinterpret_cast<const u32x2*>(lds + kVS + (b / 8) * kTokens + tok);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (bytes == 4) vw[n][i][e] = *reinterpret_cast<const uint32_t*>(w + e * kRow);
+        else if (bytes == 2) vw[n][i][e] = *reinterpret_cast<const uint16_t*>(w + e * kRow);
+        else vw[n][i][e] = w[e * kRow];
+      }
+    }
+  }
+  __device__ __forceinline__ void read_all(const uint8_t* lds, int r, int q) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) read_k(lds, n, u, r, q);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < N; ++n) read_v(lds, n, r, q);
+  }
+  __device__ __forceinline__ f32x4 scores(const uint8_t*, const u32x4 (&qf)[D / 32], int n, int u,
+                                          int, int) const {
+    f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < P::count; ++i) {
+      const f16x2 sc = scale_pair(ksc[2 * n + u][i]);
+#pragma unroll
+      for (int j = 0; j < P::size(i) / 32; ++j) {
         const _Float16 x = j >= 2 ? sc.y : sc.x;
-        s = mfma<true>(dequant8(word[j], f16x2{x, x}), qf[j0 + j], s);
+        const int at = P::at(i) / 32 + j;
+        s = mfma<true>(dequant8(kw[2 * n + u][at], f16x2{x, x}), qf[at], s);
       }
     }
     return s;
@@ -464,30 +507,17 @@ struct Step<true, D> {
   }
   // The nibbles of two tokens are brought together (four bit selects for eight
   // conversions), so that one conversion gives two tokens of one d.
-  __device__ __forceinline__ void accumulate(const uint8_t* lds, f32x4 (&o)[D / 16], int n,
-                                             const u32x4& hi, const u32x4&, int r, int q) const {
-    const int tok = 32 * n + 8 * q;                  // one key for the group's 8 rows
+  __device__ __forceinline__ void accumulate(const uint8_t*, f32x4 (&o)[D / 16], int n,
+                                             const u32x4& hi, const u32x4&, int, int) const {
 #pragma unroll
     for (int i = 0; i < P::count; ++i) {
       const int bytes = P::size(i) / 32;             // of the lane and token: 4, 2 or 1
-      const int b = P::at(i) / 2 + bytes * r;
-      const uint8_t* w = lds + kV + tok * kRow + 16 * ((b / 16) ^ key(tok)) + b % 16;
-      const u32x2 sb = *reinterpret_cast<const u32x2*>(lds + kVS + (b / 8) * kTokens + tok);
+      const u32x2 sb = vsc[n][i];
       uint32_t lo[4], up[4];
       f16x2 sc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        uint32_t x, y;
-        if (bytes == 4) {
-          x = *reinterpret_cast<const uint32_t*>(w + 2 * e * kRow);
-          y = *reinterpret_cast<const uint32_t*>(w + (2 * e + 1) * kRow);
-        } else if (bytes == 2) {
-          x = *reinterpret_cast<const uint16_t*>(w + 2 * e * kRow);
-          y = *reinterpret_cast<const uint16_t*>(w + (2 * e + 1) * kRow);
-        } else {
-          x = w[2 * e * kRow];
-          y = w[(2 * e + 1) * kRow];
-        }
+        const uint32_t x = vw[n][i][2 * e], y = vw[n][i][2 * e + 1];
         lo[e] = low_nibbles(x, y << 4);
         up[e] = low_nibbles(x >> 4, y);
         sc[e] = e & 1 ? scale_pair_hi(sb[e / 2]) : scale_pair(sb[e / 2]);
@@ -554,12 +584,14 @@ __device__ __forceinline__ void join_partials(const Plan& p, const float* all, i
   }
 }
 
-// Workgroups that a CU holds at once: what the registers of a step leave room for.
-template <bool kNVFP4, int D>
-constexpr int kPerCU = kNVFP4 ? (D <= 64 ? 3 : D <= 192 ? 2 : 1) : (D <= 64 ? 3 : D <= 128 ? 2 : 1);
+// Workgroups that a CU holds at once: what the registers of a step leave room for (two
+// with spills, NVFP4: 20.9 us instead of 18.4 at 8 x 4 heads x 8000 x 160, 34.4 instead of
+// 20.6 at 192).
+template <int D>
+constexpr int kPerCU = D <= 64 ? 3 : D <= 128 ? 2 : 1;
 
 template <bool kNVFP4, int D>
-__global__ __launch_bounds__(kThreads, (kPerCU<kNVFP4, D>)) void paged_decode_kernel(Plan p) {
+__global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan p) {
   constexpr int kSteps = D / 32;               // 32-value steps of the first product
   constexpr int kTiles = D / 16;               // 16-row tiles of the second
   constexpr int kPad = D + 4;
@@ -689,6 +721,11 @@ __global__ __launch_bounds__(kThreads, (kPerCU<kNVFP4, D>)) void paged_decode_ke
     }
     all = __all(all);
 
+    if (!all) {
+      asm volatile("");                        // a branch, not selects in every step
+      step.mask_v(mine, seen, lane);
+    }
+    if constexpr (kNVFP4) step.read_all(mine, r, q);
     float w[N][8];                             // scores, before cs
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -699,8 +736,7 @@ __global__ __launch_bounds__(kThreads, (kPerCU<kNVFP4, D>)) void paged_decode_ke
         for (int i = 0; i < 4; ++i) w[n][4 * u + i] = s[i];
       }
     if (!all) {
-      asm volatile("");                        // a branch, not selects in every step
-      step.mask_v(mine, seen, lane);
+      asm volatile("");
 #pragma unroll
       for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -816,7 +852,7 @@ __global__ __launch_bounds__(kThreads, (kPerCU<kNVFP4, D>)) void paged_decode_ke
 template <bool kNVFP4, int D>
 void launch(Plan& p, int64_t steps, hipStream_t s) {
   const int per = p.a.c.heads * p.groups;
-  p.runs = (int)max(min((int64_t)(kPerCU<kNVFP4, D> * kCUs / per), steps), (int64_t)1);
+  p.runs = (int)max(min((int64_t)(kPerCU<D> * kCUs / per), steps), (int64_t)1);
   paged_decode_kernel<kNVFP4, D><<<(uint32_t)(p.runs * per), kThreads, 0, s>>>(p);
 }
 template <bool kNVFP4>
