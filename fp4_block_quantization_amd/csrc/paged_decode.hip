@@ -21,12 +21,19 @@
 //
 // Split.  The steps (256 tokens) of all sequences form one list, and for every kv head
 // the workgroups that the GPU holds at once take equal runs of it: all start together and
-// all are done together, however ragged the lengths are.  The lengths are read on the
-// device; the host needs none.  Workgroups of the same run and neighbouring heads are
-// neighbours: they read the same pages at the same time.  A run covers parts of one or
-// more sequences.  A sequence that fell to several runs leaves partial (m, l, o) in the
-// workspace, and the last workgroup to finish joins them in their order: no second
-// launch, nobody waits, and the order of every sum depends on the lengths alone.
+// all are done together, however ragged the lengths are.  Where runs that end with their
+// sequence are hardly longer, these are taken.  The lengths are read on the device; the
+// host needs none.  Workgroups of the same run and neighbouring heads are neighbours: they
+// read the same pages at the same time.  A sequence that fell to several runs leaves partial
+// (m, l, o) in the workspace, and the last workgroup to finish joins them (of many, in two
+// levels) in their order: no second launch, nobody waits, and the order of every sum
+// depends on the lengths alone.
+//
+// Bound and figures (K and V bytes over the time of a launch).  bf16: memory; 32 sequences
+// of up to 8192 tokens, 32 heads over 8 of 128: 90 us, 6.0 TB/s of 6.8 that a plain read
+// reaches.  NVFP4: the loads and the conversions of their step share the time; 16 x up to
+// 32768 tokens, 64 heads over 8 of 128: 61 us, 5.0 TB/s (55 us with the arithmetic left
+// out).  Few tokens (1 x 200): 6 us, of which an empty launch is 2.
 #include "serving.hpp"
 
 namespace fos {
@@ -37,7 +44,6 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kHeads = 16;            // query heads per workgroup: columns of the products
 constexpr int kStepTokens = 64 * kWaves;   // a step of a workgroup
-constexpr int kMaxPerCU = 3;          // workgroups that a CU holds, at most
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -54,7 +60,9 @@ struct Plan {
   uint64_t page_magic;
   int runs;                // per head group
   uint32_t* arrived;       // per segment: workgroups done with it, 0 between launches
+  uint32_t* grouped;       // the same for a group of partials (below)
   float* parts;
+  float* group_parts;
 };
 
 // Partial results: (m, l)[rows], o[rows][dim].  Run i of a head group leaves the one of
@@ -542,45 +550,121 @@ struct Step<true, D> {
 
 constexpr float kSlack = 8.0f;    // see the rescaling below
 
-// Joins the `count` partials of a segment, in order, and writes its outputs: each thread
-// takes four values of a head, eight partials at a time.
+// Joining partials.  A thread takes four values of a head and reads kBatch partials at a
+// time; where that leaves threads idle, `split` of them share the partials of the same
+// values.  A segment of many partials is joined in two levels, by the last workgroup of
+// each group of `size` partials and by the last of the groups: what counts is how many
+// rounds of reads follow one another (1 x 41461 tokens, bf16, 2 kv heads of 192 values with
+// 16 query heads each: 50 us on one level, 32 on two; 2 x up to 27428, NVFP4, 1 head of 256:
+// 18.5 and 14.8, and 22.7 if threads do not share).  More partials at a time cost more where
+// there are two or three than they save elsewhere (24 x 12 heads x 1000 x 64: 12.8 us with
+// 4, 13.1 with 8).
+constexpr int kBatch = 4;
+struct Joining {
+  int split, size, groups;
+};
 template <int D>
-__device__ __forceinline__ void join_partials(const Plan& p, const float* all, int count, int rows,
-                                              int64_t hrow0, float vt0) {
-  constexpr int kBatch = 8;
+__device__ __forceinline__ Joining plan_joining(int rows, int count) {
+  const int items = rows * (D / 4);
+  Joining j;
+  const int most = items <= 32 ? 8 : items <= 64 ? 4 : items <= 128 ? 2 : 1;
+  j.split = 1;
+  while (j.split < most && kBatch * j.split < count) j.split *= 2;
+  const int unit = kBatch * j.split, passes = (items + kThreads - 1) / kThreads;
+  j.size = count;
+  j.groups = 1;
+  if (count > 2 * unit) {
+    int size = unit;
+    while (size * size < count) size *= 2;
+    const int groups = (int)((uint32_t)(count + size - 1) / (uint32_t)size);
+    const int one = (count + unit - 1) / unit;
+    const int two = (size + unit - 1) / unit + (groups + unit - 1) / unit;
+    if (passes * one > passes * two + 1) {
+      j.size = size;
+      j.groups = groups;
+    }
+  }
+  return j;
+}
+
+struct Joined {
+  float m, l;
+  f32x4 o;
+};
+// The sum of a and b with the common maximum.
+__device__ __forceinline__ void add(Joined& a, const Joined& b) {
+  const float m = fmaxf(a.m, b.m), ref = m == -INFINITY ? 0.0f : m;
+  const float fa = __builtin_amdgcn_exp2f(a.m - ref), fb = __builtin_amdgcn_exp2f(b.m - ref);
+  a.l = a.l * fa + b.l * fb;
+  a.o = a.o * fa + b.o * fb;
+  a.m = m;
+}
+
+// Joins `count` partials, in an order that depends on their number alone: into a partial
+// at `to`, or (null) into the outputs.  Called by the whole workgroup.
+template <int D>
+__device__ __forceinline__ void join_partials(const Plan& p, const float* all, int count, int split,
+                                              int rows, float* to, int64_t hrow0, float vt0,
+                                              Joined* scratch) {
   const int64_t step = part_stride(p);
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+  const int items = rows * (D / 4);
+  int tid = threadIdx.x;
+  asm("" : "+v"(tid));       // what depends on it is not to be kept through the steps
+  // partials sub, sub + split, .. of item i
+  auto gather = [&](int i, int sub) {
     const int g = i / (D / 4), d = 4 * (i % (D / 4));
-    float m = -INFINITY, l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-    for (int c = 0; c < count; c += kBatch) {
+    Joined r{-INFINITY, 0.0f, {0, 0, 0, 0}};
+    for (int c = sub; c < count; c += kBatch * split) {
       f32x2 ml[kBatch], x[kBatch], y[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float* part = all + min(c + k, count - 1) * step;
+        const float* part = all + min(c + k * split, count - 1) * step;
         ml[k] = load_shared(part + 2 * g);
         x[k] = load_shared(part + 2 * p.rows + g * D + d);
         y[k] = load_shared(part + 2 * p.rows + g * D + d + 2);
       }
-      float m2 = m;
+      float m = r.m;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) m2 = fmaxf(m2, ml[k].x);
-      const float m1 = m2 == -INFINITY ? 0.0f : m2;    // nothing seen so far: all weights 0
-      const float f = __builtin_amdgcn_exp2f(m - m1);
-      m = m2;
-      l *= f;
-      o *= f;
+      for (int k = 0; k < kBatch; ++k) m = fmaxf(m, ml[k].x);
+      const float ref = m == -INFINITY ? 0.0f : m;       // nothing seen so far: all weights 0
+      const float f = __builtin_amdgcn_exp2f(r.m - ref);
+      r.m = m;
+      r.l *= f;
+      r.o *= f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float w = c + k < count ? __builtin_amdgcn_exp2f(ml[k].x - m1) : 0.0f;
-        l += w * ml[k].y;
-        o += w * f32x4{x[k].x, x[k].y, y[k].x, y[k].y};
+        const float w = c + k * split < count ? __builtin_amdgcn_exp2f(ml[k].x - ref) : 0.0f;
+        r.l += w * ml[k].y;
+        r.o += w * f32x4{x[k].x, x[k].y, y[k].x, y[k].y};
       }
     }
-    const float n = l == 0.0f ? 0.0f : vt0 / l;      // a NaN sum stays one
+    return r;
+  };
+  auto finish = [&](int i, const Joined& r) {
+    const int g = i / (D / 4), d = 4 * (i % (D / 4));
+    if (to) {
+      store_shared(to + 2 * p.rows + g * D + d, f32x2{r.o[0], r.o[1]});
+      store_shared(to + 2 * p.rows + g * D + d + 2, f32x2{r.o[2], r.o[3]});
+      if (d == 0) store_shared(to + 2 * g, f32x2{r.m, r.l});
+      return;
+    }
+    const float n = r.l == 0.0f ? 0.0f : vt0 / r.l;      // a NaN sum stays one
     *reinterpret_cast<u32x2*>(p.a.out + (hrow0 + g) * D + d) =
-        u32x2{pack_bf16x2(o[0] * n, o[1] * n), pack_bf16x2(o[2] * n, o[3] * n)};
-    if (d == 0 && p.a.lse) p.a.lse[hrow0 + g] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        u32x2{pack_bf16x2(r.o[0] * n, r.o[1] * n), pack_bf16x2(r.o[2] * n, r.o[3] * n)};
+    if (d == 0 && p.a.lse)
+      p.a.lse[hrow0 + g] = r.l == 0.0f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
+  };
+  if (split == 1) {
+    for (int i = tid; i < items; i += kThreads) finish(i, gather(i, 0));
+  } else {
+    const int sub = tid / items;
+    if (sub < split) scratch[tid] = gather(tid - sub * items, sub);
+    __syncthreads();
+    if (tid < items) {
+      Joined r = scratch[tid];
+      for (int s = 1; s < split; ++s) add(r, scratch[tid + s * items]);
+      finish(tid, r);
+    }
   }
 }
 
@@ -810,7 +894,9 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
   float* parts = p.parts + ((int64_t)hg * (p.runs + a.B) + run.b) * part_stride(p);
   float* part = parts + (int64_t)(blockIdx.x / per) * part_stride(p);
   const int64_t hrow0 = (int64_t)run.b * a.Hq + head * a.G + g0;
-  for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
+  int tid = threadIdx.x;
+  asm("" : "+v"(tid));       // what depends on it is not to be kept through the steps
+  for (int i = tid; i < rows * (D / 2); i += kThreads) {
     const int g = i / (D / 2), d = 2 * (i % (D / 2));
     float mm = sm[0][g];
 #pragma unroll
@@ -838,10 +924,30 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
       first = scalar((uint32_t)run.at / (uint32_t)run.share);
       count = scalar((uint32_t)(run.at + run.steps - 1) / (uint32_t)run.share) - first + 1;
     }
+    const Joining j = plan_joining<D>(rows, count);
+    const float* src = parts + first * part_stride(p);
     uint32_t* arrived = p.arrived + (int64_t)run.b * per + hg;
-    if (last_to_finish(arrived, count, before_me)) {
-      join_partials<D>(p, parts + first * part_stride(p), count, rows, hrow0, vt0);
-      reset_counter(arrived);
+    uint32_t* counter = arrived;
+    float* to = nullptr;
+    int n = count;
+    // Group k has counter and result first + 1 + k of the head group's runs: there are
+    // fewer groups than runs between the first and the last, which are this sequence's.
+    const int at = hg * p.runs + first + 1;
+    if (j.groups > 1) {
+      const int k = scalar((uint32_t)(blockIdx.x / per - first) / (uint32_t)j.size);
+      n = min(j.size, count - k * j.size);
+      src += k * j.size * part_stride(p);
+      to = p.group_parts + (at + k) * part_stride(p);
+      counter = p.grouped + at + k;
+    }
+    while (last_to_finish(counter, n, before_me)) {
+      join_partials<D>(p, src, n, j.split, rows, to, hrow0, vt0, reinterpret_cast<Joined*>(lds));
+      reset_counter(counter);
+      if (!to) break;
+      n = j.groups;
+      src = p.group_parts + at * part_stride(p);
+      to = nullptr;
+      counter = arrived;
     }
   }
   run.pos += steps;
@@ -853,6 +959,7 @@ template <bool kNVFP4, int D>
 void launch(Plan& p, int64_t steps, hipStream_t s) {
   const int per = p.a.c.heads * p.groups;
   p.runs = (int)max(min((int64_t)(kPerCU<D> * kCUs / per), steps), (int64_t)1);
+  p.group_parts = p.parts + (int64_t)per * (p.runs + p.a.B) * p.rows * (D + 2);
   paged_decode_kernel<kNVFP4, D><<<(uint32_t)(p.runs * per), kThreads, 0, s>>>(p);
 }
 template <bool kNVFP4>
@@ -881,8 +988,8 @@ bool decode_heads_ok(int64_t Hq, int64_t heads) { return segments_of(Hq, heads) 
 
 size_t decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim) {
   const int64_t G = Hq / heads, per = segments_of(Hq, heads);
-  const int64_t runs = max(kMaxPerCU * kCUs / per, (int64_t)1);
-  const int64_t parts = (runs + launch_seqs(B, per)) * per;
+  const int64_t runs = max(kMaxResident / per, (int64_t)1);
+  const int64_t parts = (runs + launch_seqs(B, per)) * per + runs * per;
   return kCounterBytes +
          sizeof(float) * (size_t)(parts * (G < kHeads ? G : kHeads) * (dim + 2));
 }
@@ -896,6 +1003,7 @@ hipError_t launch_paged_decode(const DecodeArgs& args, hipStream_t s) {
   const uint64_t d = a.c.page_size / 8;
   p.page_magic = (((uint64_t)1 << 36) + d - 1) / d;
   p.arrived = static_cast<uint32_t*>(a.ws);
+  p.grouped = p.arrived + kCounters;
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounterBytes);
   const int64_t per = (int64_t)a.c.heads * p.groups, B = args.B, seqs = launch_seqs(B, per);
   for (int64_t b = 0; b < B; b += seqs) {

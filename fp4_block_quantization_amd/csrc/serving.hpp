@@ -13,9 +13,12 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kCUs = 256;
 
 // The workspace of the attention starts with counters of finished workgroups, 0 between
-// launches; what is behind them is scratch.
+// launches; what is behind them is scratch.  One counter for each segment (a sequence and
+// up to 16 query heads of a kv head), then one for each workgroup that runs at once.
 constexpr int kCounters = 65536;
-constexpr size_t kCounterBytes = sizeof(uint32_t) * kCounters;
+constexpr int kMaxPerCU = 3;
+constexpr int kMaxResident = kMaxPerCU * kCUs;
+constexpr size_t kCounterBytes = sizeof(uint32_t) * (kCounters + kMaxResident);
 
 // Partial results pass from one workgroup to another on any XCD, each with an L2 of its
 // own.  A release and an acquire fence at that scope write back and invalidate a whole L2

@@ -480,7 +480,7 @@ size_t fos_paged_decode_workspace_bytes(int64_t num_seqs, int64_t num_q_heads,
                                         int64_t num_kv_heads, int64_t head_dim);
 
 /* Bytes at the start of that workspace that must be 0 when a workspace is first used
- * (262144; counters of finished workgroups).  Every call leaves them 0, so one clearing
+ * (265216; counters of finished workgroups).  Every call leaves them 0, so one clearing
  * serves all later calls of any sizes, also replayed from a graph. */
 size_t fos_paged_decode_counter_bytes(void);
 

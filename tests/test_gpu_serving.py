@@ -653,3 +653,13 @@ def test_wlinear_many_weight_rows(fos, m, n, fmt, k):
     rows = np.unique(np.concatenate([np.arange(0, n, 7), np.arange(max(0, n - 80), n)]))
     check_linear(y, x, data, scales, t, rows=rows)
     assert not y.isnan().any()
+
+
+@FMTS
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [
+    (2, 1, 256, [27000]), (16, 1, 192, [9000]), (16, 2, 96, [300, 11000, 2]), (1, 1, 32, [40000, 0, 39000]),
+    (4, 1, 64, [5000, 5000, 9, 12345]), (35, 5, 128, [14000, 1000])])
+def test_decode_many_partial_results(fos, fmt, Hq, Hkv, D, lens):
+    """Few heads and long sequences: a hundred workgroups and more leave parts of one
+    output, next to sequences that fall to one."""
+    run_decode(fos, fmt, len(lens), Hq, Hkv, D, 64, lens, seed=41, garbage=False)
