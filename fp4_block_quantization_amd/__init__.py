@@ -7,7 +7,8 @@ inputs.  Tensor-level entry points (quantize, dequantize, qlinear_fwd, ...) are
 re-exported lazily from ``fos``.
 """
 _EXPORTS = ("quantize", "dequantize", "qlinear_fwd", "tensor_scale", "NVFP4Tensor", "FosError",
-            "make_config")
+            "make_config", "wlinear_fwd", "mx_wlinear_fwd", "PagedKVCache", "kv_cache", "kv_append",
+           "kv_gather", "paged_decode", "paged_decode_workspace")
 
 
 def __getattr__(name):
