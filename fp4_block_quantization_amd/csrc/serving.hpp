@@ -22,9 +22,9 @@ constexpr size_t kCounterBytes = sizeof(uint32_t) * (kCounters + kMaxResident);
 
 // Partial results pass from one workgroup to another on any XCD, each with an L2 of its
 // own.  A release and an acquire fence at that scope write back and invalidate a whole L2
-// (paged attention of 32 sequences of up to 8192 tokens: 262 us instead of 89); instead the few values
-// that are passed are themselves accessed at device scope, as relaxed atomics of 8 bytes:
-// the stores write through to memory and the loads read from there.  What orders them is
+// (paged attention of 32 sequences of up to 8192 tokens: 262 us instead of 89); instead the
+// few values that are passed are themselves accessed at device scope, as relaxed atomics of
+// 8 bytes: the stores write through to memory and the loads read from there.  What orders them is
 // that every thread waits until its stores are done (wait_stores), then the barrier, and
 // only then one thread counts the workgroup: who reads the full count reads after all
 // the stores.

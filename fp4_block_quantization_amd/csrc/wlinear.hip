@@ -1,12 +1,16 @@
 // Weight-only quantized linear layer: bf16 activations times a 4-bit weight record,
 //   y[m][n] = t * sum_k x[m][k] E(w[n][k]) D(s[n][k / block]) + bias[n].
 // The weight is read once; its bytes bound the call (x and y are small beside it).
+// Measured, a launch included (1.8 us when empty), where a plain read of the weight takes
+// 5.5 us: 1 x 12288 x 4096 NVFP4 8.0 us, 16 x 12288 x 4096 9.0 us.  With more rows the
+// conversions and the passage through LDS bound it: 61 x 4099 x 4112 12.3 us, 64 x 12288 x
+// 4096 17 us.
 //
 // Matrix form: E2M1 x E4M3 has at most 6 significant bits and E2M1 x 2^e two, so weights
 // are exact in bf16, products are exact in fp32, and every sum is fp32; y is rounded once.
-// Two kernels, by the number of activation rows: up to 4 on 4x4x4 products, where a lane
-// keeps a weight row to itself, and more on 16x16x32 tiles, where a weight is converted
-// once for up to 64 activation rows.
+// Two kernels, by the number of activation rows (shape_of): few on 4x4x4 products, where a
+// lane keeps a weight row to itself, and more on 16x16x32 tiles, where a weight is
+// converted once for up to 64 activation rows.
 #include "serving.hpp"
 
 namespace fos {

@@ -402,10 +402,9 @@ fos_status fos_mx_qlinear_fwd(const uint8_t* a_data, const uint8_t* a_scales,
  *   Y[m][n] = RN( t_w * sum_k X[m][k] * (E*D)_w[n][k] + bias[n] )
  * with exact products, fp32 sums (in an unspecified order that is the same for every
  * call of the same shape), and one rounding to the output type.  Made for few rows
- * (M = 1 is a token of one sequence; up to 64 rows share one pass over the weight);
- * any M is accepted.  2D records work (they carry one scale per 16 values too); a
- * record made with the Hadamard transform needs an activation that carries the same
- * transform.
+ * (M = 1 is a token of one sequence, 64 a large batch); any M is accepted.  2D records
+ * work (they carry one scale per 16 values too); a record made with the Hadamard
+ * transform needs an activation that carries the same transform.
  *   X: bf16, row m at x_bf16 + m * x_stride elements, 16-byte aligned, x_stride >= K
  *   and a multiple of 8 (both for M > 1).  w_data [N][K/2] 16-byte aligned, w_scales
  *   [N][K/16] 4-byte aligned.  bias_bf16 [N] or NULL.  y [M][N] of out_dtype
