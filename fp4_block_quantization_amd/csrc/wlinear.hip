@@ -2,7 +2,7 @@
 //   y[m][n] = t * sum_k x[m][k] E(w[n][k]) D(s[n][k / block]) + bias[n].
 // The weight is read once; its bytes bound the call (x and y are small beside it).
 // Measured, a launch included (1.8 us when empty), where a plain read of the weight takes
-// 5.5 us: 1 x 12288 x 4096 NVFP4 8.0 us, 16 x 12288 x 4096 9.0 us.  With more rows the
+// 5.5 us: 1 x 12288 x 4096 NVFP4 8.0 us, 16 x 12288 x 4096 9.0 us; 1 x 256 x 256 2.8 us.  With more rows the
 // conversions and the passage through LDS bound it: 61 x 4099 x 4112 12.3 us, 64 x 12288 x
 // 4096 17 us.
 //
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
   }
 }
 
-// ---- few activation rows: M <= 4 ---------------------------------------------------
+// ---- few activation rows, or few weight rows --------------------------------------
 // On the 4x4x4 instruction, 16 independent 4x4 products: a quad of lanes takes four weight
 // rows (its columns) over the same 32 values of the inner dimension and four activation
 // rows.  Each lane keeps the sums of its own weight row, so a block's scale multiplies the
@@ -227,8 +227,8 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
 // instruction per weight for up to four activation rows (a 16x16 tile takes two for any
 // number, and its operands cross lanes).
 //
-// A wave takes 16 weight rows (four to a lane) and walks the inner dimension 512 values
-// at a time; the waves of a workgroup share its rows and split the inner dimension.  The
+// A wave takes 4 R weight rows (R to a lane) and walks the inner dimension 512 values at a
+// time; the waves of a workgroup share its rows and split the inner dimension.  The
 // activation comes in memory order and goes through the wave's own LDS.
 constexpr int kQuadStep = 512;
 
@@ -242,19 +242,24 @@ __device__ __forceinline__ float sum_over_quads(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// kEven: scale rows start at even bytes (K % 32 == 0),
-// so that a lane's two NVFP4 scales are one aligned load.
-template <bool kMX, bool kEven, int KW>
-__global__ __launch_bounds__(64 * KW, 3) void wlinear_quad_kernel(WLinearArgs a) {
+// kEven: scale rows start at even bytes (K % 32 == 0), so that a lane's two NVFP4 scales
+// are one aligned load.  kMany: more than four activation rows, blockIdx.y counts the fours
+// (apart, because what it takes in registers costs two rows a lane their fourth wave on a
+// SIMD: 9.2 us instead of 7.8 at 1 x 4096 x 12288).
+template <bool kMX, bool kEven, int R, int KW, bool kMany>
+__global__ __launch_bounds__(64 * KW, R == 2 && !kMany ? 4 : 3) void wlinear_quad_kernel(WLinearArgs a) {
   constexpr int kBlock = kMX ? 32 : 16;
-  constexpr int R = 4;                  // weight rows of a lane
-  constexpr int U = 2;                  // steps in flight
+  constexpr int kRows = 4 * R;
+  constexpr int U = R == 1 ? 4 : 2;     // steps in flight
   typedef short s16x4 __attribute__((ext_vector_type(4)));
   __shared__ u32x4 xs[KW][4][64];
-  __shared__ float sums[KW][16][4];
+  __shared__ float sums[KW][kRows][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 3, g = lane >> 2;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int M = (int)a.M, K = (int)a.K, steps = (K + kQuadStep - 1) / kQuadStep;
+  const int64_t n0 = (int64_t)blockIdx.x * kRows;
+  const int m0 = kMany ? 4 * (int)blockIdx.y : 0;
+  const uint16_t* xp = a.x + m0 * a.x_stride;
+  const int M = min((int)a.M - m0, 4);
+  const int K = (int)a.K, steps = (K + kQuadStep - 1) / kQuadStep;
   const float t = kMX ? 1.0f : a.wt[0];
   const uint8_t* wp[R];
   const uint8_t* sp[R];
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(64 * KW, 3) void wlinear_quad_kernel(WLinearArgs a)
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m)
-        if (m < M) xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + s * kQuadStep)[lane];
+        if (m < M) xr[m] = reinterpret_cast<const u32x4*>(xp + m * a.x_stride + s * kQuadStep)[lane];
     } else {
       // past K everything is zero (K % 16 == 0: a lane may hold half of its 32 weights)
       const bool half = 32 * g + 16 <= left, full = 32 * g + 32 <= left;
@@ -330,7 +335,7 @@ __global__ __launch_bounds__(64 * KW, 3) void wlinear_quad_kernel(WLinearArgs a)
       for (int m = 0; m < 4; ++m) {
         xr[m] = u32x4{0, 0, 0, 0};
         if (m < M && 8 * lane < left)
-          xr[m] = reinterpret_cast<const u32x4*>(a.x + m * a.x_stride + s * kQuadStep)[lane];
+          xr[m] = reinterpret_cast<const u32x4*>(xp + m * a.x_stride + s * kQuadStep)[lane];
       }
     }
   };
@@ -353,37 +358,47 @@ __global__ __launch_bounds__(64 * KW, 3) void wlinear_quad_kernel(WLinearArgs a)
       if (g == 0) sums[wave][4 * j + i][c] = v;
     }
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * M; e += 64 * KW) {
-    const int n = e & 15, m = e >> 4;
+  for (int e = threadIdx.x; e < kRows * M; e += 64 * KW) {
+    const int n = e % kRows, m = e / kRows;
     if (n0 + n >= a.N) continue;
     float v = sums[0][n][m];
 #pragma unroll
     for (int w = 1; w < KW; ++w) v += sums[w][n][m];
     v *= t;
     if (a.bias) v += bf16_lo(a.bias[n0 + n]);
-    const int64_t at = m * a.N + n0 + n;
+    const int64_t at = (int64_t)(m0 + m) * a.N + n0 + n;
     if (a.f32_out) static_cast<float*>(a.y)[at] = v;
     else static_cast<uint16_t*>(a.y)[at] = (uint16_t)pack_bf16x2(v, v);
   }
 }
 
 // Kernel and tile for a shape: 16 NT weight rows by 16 MT activation rows (MT 0: the quad
-// kernel), KW waves.
+// kernel with R = NT), KW waves.
 struct Shape {
   int nt, mt, kw;
 };
 int64_t tiles_of(const WLinearArgs& a, const Shape& h);
 
-// The quad kernel for up to 2 activation rows, and up to 4 where the weight rows alone do
-// not give two workgroups per CU (1 x 12288 x 4096: 8.0 us, a tile 8.6; 4 x 4096 x 12288: 9.3,
-// a tile 9.6; 4 x 12288 x 4096: 9.1, a tile 8.6).  Otherwise the tile that is done first, by
-// what one workgroup of each takes at K = 4096 (us, measured) times the rounds of 256
-// workgroups.  Eight waves on 32 activation rows take most of a CU's LDS: no other
-// workgroup runs beside them, so they are for one round (61 x 4099 x 4096: 10.2 us, four
-// waves 11.0; 24 x 8192 x 4096: 8.4 and 9.0; but two rounds, 64 x 16384 x 1024: 15.1 and 9.9).
+// The quad kernel wherever its workgroups of 4 or 8 weight rows by 4 activation rows fit on
+// the GPU one to a CU: fewer rows a lane are more workgroups, each with a shorter chain (1 x
+// 256 x 256: 2.8 us, with 16 weight rows 3.7; 1 x 1024 x 8192: 4.0 and 6.3; 3 x 1073 x 11344: 6.3
+// and 8.9; 16 x 256 x 8192: 4.1, a tile 6.9; but two to a CU, 16 x 1024 x 4096: 6.5, a tile
+// 4.9).  Then for up to 4 activation rows, or 2 where the weight rows alone give two tiles
+// per CU (4 x 4096 x 12288: 9.3, a tile 9.6; 4 x 12288 x 4096: 9.1, a tile 8.5); one
+// activation row is little enough to be read by twice the workgroups (1 x 4096 x 12288: 7.8
+// with 8 weight rows, 8.2 with 16; 2 x 4096 x 12288: 9.2 and 8.5).
+//
+// Otherwise the tile that is done first, by what one workgroup of each takes at K = 4096 (us,
+// measured) times the rounds of 256 workgroups.  Eight waves on 32 activation rows take most
+// of a CU's LDS: no other workgroup runs beside them, so they are for one round (61 x 4099 x
+// 4096: 10.2 us, four waves 11.0; 24 x 8192 x 4096: 8.4 and 9.0; but two rounds, 64 x 16384 x
+// 1024: 15.1 and 9.9).
 Shape shape_of(const WLinearArgs& a) {
+  const Shape few[] = {{1, 0, 8}, {2, 0, 8}};
+  for (const Shape& h : few)
+    if (tiles_of(a, h) <= kCUs) return h;
   const bool wide = a.N >= 2 * 16 * kCUs;
-  if (a.M <= (wide ? 2 : 4)) return Shape{1, 0, wide ? 4 : 8};
+  if (a.M <= (wide ? 2 : 4)) return wide ? Shape{4, 0, 4} : Shape{a.M == 1 ? 2 : 4, 0, 8};
   constexpr struct {
     Shape shape;
     float us;
@@ -404,7 +419,7 @@ Shape shape_of(const WLinearArgs& a) {
   return best;
 }
 int64_t tiles_of(const WLinearArgs& a, const Shape& h) {
-  if (h.mt == 0) return (a.N + 15) / 16;
+  if (h.mt == 0) return ((a.N + 4 * h.nt - 1) / (4 * h.nt)) * ((a.M + 3) / 4);
   return ((a.N + 16 * h.nt - 1) / (16 * h.nt)) * ((a.M + 16 * h.mt - 1) / (16 * h.mt));
 }
 
@@ -418,13 +433,13 @@ bool launch_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
   return true;
 }
 
-template <int KW>
+template <int R, int KW, bool kMany>
 bool launch_quad_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
-  if (h.mt != 0 || h.kw != KW) return false;
-  const uint32_t grid = (uint32_t)tiles_of(a, h);
-  if (a.mx) wlinear_quad_kernel<true, true, KW><<<grid, 64 * KW, 0, s>>>(a);
-  else if (a.K % 32 == 0) wlinear_quad_kernel<false, true, KW><<<grid, 64 * KW, 0, s>>>(a);
-  else wlinear_quad_kernel<false, false, KW><<<grid, 64 * KW, 0, s>>>(a);
+  if (h.nt != R || h.mt != 0 || h.kw != KW || (a.M > 4) != kMany) return false;
+  const dim3 grid((uint32_t)((a.N + 4 * R - 1) / (4 * R)), (uint32_t)((a.M + 3) / 4));
+  if (a.mx) wlinear_quad_kernel<true, true, R, KW, kMany><<<grid, 64 * KW, 0, s>>>(a);
+  else if (a.K % 32 == 0) wlinear_quad_kernel<false, true, R, KW, kMany><<<grid, 64 * KW, 0, s>>>(a);
+  else wlinear_quad_kernel<false, false, R, KW, kMany><<<grid, 64 * KW, 0, s>>>(a);
   return true;
 }
 
@@ -438,7 +453,10 @@ int64_t wlinear_threads(const WLinearArgs& a) {
 hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s) {
   const Shape h = shape_of(a);
   const bool launched =
-      launch_quad_if<4>(a, h, s) || launch_quad_if<8>(a, h, s) || launch_if<1, 1, 8>(a, h, s) ||
+      launch_quad_if<1, 8, false>(a, h, s) || launch_quad_if<2, 8, false>(a, h, s) ||
+      launch_quad_if<4, 8, false>(a, h, s) || launch_quad_if<4, 4, false>(a, h, s) ||
+      launch_quad_if<1, 8, true>(a, h, s) || launch_quad_if<2, 8, true>(a, h, s) ||
+      launch_if<1, 1, 8>(a, h, s) ||
       launch_if<2, 1, 8>(a, h, s) || launch_if<3, 1, 8>(a, h, s) || launch_if<2, 2, 8>(a, h, s) ||
       launch_if<2, 2, 4>(a, h, s) || launch_if<3, 2, 8>(a, h, s) || launch_if<3, 2, 4>(a, h, s) ||
       launch_if<3, 4, 4>(a, h, s);

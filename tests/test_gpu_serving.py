@@ -663,3 +663,17 @@ def test_decode_many_partial_results(fos, fmt, Hq, Hkv, D, lens):
     """Few heads and long sequences: a hundred workgroups and more leave parts of one
     output, next to sequences that fall to one."""
     run_decode(fos, fmt, len(lens), Hq, Hkv, D, 64, lens, seed=41, garbage=False)
+
+
+@pytest.mark.parametrize("m,n", [(1, 1), (3, 1023), (4, 1025), (1, 2051), (3, 4099), (5, 7), (6, 510),
+                                 (7, 1000), (13, 255), (16, 256), (33, 111), (64, 61), (90, 40)])
+@pytest.mark.parametrize("fmt,k", [("nvfp4", 16), ("nvfp4", 528), ("nvfp4", 4640), ("mxfp4", 96), ("mxfp4", 2592)])
+def test_wlinear_few_weight_rows(fos, m, n, fmt, k):
+    """Few weight rows, where each workgroup takes few of them and groups of activation
+    rows share them."""
+    data, scales, t, w = (nv_weight if fmt == "nvfp4" else mx_weight)(fos, n, k, m + n)
+    wide = W.random_bf16(m, k + 24, n, "normal").to(DEV)
+    x = wide[:, 8:8 + k]
+    bias = W.random_bf16(1, n, 3, "normal")[0].to(DEV) if n % 2 else None
+    run = fos.wlinear_fwd if fmt == "nvfp4" else fos.mx_wlinear_fwd
+    check_linear(run(x, w, bias=bias, out_dtype=torch.float32), x, data, scales, t, bias)
