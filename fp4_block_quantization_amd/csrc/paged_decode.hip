@@ -65,11 +65,14 @@ struct Plan {
   float* group_parts;
 };
 
-// Partial results: (m, l)[rows], o[rows][dim].  Run i of a head group leaves the one of
-// sequence b at i + b: along the list one of the two grows from each to the next, so the
-// places are distinct, and those of a sequence lie in a row.
+// Partial results: o[rows][dim], (m, l)[rows], padded to 16 bytes.  Run i of a head group
+// leaves the one of sequence b at i + b: along the list one of the two grows from each to
+// the next, so the places are distinct, and those of a sequence lie in a row.
+__host__ __device__ constexpr int64_t part_floats(int rows, int dim) {
+  return (int64_t)rows * dim + ((2 * rows + 3) & ~3);
+}
 __device__ __forceinline__ int64_t part_stride(const Plan& p) {
-  return (int64_t)p.rows * (p.a.c.dim + 2);
+  return part_floats(p.rows, p.a.c.dim);
 }
 
 // ---- chunks ----------------------------------------------------------------------
@@ -606,7 +609,8 @@ template <int D>
 __device__ __forceinline__ void join_partials(const Plan& p, const float* all, int count, int split,
                                               int rows, float* to, int64_t hrow0, float vt0,
                                               Joined* scratch) {
-  const int64_t step = part_stride(p);
+  const int step = 4 * (int)part_stride(p);      // bytes; all of a segment are below 2^24
+  const __amdgpu_buffer_rsrc_t parts = shared_floats(all, count * step);
   const int items = rows * (D / 4);
   int tid = threadIdx.x;
   asm("" : "+v"(tid));       // what depends on it is not to be kept through the steps
@@ -615,13 +619,13 @@ __device__ __forceinline__ void join_partials(const Plan& p, const float* all, i
     const int g = i / (D / 4), d = 4 * (i % (D / 4));
     Joined r{-INFINITY, 0.0f, {0, 0, 0, 0}};
     for (int c = sub; c < count; c += kBatch * split) {
-      f32x2 ml[kBatch], x[kBatch], y[kBatch];
+      f32x2 ml[kBatch];
+      f32x4 x[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float* part = all + min(c + k * split, count - 1) * step;
-        ml[k] = load_shared(part + 2 * g);
-        x[k] = load_shared(part + 2 * p.rows + g * D + d);
-        y[k] = load_shared(part + 2 * p.rows + g * D + d + 2);
+        const int at = min(c + k * split, count - 1) * step;
+        ml[k] = load_shared2(parts, at + 4 * (p.rows * D + 2 * g));
+        x[k] = load_shared4(parts, at + 4 * (g * D + d));
       }
       float m = r.m;
 #pragma unroll
@@ -635,7 +639,7 @@ __device__ __forceinline__ void join_partials(const Plan& p, const float* all, i
       for (int k = 0; k < kBatch; ++k) {
         const float w = c + k * split < count ? __builtin_amdgcn_exp2f(ml[k].x - ref) : 0.0f;
         r.l += w * ml[k].y;
-        r.o += w * f32x4{x[k].x, x[k].y, y[k].x, y[k].y};
+        r.o += w * x[k];
       }
     }
     return r;
@@ -643,9 +647,9 @@ __device__ __forceinline__ void join_partials(const Plan& p, const float* all, i
   auto finish = [&](int i, const Joined& r) {
     const int g = i / (D / 4), d = 4 * (i % (D / 4));
     if (to) {
-      store_shared(to + 2 * p.rows + g * D + d, f32x2{r.o[0], r.o[1]});
-      store_shared(to + 2 * p.rows + g * D + d + 2, f32x2{r.o[2], r.o[3]});
-      if (d == 0) store_shared(to + 2 * g, f32x2{r.m, r.l});
+      store_shared(to + g * D + d, f32x2{r.o[0], r.o[1]});
+      store_shared(to + g * D + d + 2, f32x2{r.o[2], r.o[3]});
+      if (d == 0) store_shared(to + p.rows * D + 2 * g, f32x2{r.m, r.l});
       return;
     }
     const float n = r.l == 0.0f ? 0.0f : vt0 / r.l;      // a NaN sum stays one
@@ -914,8 +918,8 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
       *reinterpret_cast<uint32_t*>(a.out + (hrow0 + g) * D + d) = pack_bf16x2(x * n, y * n);
       if (d == 0 && a.lse) a.lse[hrow0 + g] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     } else {
-      store_shared(part + 2 * p.rows + g * D + d, f32x2{x, y});
-      if (d == 0) store_shared(part + 2 * g, f32x2{mm, ll});
+      store_shared(part + g * D + d, f32x2{x, y});
+      if (d == 0) store_shared(part + p.rows * D + 2 * g, f32x2{mm, ll});
     }
   }
   if (!whole) {
@@ -959,7 +963,7 @@ template <bool kNVFP4, int D>
 void launch(Plan& p, int64_t steps, hipStream_t s) {
   const int per = p.a.c.heads * p.groups;
   p.runs = (int)max(min((int64_t)(kPerCU<D> * kCUs / per), steps), (int64_t)1);
-  p.group_parts = p.parts + (int64_t)per * (p.runs + p.a.B) * p.rows * (D + 2);
+  p.group_parts = p.parts + (int64_t)per * (p.runs + p.a.B) * part_floats(p.rows, D);
   paged_decode_kernel<kNVFP4, D><<<(uint32_t)(p.runs * per), kThreads, 0, s>>>(p);
 }
 template <bool kNVFP4>
@@ -991,7 +995,7 @@ size_t decode_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t dim)
   const int64_t runs = max(kMaxResident / per, (int64_t)1);
   const int64_t parts = (runs + launch_seqs(B, per)) * per + runs * per;
   return kCounterBytes +
-         sizeof(float) * (size_t)(parts * (G < kHeads ? G : kHeads) * (dim + 2));
+         sizeof(float) * (size_t)(parts * part_floats(G < kHeads ? (int)G : kHeads, (int)dim));
 }
 
 hipError_t launch_paged_decode(const DecodeArgs& args, hipStream_t s) {

@@ -32,9 +32,17 @@ __device__ __forceinline__ void store_shared(float* p, f32x2 v) {
   __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v),
                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ f32x2 load_shared(const float* p) {
-  return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p),
-                                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+// The loads go to memory too (the cache policy of device scope), 8 or 16 bytes at a byte
+// offset of `bytes` bytes at p; offsets behind them read zeros.
+constexpr int kDeviceScope = 16;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_floats(const float* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), 0, bytes, 0x27000);
+}
+__device__ __forceinline__ f32x2 load_shared2(__amdgpu_buffer_rsrc_t r, int offset) {
+  return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, kDeviceScope));
+}
+__device__ __forceinline__ f32x4 load_shared4(__amdgpu_buffer_rsrc_t r, int offset) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, kDeviceScope));
 }
 __device__ __forceinline__ void wait_stores() {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
