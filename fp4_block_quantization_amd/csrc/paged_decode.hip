@@ -578,7 +578,7 @@ __device__ __forceinline__ Joining plan_joining(int rows, int count) {
   j.groups = 1;
   if (count > 2 * unit) {
     int size = unit;
-    while (size * size < count) size *= 2;
+    while (2 * size * size < count) size *= 2;
     const int groups = (int)((uint32_t)(count + size - 1) / (uint32_t)size);
     const int one = (count + unit - 1) / unit;
     const int two = (size + unit - 1) / unit + (groups + unit - 1) / unit;
