@@ -558,8 +558,8 @@ constexpr float kSlack = 8.0f;    // see the rescaling below
 // values.  A segment of many partials is joined in two levels, by the last workgroup of
 // each group of `size` partials and by the last of the groups: what counts is how many
 // rounds of reads follow one another (1 x 41461 tokens, bf16, 2 kv heads of 192 values with
-// 16 query heads each: 50 us on one level, 32 on two; 2 x up to 27428, NVFP4, 1 head of 256:
-// 18.5 and 14.8, and 22.7 if threads do not share).  More partials at a time cost more where
+// 16 query heads each: 50 us on one level, 30 on two; 2 x up to 27428, NVFP4, 1 head of 256:
+// 18.5 and 14.3, and 22.7 if threads do not share).  More partials at a time cost more where
 // there are two or three than they save elsewhere (24 x 12 heads x 1000 x 64: 12.8 us with
 // 4, 13.1 with 8).
 constexpr int kBatch = 4;

@@ -23,8 +23,8 @@ constexpr size_t kCounterBytes = sizeof(uint32_t) * (kCounters + kMaxResident);
 // Partial results pass from one workgroup to another on any XCD, each with an L2 of its
 // own.  A release and an acquire fence at that scope write back and invalidate a whole L2
 // (paged attention of 32 sequences of up to 8192 tokens: 262 us instead of 89); instead the
-// few values that are passed are themselves accessed at device scope, as relaxed atomics of
-// 8 bytes: the stores write through to memory and the loads read from there.  What orders them is
+// few values that are passed are themselves accessed at device scope: the stores (relaxed
+// atomics of 8 bytes) write through to memory and the loads read from there.  What orders them is
 // that every thread waits until its stores are done (wait_stores), then the barrier, and
 // only then one thread counts the workgroup: who reads the full count reads after all
 // the stores.
@@ -32,8 +32,8 @@ __device__ __forceinline__ void store_shared(float* p, f32x2 v) {
   __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v),
                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// The loads go to memory too (the cache policy of device scope), 8 or 16 bytes at a byte
-// offset of `bytes` bytes at p; offsets behind them read zeros.
+// The loads, with the cache policy of device scope: 8 or 16 bytes at a byte offset of the
+// `bytes` bytes at p (behind them: zeros).
 constexpr int kDeviceScope = 16;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_floats(const float* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), 0, bytes, 0x27000);
