@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple, Union
@@ -535,48 +534,56 @@ def mx_qlinear_fwd(aq: MXFP4Tensor, bq: MXFP4Tensor, out: Optional[torch.Tensor]
 
 # ---------------------------------------------------------------- serving one token at a time
 # These calls run once per layer and token, so their wrappers marshal raw addresses and
-# check no more than the library needs to stay inside its tensors.
+# check no more than the library needs to stay inside its tensors.  A call on a small
+# problem takes as long as its launch (3 of 6 to 8 us) and what happens here, so devices are
+# compared by index and a tensor's shape and stride are taken once.
+_BF16, _U8, _F32, _I32, _I64 = (torch.bfloat16, torch.uint8, torch.float32, torch.int32,
+                                torch.int64)
 
 # The handle of a device's current stream; torch's own accessor where this build of torch
 # has it (0.1 us; building a Stream object for it takes 1.9 us of a call's 10).
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _raw_stream(device: torch.device) -> int:
+def _raw_stream(index: int) -> int:
     if _current_raw_stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _current_raw_stream(device.index)
+        return torch.cuda.current_stream(index).cuda_stream
+    return _current_raw_stream(index)
+
+
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                        torch.cuda.is_current_stream_capturing)
 
 
 _OUT_CODE = {torch.float32: FOS_OUT_F32, torch.bfloat16: FOS_OUT_BF16}
 
 
 def _wlinear_args(x, wq, bias, out_dtype, out, block):
-    """Checked (M, N, K, row stride, y) of a weight-only product."""
+    """Checked (device, M, N, K, row stride, y) of a weight-only product."""
     data, scales = wq.data, wq.scales
-    dev = data.device
-    if x.dim() != 2 or x.dtype != torch.bfloat16 or not x.is_cuda or x.stride(1) != 1:
+    dev, strides = data.get_device(), x.stride()
+    if len(strides) != 2 or strides[1] != 1 or x.dtype != _BF16 or x.get_device() < 0:
         raise ValueError("x must be a 2-D bfloat16 CUDA tensor with contiguous rows")
     M, K = x.shape
-    N, K2 = data.shape[0], 2 * data.shape[1]
-    if K != K2:
+    N, half = data.shape
+    if K != 2 * half:
         raise ValueError("inner dimensions differ")
-    if (data.dtype != torch.uint8 or scales.dtype != torch.uint8 or not data.is_contiguous()
-            or not scales.is_contiguous() or tuple(scales.shape) != (N, K // block)):
+    if (data.dtype != _U8 or scales.dtype != _U8 or not data.is_contiguous()
+            or not scales.is_contiguous() or scales.shape != (N, K // block)):
         raise ValueError(f"the record must be contiguous uint8 data [N, K/2] and scales [N, K/{block}]")
-    if x.device != dev or scales.device != dev:
+    if x.get_device() != dev or scales.get_device() != dev:
         raise ValueError("x and the weight record are on different devices")
-    if bias is not None and (bias.shape != (N,) or bias.dtype != torch.bfloat16
-                             or bias.device != dev or not bias.is_contiguous()):
+    if bias is not None and (bias.shape != (N,) or bias.dtype != _BF16
+                             or bias.get_device() != dev or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous bf16 [N] tensor on x's device")
     if out is None:
         if out_dtype not in _OUT_CODE:
             raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+        out = x.new_empty(M, N) if out_dtype == _BF16 else x.new_empty(M, N, dtype=out_dtype)
     elif (out.shape != (M, N) or out.dtype != out_dtype or out_dtype not in _OUT_CODE
-          or out.device != dev or not out.is_contiguous()):
+          or out.get_device() != dev or not out.is_contiguous()):
         raise ValueError("out must be a contiguous [M, N] tensor of out_dtype on x's device")
-    return M, N, K, (x.stride(0) if M > 1 else K), out
+    return dev, M, N, K, (strides[0] if M > 1 else K), out
 
 
 def wlinear_fwd(x: torch.Tensor, wq: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
@@ -589,12 +596,12 @@ def wlinear_fwd(x: torch.Tensor, wq: NVFP4Tensor, bias: Optional[torch.Tensor] =
     if wq.hadamard_seed is not None:
         raise ValueError("the weight record carries a Hadamard transform that x does not")
     t = wq.tensor_scale
-    if t.dtype != torch.float32 or t.numel() != 1 or t.device != x.device:
+    if t.dtype != _F32 or t.numel() != 1 or t.get_device() != x.get_device():
         raise ValueError("tensor_scale must be a one-element fp32 tensor on x's device")
-    M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 16)
+    dev, M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 16)
     _check(_lib.fos_wlinear_fwd(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
                                 t.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K,
-                                _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(x.device)),
+                                _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(dev)),
            "fos_wlinear_fwd")
     return y
 
@@ -603,10 +610,10 @@ def mx_wlinear_fwd(x: torch.Tensor, wq: MXFP4Tensor, bias: Optional[torch.Tensor
                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None
                    ) -> torch.Tensor:
     """wlinear_fwd for an MXFP4 weight record."""
-    M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 32)
+    dev, M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 32)
     _check(_lib.fos_mx_wlinear_fwd(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
                                    None if bias is None else bias.data_ptr(), M, N, K,
-                                   _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(x.device)),
+                                   _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(dev)),
            "fos_mx_wlinear_fwd")
     return y
 
@@ -619,7 +626,7 @@ class PagedKVCache:
     (fp32 [1]).  ``kv_cache`` allocates one."""
 
     __slots__ = ("k", "v", "k_scales", "v_scales", "k_tensor_scale", "v_tensor_scale",
-                 "num_pages", "num_kv_heads", "page_size", "head_dim", "format", "device", "_c",
+                 "num_pages", "num_kv_heads", "page_size", "head_dim", "format", "device", "_index", "_c",
                  "_ref")
 
     def __init__(self, k, v, k_scales=None, v_scales=None, k_tensor_scale=None,
@@ -652,6 +659,7 @@ class PagedKVCache:
         self.k_tensor_scale, self.v_tensor_scale = k_tensor_scale, v_tensor_scale
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = P, H, S, D
         self.format, self.device = ("nvfp4" if nvfp4 else "bf16"), k.device
+        self._index = k.get_device()
         ptr = lambda t: t.data_ptr() if nvfp4 else None
         self._c = FosKVCache(ctypes.sizeof(FosKVCache), FOS_KV_NVFP4 if nvfp4 else FOS_KV_BF16, P,
                              S, H, D, 0, k.data_ptr(), v.data_ptr(), ptr(k_scales), ptr(v_scales),
@@ -676,19 +684,27 @@ def kv_cache(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
     return PagedKVCache(k, v, ks, vs, k_tensor_scale, v_tensor_scale)
 
 
-def _check_rows(cache: PagedKVCache, x: torch.Tensor, what: str):
-    s = x.stride()
-    if (x.dim() != 3 or x.shape[1] != cache.num_kv_heads or x.shape[2] != cache.head_dim
-            or x.dtype != torch.bfloat16 or x.device != cache.device or s[2] != 1
-            or (x.shape[1] > 1 and s[1] != cache.head_dim)):
+def _check_rows(cache: PagedKVCache, x: torch.Tensor, T: int, what: str) -> int:
+    """The token stride of x."""
+    H, D, s = cache.num_kv_heads, cache.head_dim, x.stride()
+    if (len(s) != 3 or x.shape[1:] != (H, D) or x.dtype != _BF16 or x.get_device() != cache._index
+            or s[2] != 1 or (H > 1 and s[1] != D)):
         raise ValueError(f"{what} must be bf16 [tokens, kv heads, head dim] on the cache's device, "
                          "each token's heads in one run")
+    if x.shape[0] != T:
+        raise ValueError("k, v and slots disagree on the number of tokens")
+    return s[0]
 
 
-def _check_slots(cache: PagedKVCache, slots: torch.Tensor):
-    if (slots.dim() != 1 or slots.dtype != torch.int64 or slots.device != cache.device
+def _check_slots(cache: PagedKVCache, slots: torch.Tensor) -> int:
+    """The number of slots."""
+    if (slots.dim() != 1 or slots.dtype != _I64 or slots.get_device() != cache._index
             or not slots.is_contiguous()):
         raise ValueError("slots must be a contiguous 1-D int64 tensor on the cache's device")
+    return slots.shape[0]
+
+
+_KV_RULES = {"4/6": FOS_RULE_4OVER6, "6": FOS_RULE_6ONLY}
 
 
 def kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -698,27 +714,21 @@ def kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     [T], page * page_size + token of the page; negative or past the cache: skipped).
     An NVFP4 cache quantizes each 16 values with ``rule`` ("4/6" or "6") under the
     cache's tensor scales.  Slots of one call must be distinct."""
-    _check_rows(cache, k, "k")
-    _check_rows(cache, v, "v")
-    _check_slots(cache, slots)
-    T = slots.shape[0]
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("k, v and slots disagree on the number of tokens")
-    rules = {"4/6": FOS_RULE_4OVER6, "6": FOS_RULE_6ONLY}
-    _check(_lib.fos_kv_append(cache._ref, rules[rule], k.data_ptr(), k.stride(0), v.data_ptr(),
-                              v.stride(0), slots.data_ptr(), T, _raw_stream(cache.device)),
+    T = _check_slots(cache, slots)
+    k_stride, v_stride = _check_rows(cache, k, T, "k"), _check_rows(cache, v, T, "v")
+    _check(_lib.fos_kv_append(cache._ref, _KV_RULES[rule], k.data_ptr(), k_stride, v.data_ptr(),
+                              v_stride, slots.data_ptr(), T, _raw_stream(cache._index)),
            "fos_kv_append")
 
 
 def kv_gather(cache: PagedKVCache, slots: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """Keys and values of ``slots`` (int64 [T]) as bf16 [T, kv heads, head dim]; zeros for
     slots outside the cache."""
-    _check_slots(cache, slots)
-    T, H, D = slots.shape[0], cache.num_kv_heads, cache.head_dim
-    k = torch.empty(T, H, D, dtype=torch.bfloat16, device=cache.device)
-    v = torch.empty(T, H, D, dtype=torch.bfloat16, device=cache.device)
+    T, H, D = _check_slots(cache, slots), cache.num_kv_heads, cache.head_dim
+    k = torch.empty(T, H, D, dtype=_BF16, device=cache.device)
+    v = torch.empty(T, H, D, dtype=_BF16, device=cache.device)
     _check(_lib.fos_kv_gather(cache._ref, slots.data_ptr(), T, k.data_ptr(), H * D, v.data_ptr(),
-                              H * D, _raw_stream(cache.device)), "fos_kv_gather")
+                              H * D, _raw_stream(cache._index)), "fos_kv_gather")
     return k, v
 
 
@@ -745,7 +755,7 @@ def _decode_workspace(device: torch.device, stream: int, sizes) -> torch.Tensor:
     """The current stream's scratch for paged_decode, grown by powers of two.  A captured
     call gets one of its own, cleared in the graph: the graph may be replayed on another
     stream, or later than the next eager call on this one."""
-    if torch.cuda.is_current_stream_capturing():
+    if _is_capturing():
         return paged_decode_workspace(*sizes, device=device)
     key = (device.index, stream)
     ws = _decode_workspaces.get(key)
@@ -770,35 +780,36 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
     Returns bf16 [B, query heads, head dim] (``out`` if given), and with
     ``return_lse`` also the fp32 [B, query heads] log-sum-exp of the scaled scores.
     Where nothing is visible the output is 0 and its lse -inf."""
-    dev, D = cache.device, cache.head_dim
-    s = q.stride()
-    if (q.dim() != 3 or q.dtype != torch.bfloat16 or q.device != dev or q.shape[2] != D
-            or s[2] != 1 or (q.shape[1] > 1 and s[1] != D)):
-        raise ValueError("q must be bf16 [sequences, query heads, head dim] on the cache's device, "
-                         "each sequence's heads in one run")
-    B, Hq, _ = q.shape
+    dev, D, s = cache._index, cache.head_dim, q.stride()
+    if len(s) != 3 or q.dtype != _BF16 or q.get_device() != dev:
+        raise ValueError("q must be bf16 [sequences, query heads, head dim] on the cache's device")
+    B, Hq, Dq = q.shape
+    if Dq != D or s[2] != 1 or (Hq > 1 and s[1] != D):
+        raise ValueError("q must have the cache's head dim, each sequence's heads in one run")
     if Hq < 1 or Hq % cache.num_kv_heads:
         raise ValueError("query heads must be a multiple of the cache's kv heads")
-    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev
-            or block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+    t = block_table.stride()
+    if len(t) != 2 or block_table.dtype != _I32 or block_table.get_device() != dev:
         raise ValueError("block_table must be int32 [sequences, pages] on the cache's device")
-    if (seq_lens.shape != (B,) or seq_lens.dtype != torch.int32 or seq_lens.device != dev
+    rows, pages = block_table.shape
+    if rows != B or (pages > 1 and t[1] != 1):
+        raise ValueError("block_table must have a row of pages for each sequence")
+    if (seq_lens.shape != (B,) or seq_lens.dtype != _I32 or seq_lens.get_device() != dev
             or not seq_lens.is_contiguous()):
         raise ValueError("seq_lens must be a contiguous int32 [sequences] tensor on the cache's device")
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev)
-    elif (out.shape != (B, Hq, D) or out.dtype != torch.bfloat16 or out.device != dev
+        out = q.new_empty(B, Hq, D)
+    elif (out.shape != (B, Hq, D) or out.dtype != _BF16 or out.get_device() != dev
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous bf16 tensor of q's shape on the cache's device")
-    lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
+    lse = q.new_empty(B, Hq, dtype=_F32) if return_lse else None
     stream = _raw_stream(dev)
     if ws is None:
-        ws = _decode_workspace(dev, stream, (B, Hq, cache.num_kv_heads, D))
-    elif ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        ws = _decode_workspace(cache.device, stream, (B, Hq, cache.num_kv_heads, D))
+    elif ws.dtype != _U8 or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on the cache's device")
-    _check(_lib.fos_paged_decode(cache._ref, q.data_ptr(), s[0], B, Hq, block_table.data_ptr(),
-                                 block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
-                                 1.0 / math.sqrt(D) if scale is None else scale, int(window),
-                                 out.data_ptr(), None if lse is None else lse.data_ptr(),
+    _check(_lib.fos_paged_decode(cache._ref, q.data_ptr(), s[0], B, Hq, block_table.data_ptr(), t[0],
+                                 pages, seq_lens.data_ptr(), D ** -0.5 if scale is None else scale,
+                                 int(window), out.data_ptr(), None if lse is None else lse.data_ptr(),
                                  ws.data_ptr(), ws.numel(), stream), "fos_paged_decode")
     return (out, lse) if return_lse else out
