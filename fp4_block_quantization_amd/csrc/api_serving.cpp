@@ -16,6 +16,7 @@ constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;   // work-items of one launch
 constexpr int kMinPage = 16, kMaxPage = 4096;
 constexpr int kMaxHeadDim = 256;
+constexpr int kMaxHeads = 65536;   // keeps the index arithmetic of the cache kernels in range
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;   // of one sequence
 constexpr int64_t kMaxBatchTokens = (int64_t)1 << 38;
 
@@ -70,7 +71,8 @@ fos_status check_cache(const fos_kv_cache* c) {
       (c->format != FOS_KV_BF16 && c->format != FOS_KV_NVFP4))
     return FOS_E_FLAGS;
   if (c->num_pages < 0 || c->num_pages >= kMaxDim || c->page_size < kMinPage ||
-      c->page_size > kMaxPage || c->page_size % 16 || c->num_kv_heads < 1 || c->head_dim < 32 ||
+      c->page_size > kMaxPage || c->page_size % 16 || c->num_kv_heads < 1 ||
+      c->num_kv_heads > kMaxHeads || c->head_dim < 32 ||
       c->head_dim > kMaxHeadDim || c->head_dim % 32)
     return FOS_E_SHAPE;
   const int64_t row = (int64_t)c->page_size * c->head_dim;   // at most 2^20

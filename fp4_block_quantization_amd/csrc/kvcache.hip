@@ -33,7 +33,7 @@ struct Div32 {                  // dividend * d < 2^32
 struct Plan {
   KVRowsArgs a;
   int64_t n;                    // threads of K
-  uint32_t per, units;          // threads of a token (fewer than 2^24), of a row
+  uint32_t per, units;          // threads of a token (at most 65536 * 32), of a row
   Div64 by_per, by_page;
   Div32 by_units;
   Plan(const KVRowsArgs& args, int values)

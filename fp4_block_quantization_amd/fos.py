@@ -652,9 +652,10 @@ class PagedKVCache:
         for t in tensors:
             if not t.is_cuda or t.device != k.device or not t.is_contiguous():
                 raise ValueError("cache tensors must be contiguous CUDA tensors on one device")
-        if not (16 <= S <= 4096 and S % 16 == 0 and 32 <= D <= 256 and D % 32 == 0 and H >= 1):
+        if not (16 <= S <= 4096 and S % 16 == 0 and 32 <= D <= 256 and D % 32 == 0
+                and 1 <= H <= 65536):
             raise ValueError("page size must be a multiple of 16 from 16 to 4096, head dim a "
-                             "multiple of 32 from 32 to 256")
+                             "multiple of 32 from 32 to 256, kv heads 1 to 65536")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.k_tensor_scale, self.v_tensor_scale = k_tensor_scale, v_tensor_scale
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = P, H, S, D

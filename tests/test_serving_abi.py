@@ -159,3 +159,12 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         fos.kv_cache(2, 16, 2, 64, format="fp8", device="cpu")
     with pytest.raises(ValueError):
         fos.kv_cache(2, 16, 2, 64, format="nvfp4", device="cpu")    # no tensor scales
+
+
+def test_too_many_kv_heads():
+    """More than 65536 kv heads are refused by every call, also with no page and one token."""
+    c = cache(num_kv_heads=65537, num_pages=0, head_dim=32)
+    width = 65537 * 32
+    assert append(c, ks=width, vs=width, T=1) == SHAPE
+    assert gather(c, ks=width, vs=width, T=1) == SHAPE
+    assert gather(cache(num_kv_heads=65536, num_pages=0, head_dim=32), T=0) == OK
