@@ -233,8 +233,10 @@ fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64
   a.G = (int)(num_q_heads / cache->num_kv_heads);
   a.table = block_table;
   a.table_stride = table_stride;
-  // an empty cache holds no page: nothing is visible
+  // An empty cache holds no page: nothing is visible.  Its pointers may be null, and the
+  // kernel of a bf16 cache, unlike that of an NVFP4 one, reads none before it sees a token.
   a.pages_per_seq = cache->num_pages > 0 ? (int)pages_per_seq : 0;
+  if (cache->num_pages == 0) a.c.nvfp4 = false;
   a.lens = seq_lens;
   a.scale = softmax_scale;
   a.window = window;

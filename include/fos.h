@@ -436,7 +436,8 @@ enum { FOS_KV_BF16 = 0, FOS_KV_NVFP4 = 1 };
  * rows appended at different times share them.
  *   page_size: 16 to 4096, a multiple of 16; head_dim: 32 to 256, a multiple of 32;
  *   num_kv_heads: 1 to 65536; num_pages >= 0; fewer than 2^40 values in each of K and V.
- *   Data and scales 16-byte aligned, tensor scales 4-byte. */
+ *   Data and scales 16-byte aligned, tensor scales 4-byte; with num_pages 0 nothing is
+ *   read or written through any of these pointers. */
 typedef struct {
   uint32_t struct_size;       /* must equal sizeof(fos_kv_cache)                      */
   uint32_t format;            /* FOS_KV_*                                             */
