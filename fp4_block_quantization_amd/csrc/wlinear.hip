@@ -82,7 +82,7 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
   const uint32_t tiles_m = (uint32_t)((a.M + kTileM - 1) / kTileM);
   const int64_t n0 = (int64_t)(blockIdx.x / tiles_m) * kTileN;
   const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * kTileM;
-  const int K = (int)a.K, chunks = (K + kChunk - 1) / kChunk;
+  const int K = (int)a.K, chunks = (K - 1) / kChunk + 1;   // K is below 2^31, K + 127 need not be
   const float t = kMX ? 1.0f : a.wt[0];
   const int rows_m = (int)min((int64_t)kTileM, a.M - m0);
   // loads in memory order: four lanes to a weight row, 16 to an activation row; rows past
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * KW, R == 2 && !kMany ? 4 : 3) void wlinear_qua
   const int m0 = kMany ? 4 * (int)blockIdx.y : 0;
   const uint16_t* xp = a.x + m0 * a.x_stride;
   const int M = min((int)a.M - m0, 4);
-  const int K = (int)a.K, steps = (K + kQuadStep - 1) / kQuadStep;
+  const int K = (int)a.K, steps = (K - 1) / kQuadStep + 1;   // K is below 2^31, K + 511 need not be
   const float t = kMX ? 1.0f : a.wt[0];
   const uint8_t* wp[R];
   const uint8_t* sp[R];
