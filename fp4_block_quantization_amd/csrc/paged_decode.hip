@@ -232,6 +232,13 @@ __device__ __forceinline__ u32x4 dequant8(uint32_t w, f16x2 s) {
   return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
                __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)};
 }
+// The same as bf16, where it is exact too.
+__device__ __forceinline__ u32x4 dequant8_bf16(uint32_t w, float s) {
+  const f32x2 a = cvt_pk_f32_fp4<0>(w), b = cvt_pk_f32_fp4<1>(w);
+  const f32x2 c = cvt_pk_f32_fp4<2>(w), d = cvt_pk_f32_fp4<3>(w);
+  return u32x4{pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s),
+               pack_bf16x2(c.x * s, c.y * s), pack_bf16x2(d.x * s, d.y * s)};
+}
 // Byte kSel of w (two nibbles) times the two scales of s.
 template <int kSel>
 __device__ __forceinline__ uint32_t dequant2(uint32_t w, f16x2 s) {
@@ -247,6 +254,12 @@ __device__ __forceinline__ f16x2 scale_pair_hi(uint32_t w) {
 // The nibbles selected by 0x0f0f0f0f from x, the others from y.
 __device__ __forceinline__ uint32_t low_nibbles(uint32_t x, uint32_t y) {
   return (x & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+}
+
+// The smaller of m and the magnitudes of two bf16 less 1 (a zero: the largest), by halves.
+__device__ __forceinline__ uint32_t pk_min_less1(uint32_t m, uint32_t w) {
+  const u16x2 b = __builtin_bit_cast(u16x2, w & 0x7fff7fffu) - u16x2{1, 1};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, m), b));
 }
 
 template <bool kNVFP4>
@@ -504,6 +517,21 @@ struct Step<true, D> {
     }
     return s;
   }
+  // The same for queries that half precision cannot hold: bf16 operands.  K is exact in
+  // them too, but its block scale is applied in fp32, value by value.
+  __device__ __forceinline__ f32x4 scores_bf16(const u32x4 (&qf)[D / 32], int n, int u) const {
+    f32x4 s = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < P::count; ++i) {
+      const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8(ksc[2 * n + u][i], false);
+#pragma unroll
+      for (int j = 0; j < P::size(i) / 32; ++j) {
+        const int at = P::at(i) / 32 + j;
+        s = mfma<false>(dequant8_bf16(kw[2 * n + u][at], j >= 2 ? sc.y : sc.x), qf[at], s);
+      }
+    }
+    return s;
+  }
   __device__ __forceinline__ void mask_v(uint8_t* lds, const uint32_t* seen, int lane) {
     // lane r < 8 of group q holds the mask of groups q and 4 + q of 8 tokens: each of the
     // group's 16 lanes clears the scales of one token and half
@@ -754,18 +782,32 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
     look_up(t + kStride);
   }
 
-  // Queries: column r of both products, scaled by a power of two so that the largest is in
-  // [1, 2): exact in bf16, and in half precision but for values below 2^-14 of it, which
-  // keep an absolute 2^-25 of the largest.  The power goes into the scale of the scores.
+  // Queries: column r of both products, scaled by a power of two that goes into the scale
+  // of the scores.  Beside a bf16 cache they are bf16, the largest in [1, 2); beside an NVFP4
+  // one half precision, the largest in [2^14, 2^15): exact for bf16 values down to 2^-31 of
+  // it.  A wave that holds a smaller one (K may be 0 beside the large ones, so that it
+  // decides the scores) takes the queries as bf16, up to 2^100 as they are (every wave of 16 x
+  // up to 32768 tokens: 66.4 us instead of 64.3).
   u32x4 qf[kSteps];
   float cs;
+  bool in_bf16 = false;
   {
-    uint32_t mx = 0;
+    uint32_t mx = 0, least = ~0u;              // least: of the magnitudes but 0, less 1
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j)
+    for (int j = 0; j < kSteps; ++j) {
       mx = pk_max_abs4(mx, make_uint4(raw[j].x, raw[j].y, raw[j].z, raw[j].w));
+      if constexpr (kNVFP4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) least = pk_min_less1(least, raw[j][i]);
+      }
+    }
     const float top = max_over_groups(__uint_as_float(pk_max_to_f32_bits(mx)));
-    const int e = top > 0.0f ? ilogbf(top) : 0;
+    int e = top > 0.0f ? ilogbf(top) : 0;
+    if constexpr (kNVFP4) {
+      const int field = (int)((min(least & 0xffffu, least >> 16) + 1) >> 7);
+      in_bf16 = __any(field < e + 127 - 31);
+      e = in_bf16 ? max(e - 100, 0) : e - 14;
+    }
 #pragma unroll
     for (int j = 0; j < kSteps; ++j)
 #pragma unroll
@@ -773,6 +815,14 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
         const float x = ldexpf(bf16_lo(raw[j][i]), -e), y = ldexpf(bf16_hi(raw[j][i]), -e);
         qf[j][i] = kNVFP4 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
       }
+    if (kNVFP4 && in_bf16) {
+      asm volatile("");                        // a branch, not selects for every query
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qf[j][i] = pack_bf16x2(ldexpf(bf16_lo(raw[j][i]), -e), ldexpf(bf16_hi(raw[j][i]), -e));
+    }
     // the sign of the scale goes into the queries: cs >= 0, and the maximum can be taken
     // before the scale (a scale of 0 as queries of 0: -inf * 0 is not -inf)
     const float full = ldexpf(a.scale * kLog2e * kt0, e);
@@ -815,14 +865,25 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
     }
     if constexpr (kNVFP4) step.read_all(mine, r, q);
     float w[N][8];                             // scores, before cs
+    if (!kNVFP4 || !in_bf16) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const f32x4 s = step.scores(mine, qf, n, u, r, q);
+        for (int u = 0; u < 2; ++u) {
+          const f32x4 s = step.scores(mine, qf, n, u, r, q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[n][4 * u + i] = s[i];
-      }
+          for (int i = 0; i < 4; ++i) w[n][4 * u + i] = s[i];
+        }
+    } else if constexpr (kNVFP4) {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const f32x4 s = step.scores_bf16(qf, n, u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[n][4 * u + i] = s[i];
+        }
+    }
     if (!all) {
       asm volatile("");
 #pragma unroll

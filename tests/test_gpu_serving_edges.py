@@ -7,9 +7,10 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_serving as T
 from fp4_block_quantization_amd import workloads as W
 from oracle import serving as S
-from test_gpu_serving import DEV, U, dev, f64, fos, within  # noqa: F401
+from test_gpu_serving import DEV, FMTS, U, dev, f64, fos, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,34 @@ def test_decode_over_an_empty_nvfp4_cache(fos):
     out, lse = fos.paged_decode(q, cache, torch.zeros(2, 3, dtype=torch.int32, device=DEV),
                                 torch.tensor([5, 48], dtype=torch.int32, device=DEV), return_lse=True)
     assert not out.any() and (lse == -float("inf")).all()
+
+
+def one_sequence(fos, fmt, k, v, page=16):
+    """A cache with these rows (bf16 [tokens, heads, dim]) as one sequence, and what to call
+    paged_decode with."""
+    n, heads, dim = k.shape
+    pages = -(-n // page)
+    cache = T.new_cache(fos, fmt, pages, page, heads, dim)
+    fos.kv_append(cache, k.to(DEV), v.to(DEV), torch.arange(n, device=DEV))
+    return cache, (torch.arange(pages, dtype=torch.int32, device=DEV)[None],
+                   torch.tensor([n], dtype=torch.int32, device=DEV))
+
+
+@FMTS
+@pytest.mark.parametrize("top,others,scale", [(10, 0, None), (17, 0, None), (20, 0, None), (24, 0, None),
+                                              (45, 0, None), (100, 0, 0.25), (0, -100, 1e30),
+                                              (-3, -20, 1e5)])
+def test_decode_query_of_wide_range(fos, fmt, top, others, scale):
+    """Some heads have a value of 2^top beside others of about 2^others, where K is zero: the
+    scores are the others'."""
+    n, Hq, Hkv, D = 300, 8, 2, 128
+    k = W.random_bf16(n, Hkv * D, 1, "normal").view(n, Hkv, D)
+    v = W.random_bf16(n, Hkv * D, 2, "normal").view(n, Hkv, D)
+    q = W.random_bf16(Hq, D, 3, "normal", scale=2.0 ** others)
+    for h, d in ((0, 5), (1, 126), (6, 64)):
+        q[h, d] = 1.75 * 2.0 ** top
+        k[:, h // 4, d] = 0.0
+    cache, args = one_sequence(fos, fmt, k, v)
+    out, lse = fos.paged_decode(q[None].to(DEV), cache, *args, scale=scale, return_lse=True)
+    kk, vv = (T.N_rows(cache, name)[:n] for name in "kv")
+    T.check_attention(out[0], lse[0], f64(q), kk, vv, D ** -0.5 if scale is None else scale)
