@@ -34,6 +34,8 @@
 // reaches.  NVFP4: the loads and the conversions of their step share the time; 16 x up to
 // 32768 tokens, 64 heads over 8 of 128: 61 us, 5.0 TB/s (55 us with the arithmetic left
 // out).  Few tokens (1 x 200): 6 us, of which an empty launch is 2.
+#include <cfloat>
+
 #include "serving.hpp"
 
 namespace fos {
@@ -239,6 +241,7 @@ __device__ __forceinline__ u32x4 dequant8_bf16(uint32_t w, float s) {
   return u32x4{pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s),
                pack_bf16x2(c.x * s, c.y * s), pack_bf16x2(d.x * s, d.y * s)};
 }
+constexpr int kShiftBf16 = 12;    // 6 * 448 < 2^12
 // Byte kSel of w (two nibbles) times the two scales of s.
 template <int kSel>
 __device__ __forceinline__ uint32_t dequant2(uint32_t w, f16x2 s) {
@@ -518,12 +521,14 @@ struct Step<true, D> {
     return s;
   }
   // The same for queries that half precision cannot hold: bf16 operands.  K is exact in
-  // them too, but its block scale is applied in fp32, value by value.
+  // them too, but its block scale is applied in fp32, value by value.  K enters times
+  // 2^-kShiftBf16, below 1, so that a product with any query is finite.
   __device__ __forceinline__ f32x4 scores_bf16(const u32x4 (&qf)[D / 32], int n, int u) const {
     f32x4 s = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < P::count; ++i) {
-      const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8(ksc[2 * n + u][i], false);
+      const f32x2 sc = __builtin_amdgcn_cvt_pk_f32_fp8(ksc[2 * n + u][i], false) *
+                       __builtin_ldexpf(1.0f, -kShiftBf16);
 #pragma unroll
       for (int j = 0; j < P::size(i) / 32; ++j) {
         const int at = P::at(i) / 32 + j;
@@ -783,11 +788,11 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
   }
 
   // Queries: column r of both products, scaled by a power of two that goes into the scale
-  // of the scores.  Beside a bf16 cache they are bf16, the largest in [1, 2); beside an NVFP4
-  // one half precision, the largest in [2^14, 2^15): exact for bf16 values down to 2^-31 of
-  // it.  A wave that holds a smaller one (K may be 0 beside the large ones, so that it
-  // decides the scores) takes the queries as bf16, up to 2^100 as they are (every wave of 16 x
-  // up to 32768 tokens: 66.4 us instead of 64.3).
+  // of the scores.  Beside a bf16 cache they are bf16 and only ever scaled up, to a largest of
+  // 1 or more, which loses nothing; beside an NVFP4 one half precision, the largest in [2^14,
+  // 2^15): exact for bf16 values down to 2^-31 of it.  A wave that holds a smaller one (K may
+  // be 0 beside the large ones, so that it decides the scores) takes the queries as bf16 there
+  // too (every wave of 16 x up to 32768 tokens: 66.4 us instead of 64.3).
   u32x4 qf[kSteps];
   float cs;
   bool in_bf16 = false;
@@ -802,11 +807,15 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
       }
     }
     const float top = max_over_groups(__uint_as_float(pk_max_to_f32_bits(mx)));
-    int e = top > 0.0f ? ilogbf(top) : 0;
+    int e = top > 0.0f ? ilogbf(top) : 0;      // queries times 2^-e
+    int more = 0;                              // K times 2^-more
     if constexpr (kNVFP4) {
       const int field = (int)((min(least & 0xffffu, least >> 16) + 1) >> 7);
       in_bf16 = __any(field < e + 127 - 31);
-      e = in_bf16 ? max(e - 100, 0) : e - 14;
+      e = in_bf16 ? min(e, 0) : e - 14;
+      more = in_bf16 ? kShiftBf16 : 0;
+    } else {
+      e = min(e, 0);
     }
 #pragma unroll
     for (int j = 0; j < kSteps; ++j)
@@ -825,8 +834,8 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
     }
     // the sign of the scale goes into the queries: cs >= 0, and the maximum can be taken
     // before the scale (a scale of 0 as queries of 0: -inf * 0 is not -inf)
-    const float full = ldexpf(a.scale * kLog2e * kt0, e);
-    cs = full == 0.0f ? 1.0f : fabsf(full);
+    const float full = ldexpf(a.scale * kLog2e * kt0, e + more);
+    cs = full == 0.0f ? 1.0f : fabsf(full) > FLT_MAX ? FLT_MAX : fabsf(full);   // inf * 0 is not 0
     if (!(full > 0.0f)) {
       const uint32_t flip = full < 0.0f ? 0x80008000u : 0u, keep = full < 0.0f ? ~0u : 0u;
 #pragma unroll

@@ -497,7 +497,8 @@ size_t fos_paged_decode_counter_bytes(void);
  * below 1 has none.  Where nothing is visible, out is 0 and lse -infinity.  What the
  * pages hold in places that are not visible does not matter (NaN included); q and the
  * visible rows must be finite (a NaN score is not lost: the head's out and lse are NaN).
- * Statistics and sums are fp32; results do not depend
+ * The scores' products of q with the stored values are exact, whatever the range within a
+ * query; statistics and sums are fp32; results do not depend
  * on what else the GPU runs (no atomic sums).
  *   q_bf16: [num_seqs][num_q_heads][head_dim], sequence stride q_stride elements;
  *   block_table: int32 [num_seqs][pages_per_seq], row stride table_stride elements;

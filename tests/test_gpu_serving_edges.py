@@ -104,3 +104,24 @@ def test_decode_query_of_wide_range(fos, fmt, top, others, scale):
     out, lse = fos.paged_decode(q[None].to(DEV), cache, *args, scale=scale, return_lse=True)
     kk, vv = (T.N_rows(cache, name)[:n] for name in "kv")
     T.check_attention(out[0], lse[0], f64(q), kk, vv, D ** -0.5 if scale is None else scale)
+
+
+@FMTS
+@pytest.mark.parametrize("top,others,scale", [(127, 0, 2.0), (60, -100, 1e30), (127, -100, 1e30),
+                                              (-100, -120, 1e36), (127, 120, 2.0 ** -119)])
+def test_decode_query_and_scale_at_their_ends(fos, fmt, top, others, scale):
+    """The same at the ends of the range of bf16, with a scale that the large values alone
+    would take past fp32."""
+    test_decode_query_of_wide_range(fos, fmt, top, others, scale)
+
+
+@FMTS
+@pytest.mark.parametrize("q", [1.0, 2.0 ** 127])
+def test_decode_scores_of_zero_under_any_scale(fos, fmt, q):
+    """K is 0: every token has the same weight, however large the query and the scale."""
+    n = 70
+    v = W.random_bf16(n, 64, 2, "normal").view(n, 1, 64)
+    cache, args = one_sequence(fos, fmt, torch.zeros(n, 1, 64, dtype=torch.bfloat16), v)
+    out, lse = fos.paged_decode(torch.full((1, 1, 64), q, dtype=torch.bfloat16, device=DEV), cache, *args,
+                                scale=3.4e38, return_lse=True)
+    T.check_attention(out[0], lse[0], np.zeros((1, 64)), np.zeros((n, 1, 64)), T.N_rows(cache, "v")[:n], 1.0)
