@@ -584,7 +584,7 @@ struct Step<true, D> {
   }
 };
 
-constexpr float kSlack = 8.0f;    // see the rescaling below
+constexpr float kSlack = 8.0f, kBelow = 7.0f;    // see the rescaling below
 
 // Joining partials.  A thread takes four values of a head and reads kBatch partials at a
 // time; where that leaves threads idle, `split` of them share the partials of the same
@@ -901,17 +901,19 @@ __global__ __launch_bounds__(kThreads, kPerCU<D>) void paged_decode_kernel(Plan 
         for (int e = 0; e < 8; ++e) w[n][e] = (seen[n] >> e) & 1 ? w[n][e] : -INFINITY;
     }
     // Rescaling.  m is a common reference of a head's four lanes rather than the exact
-    // maximum: it moves only when a score is more than 2^kSlack above it, so that most
-    // steps need neither the exchange between the lanes nor the products with o.  Weights
-    // are then at most 2^kSlack, well inside half precision.
+    // maximum: it moves only when a score is more than 2^kSlack above where it was set, so
+    // that most steps need neither the exchange between the lanes nor the products with o.
+    // It is set to 2^kBelow under the maximum: the largest weight is between 2^kBelow and
+    // 2^(kBelow + kSlack), inside half precision, whose 11 bits reach down to 2^-21 of it or
+    // less and whose last step is 2^-32 of it (from 1 on up they would reach 2^-14 and 2^-25).
     float top = w[0][0];
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, w[n][e]);
     top *= cs;
-    if (__any(top > m + kSlack)) {
-      const float m2 = fmaxf(m, max_over_groups(top));
+    if (__any(top > m + (kBelow + kSlack))) {
+      const float m2 = fmaxf(m, max_over_groups(top) - kBelow);
       const float f = m2 == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
       m = m2;
       l *= f;

@@ -498,8 +498,9 @@ size_t fos_paged_decode_counter_bytes(void);
  * pages hold in places that are not visible does not matter (NaN included); q and the
  * visible rows must be finite (a NaN score is not lost: the head's out and lse are NaN).
  * The scores' products of q with the stored values are exact, whatever the range within a
- * query; statistics and sums are fp32; results do not depend
- * on what else the GPU runs (no atomic sums).
+ * query; statistics and sums are fp32.  A weight exp(s_j - lse) meets v_j rounded: to 16
+ * bits over a bf16 cache; over an NVFP4 cache to 11, or by 2^-32 of the largest weight
+ * where that is more.  Results do not depend on what else the GPU runs (no atomic sums).
  *   q_bf16: [num_seqs][num_q_heads][head_dim], sequence stride q_stride elements;
  *   block_table: int32 [num_seqs][pages_per_seq], row stride table_stride elements;
  *   out_bf16 [num_seqs][num_q_heads][head_dim] contiguous; lse fp32

@@ -125,3 +125,27 @@ def test_decode_scores_of_zero_under_any_scale(fos, fmt, q):
     out, lse = fos.paged_decode(torch.full((1, 1, 64), q, dtype=torch.bfloat16, device=DEV), cache, *args,
                                 scale=3.4e38, return_lse=True)
     T.check_attention(out[0], lse[0], np.zeros((1, 64)), np.zeros((n, 1, 64)), T.N_rows(cache, "v")[:n], 1.0)
+
+
+@FMTS
+@pytest.mark.parametrize("n", [3, 60, 64, 1000])
+@pytest.mark.parametrize("gap", [8.0, 12.0, 16.0, 24.0, 28.0, 30.0, 33.0, 36.0, 56.0])
+def test_decode_beside_a_token_that_takes_the_weight(fos, fmt, n, gap):
+    """The first token's score is about ``gap`` above all others and its value is 0: the output
+    is what the others leave.  A weight may be rounded to 11 bits, or by 2^-32 of the largest
+    weight if that is more."""
+    Hq, Hkv, D = 4, 2, 64
+    k = W.random_bf16(n, Hkv * D, 1, "normal", scale=0.25).view(n, Hkv, D)
+    v = W.random_bf16(n, Hkv * D, 2, "uniform").view(n, Hkv, D) + 2.0
+    q = torch.ones(Hq, D, dtype=torch.bfloat16)
+    k[0], v[0] = gap / D, 0.0
+    cache, args = one_sequence(fos, fmt, k.bfloat16(), v.bfloat16())
+    out, lse = fos.paged_decode(q[None].to(DEV), cache, *args, scale=1.0, return_lse=True)
+    kk, vv = (T.N_rows(cache, name)[:n] for name in "kv")
+    ref, rl, A, V, E = S.attend_ref64(f64(q), kk, vv, 1.0)
+    dS, adds = (D + 8) * U * A, (n / 4 + 64) * U
+    rel = 2 * dS + 2.0 ** -20 + adds + 2.0 ** -11
+    low = n * 2.0 ** -32 * np.abs(vv).max(axis=0).repeat(2, axis=0) / E[:, None]
+    within(f64(out[0]), ref, 2.0 ** -8 * np.abs(ref) + (rel[:, None] * V + low) * (1 + 2.0 ** -8)
+           + 2.0 ** -133, "out")
+    within(f64(lse[0]), rl, dS + 2.0 ** -20 + adds + 4 * U * np.abs(rl), "lse")
