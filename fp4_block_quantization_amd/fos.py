@@ -7,6 +7,8 @@ module raises.
 
 Low-level functions carry the C names (fos_quantize, fos_dequantize, ...) and take
 device tensors; ``quantize`` / ``dequantize`` / ``qlinear_fwd`` allocate the outputs.
+The calls that serve one token at a time run on their tensors' device; all others want it to
+be the current one (``torch.cuda.device``).
 """
 from __future__ import annotations
 
@@ -555,6 +557,20 @@ _is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
                         torch.cuda.is_current_stream_capturing)
 
 
+# A launch goes to the current device, whichever device its stream and its tensors are of.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _with_device(index: int, fn, *args):
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+def _on(index: int, fn):
+    """fn, called with device ``index`` as the current one."""
+    return functools.partial(_with_device, index, fn)
+
+
 _OUT_CODE = {torch.float32: FOS_OUT_F32, torch.bfloat16: FOS_OUT_BF16}
 
 
@@ -599,9 +615,12 @@ def wlinear_fwd(x: torch.Tensor, wq: NVFP4Tensor, bias: Optional[torch.Tensor] =
     if t.dtype != _F32 or t.numel() != 1 or t.get_device() != x.get_device():
         raise ValueError("tensor_scale must be a one-element fp32 tensor on x's device")
     dev, M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 16)
-    _check(_lib.fos_wlinear_fwd(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
-                                t.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K,
-                                _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(dev)),
+    call = _lib.fos_wlinear_fwd
+    if dev != _current_device():
+        call = _on(dev, call)
+    _check(call(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
+                t.data_ptr(), None if bias is None else bias.data_ptr(), M, N, K,
+                _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(dev)),
            "fos_wlinear_fwd")
     return y
 
@@ -611,9 +630,12 @@ def mx_wlinear_fwd(x: torch.Tensor, wq: MXFP4Tensor, bias: Optional[torch.Tensor
                    ) -> torch.Tensor:
     """wlinear_fwd for an MXFP4 weight record."""
     dev, M, N, K, stride, y = _wlinear_args(x, wq, bias, out_dtype, out, 32)
-    _check(_lib.fos_mx_wlinear_fwd(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
-                                   None if bias is None else bias.data_ptr(), M, N, K,
-                                   _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(dev)),
+    call = _lib.fos_mx_wlinear_fwd
+    if dev != _current_device():
+        call = _on(dev, call)
+    _check(call(x.data_ptr(), stride, wq.data.data_ptr(), wq.scales.data_ptr(),
+                None if bias is None else bias.data_ptr(), M, N, K,
+                _OUT_CODE[out_dtype], y.data_ptr(), _raw_stream(dev)),
            "fos_mx_wlinear_fwd")
     return y
 
@@ -717,8 +739,11 @@ def kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     cache's tensor scales.  Slots of one call must be distinct."""
     T = _check_slots(cache, slots)
     k_stride, v_stride = _check_rows(cache, k, T, "k"), _check_rows(cache, v, T, "v")
-    _check(_lib.fos_kv_append(cache._ref, _KV_RULES[rule], k.data_ptr(), k_stride, v.data_ptr(),
-                              v_stride, slots.data_ptr(), T, _raw_stream(cache._index)),
+    call = _lib.fos_kv_append
+    if cache._index != _current_device():
+        call = _on(cache._index, call)
+    _check(call(cache._ref, _KV_RULES[rule], k.data_ptr(), k_stride, v.data_ptr(),
+                v_stride, slots.data_ptr(), T, _raw_stream(cache._index)),
            "fos_kv_append")
 
 
@@ -728,8 +753,11 @@ def kv_gather(cache: PagedKVCache, slots: torch.Tensor) -> Tuple[torch.Tensor, t
     T, H, D = _check_slots(cache, slots), cache.num_kv_heads, cache.head_dim
     k = torch.empty(T, H, D, dtype=_BF16, device=cache.device)
     v = torch.empty(T, H, D, dtype=_BF16, device=cache.device)
-    _check(_lib.fos_kv_gather(cache._ref, slots.data_ptr(), T, k.data_ptr(), H * D, v.data_ptr(),
-                              H * D, _raw_stream(cache._index)), "fos_kv_gather")
+    call = _lib.fos_kv_gather
+    if cache._index != _current_device():
+        call = _on(cache._index, call)
+    _check(call(cache._ref, slots.data_ptr(), T, k.data_ptr(), H * D, v.data_ptr(),
+                H * D, _raw_stream(cache._index)), "fos_kv_gather")
     return k, v
 
 
@@ -752,11 +780,11 @@ def paged_decode_workspace(B: int, Hq: int, Hkv: int, D: int, device="cuda") -> 
     return ws
 
 
-def _decode_workspace(device: torch.device, stream: int, sizes) -> torch.Tensor:
+def _decode_workspace(device: torch.device, stream: int, capturing: bool, sizes) -> torch.Tensor:
     """The current stream's scratch for paged_decode, grown by powers of two.  A captured
     call gets one of its own, cleared in the graph: the graph may be replayed on another
     stream, or later than the next eager call on this one."""
-    if _is_capturing():
+    if capturing:
         return paged_decode_workspace(*sizes, device=device)
     key = (device.index, stream)
     ws = _decode_workspaces.get(key)
@@ -804,13 +832,15 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous bf16 tensor of q's shape on the cache's device")
     lse = q.new_empty(B, Hq, dtype=_F32) if return_lse else None
-    stream = _raw_stream(dev)
+    stream, call, capturing = _raw_stream(dev), _lib.fos_paged_decode, _is_capturing
+    if dev != _current_device():
+        call, capturing = _on(dev, call), _on(dev, capturing)
     if ws is None:
-        ws = _decode_workspace(cache.device, stream, (B, Hq, cache.num_kv_heads, D))
+        ws = _decode_workspace(cache.device, stream, capturing(), (B, Hq, cache.num_kv_heads, D))
     elif ws.dtype != _U8 or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on the cache's device")
-    _check(_lib.fos_paged_decode(cache._ref, q.data_ptr(), s[0], B, Hq, block_table.data_ptr(), t[0],
-                                 pages, seq_lens.data_ptr(), D ** -0.5 if scale is None else scale,
-                                 int(window), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), stream), "fos_paged_decode")
+    _check(call(cache._ref, q.data_ptr(), s[0], B, Hq, block_table.data_ptr(), t[0],
+                pages, seq_lens.data_ptr(), D ** -0.5 if scale is None else scale,
+                int(window), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                ws.data_ptr(), ws.numel(), stream), "fos_paged_decode")
     return (out, lse) if return_lse else out

@@ -12,7 +12,8 @@
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The library never
  *     allocates, frees or keeps a pointer after returning.
- *   - `stream` is a hipStream_t (NULL = the default stream).  Calls are
+ *   - `stream` is a hipStream_t (NULL = the default stream) of the current HIP device,
+ *     which is also the device of the pointers.  Calls are
  *     stream-ordered and asynchronous: the status reports argument validation and
  *     launch errors only; faults in the kernels surface at the caller's next sync.
  *   - Validation runs before any HIP call; a non-FOS_OK status means nothing was

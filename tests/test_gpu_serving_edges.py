@@ -11,6 +11,7 @@ import test_gpu_serving as T
 from fp4_block_quantization_amd import workloads as W
 from oracle import serving as S
 from test_gpu_serving import DEV, FMTS, U, dev, f64, fos, within  # noqa: F401
+from test_serving_abi import Devices
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +150,32 @@ def test_decode_beside_a_token_that_takes_the_weight(fos, fmt, n, gap):
     within(f64(out[0]), ref, 2.0 ** -8 * np.abs(ref) + (rel[:, None] * V + low) * (1 + 2.0 ** -8)
            + 2.0 ** -133, "out")
     within(f64(lse[0]), rl, dS + 2.0 ** -20 + adds + 4 * U * np.abs(rl), "lse")
+
+
+def test_every_call_runs_on_the_device_of_its_tensors(fos, monkeypatch):
+    """With another device current, each call makes its tensors' device current for its launch
+    and for what it asks about the stream's capture."""
+    t = torch.ones(1, device=DEV)
+    cache = fos.kv_cache(4, 16, 2, 64, "nvfp4", t, t, device=DEV)
+    x = torch.ones(3, 128, dtype=torch.bfloat16, device=DEV)
+    k, slots = x.view(3, 2, 64), torch.arange(3, device=DEV)
+    table = torch.arange(4, dtype=torch.int32, device=DEV).expand(3, 4).contiguous()
+    lens = torch.full((3,), 3, dtype=torch.int32, device=DEV)
+    w, mx = fos.quantize(x), fos.mx_quantize(x)
+    calls = [lambda: fos.wlinear_fwd(x, w), lambda: fos.mx_wlinear_fwd(x, mx),
+             lambda: fos.kv_append(cache, k, k, slots), lambda: fos.kv_gather(cache, slots),
+             lambda: fos.paged_decode(k, cache, table, lens)]
+    want = [f() for f in calls]
+    index = torch.device(DEV).index
+    devices = Devices(monkeypatch, current=index + 5)
+    for f, y in zip(calls, want):
+        devices.entered.clear()
+        got = f()
+        assert devices.entered and set(devices.entered) == {index}
+        for a, b in zip(got if isinstance(got, tuple) else (got,), y if isinstance(y, tuple) else (y,)):
+            assert a is b is None or torch.equal(a, b)
+    devices.current = index
+    devices.entered.clear()
+    for f in calls:
+        f()
+    assert not devices.entered

@@ -1,6 +1,7 @@
 """Refusals of the token-serving entry points, which need no GPU: bad arguments get the
 documented status before any HIP call (the pointers are never dereferenced), and the
 binding refuses tensors that the library could not address."""
+import contextlib
 import ctypes
 
 import pytest
@@ -168,3 +169,26 @@ def test_too_many_kv_heads():
     assert append(c, ks=width, vs=width, T=1) == SHAPE
     assert gather(c, ks=width, vs=width, T=1) == SHAPE
     assert gather(cache(num_kv_heads=65536, num_pages=0, head_dim=32), T=0) == OK
+
+
+class Devices:
+    """torch.cuda.device as a record of what was made current."""
+
+    def __init__(self, monkeypatch, current):
+        self.current, self.entered = current, []
+        monkeypatch.setattr(fos, "_current_device", lambda: self.current)
+        monkeypatch.setattr(torch.cuda, "device", self.enter)
+
+    @contextlib.contextmanager
+    def enter(self, index):
+        before, self.current = self.current, index
+        self.entered.append(index)
+        yield
+        self.current = before
+
+
+def test_calls_run_with_their_device_current(monkeypatch):
+    devices = Devices(monkeypatch, current=1)
+    report = lambda *args: (devices.current, args)
+    assert fos._on(3, report)("a", 2) == (3, ("a", 2))
+    assert devices.entered == [3] and devices.current == 1
