@@ -9,6 +9,8 @@ import torch
 
 import test_gpu_serving as T
 from fp4_block_quantization_amd import workloads as W
+from oracle import formats as F
+from oracle import nvfp4 as N
 from oracle import serving as S
 from test_gpu_serving import DEV, FMTS, U, dev, f64, fos, within  # noqa: F401
 from test_serving_abi import Devices
@@ -44,6 +46,81 @@ def test_wlinear_longest_inner_dimension(fos, fmt):
                                np.float32(0.01) if fmt == "nvfp4" else None, np.ones(1))
     # the other products are zeros: only sums with these blocks' values round
     within(f64(y), ref, U * np.abs(ref) + (32 * blocks + 8) * U * mag, "y")
+
+
+# More than 1024 weight rows and more than four activation rows are products of 16x16x32 tiles
+# (fewer weight rows fit the GPU as groups of 4 or 8 that get a CU each and take the kernel
+# of few rows).
+
+def records(fmt):
+    return T.nv_weight if fmt == "nvfp4" else T.mx_weight
+
+
+def linear(fos, fmt):
+    return fos.wlinear_fwd if fmt == "nvfp4" else fos.mx_wlinear_fwd
+
+
+def some_rows(n):
+    return np.unique(np.concatenate([np.arange(0, n, 37), np.arange(16), np.arange(n - 70, n)]))
+
+
+@pytest.mark.parametrize("m", [5, 16, 24, 40, 64])
+@pytest.mark.parametrize("k", [16, 48, 80, 1008, 4112])
+def test_wlinear_tiles_of_rows_that_end_in_half_a_load(fos, m, k):
+    """K a multiple of 16 but not of 32: a weight row starts at 8-byte alignment."""
+    n = 1203
+    data, scales, t, w = T.nv_weight(fos, n, k, m + k)
+    x = W.random_bf16(m, k, k, "normal").to(DEV)
+    T.check_linear(fos.wlinear_fwd(x, w, out_dtype=torch.float32), x, data, scales, t, rows=some_rows(n))
+
+
+@pytest.mark.parametrize("m,n", [(5, 1203), (16, 2050), (9, 6000), (16, 8200), (250, 1000), (17, 12300),
+                                 (61, 4099), (33, 16400), (100, 6000)])
+@pytest.mark.parametrize("fmt,k,out", [("nvfp4", 304, torch.float32), ("nvfp4", 1056, torch.bfloat16),
+                                       ("mxfp4", 1056, torch.float32)])
+def test_wlinear_tiles_with_bias_strided_rows_and_given_output(fos, m, n, fmt, k, out):
+    """Sizes for which the GPU is filled with each of the tiles; NaN next to the activation
+    rows, and rows of the output next to the given ones that stay."""
+    data, scales, t, w = records(fmt)(fos, n, k, m + n)
+    wide = torch.full((m, k + 72), float("nan"), dtype=torch.bfloat16, device=DEV)
+    x = wide[:, 40:40 + k]
+    x.copy_(W.random_bf16(m, k, n, "normal"))
+    bias = W.random_bf16(1, n, 3, "normal")[0].to(DEV)
+    full = torch.full((m + 2, n), 7.0, dtype=out, device=DEV)
+    y = linear(fos, fmt)(x, w, bias=bias, out_dtype=out, out=full[1:m + 1])
+    rows = some_rows(n)
+    ref, mag = S.wlinear_ref64(f64(x), data, scales, t, rows=rows)
+    ref, mag = ref + f64(bias)[rows], mag + np.abs(f64(bias)[rows])
+    rnd = 2.0 ** -8 if out == torch.bfloat16 else U
+    within(f64(y[:, dev(rows)]), ref, rnd * np.abs(ref) + (k + 8) * U * mag * (1 + rnd), "y")
+    assert not y.isnan().any() and (full[0] == 7).all() and (full[m + 1] == 7).all()
+
+
+@pytest.mark.parametrize("m", [6, 32, 64])
+@pytest.mark.parametrize("block", ["1d", "2d"])
+def test_wlinear_tiles_of_wide_values(fos, m, block):
+    """Activations from 2^-100 to 2^100 side by side, a weight that uses the whole range of
+    block scales, and a 2D record."""
+    n, k = 1200, 1024
+    data, scales, t, w = T.nv_weight(fos, n, k, 9, N.Config(block=block), scale=1.0)
+    g = np.random.RandomState(m)
+    x = np.ldexp(g.randn(m, k), g.randint(-100, 100, (m, k)))
+    x = T.to_gpu_bf16(F.f32_to_bf16_bits(x.astype(np.float32)))
+    T.check_linear(fos.wlinear_fwd(x, w, out_dtype=torch.float32), x, data, scales, t, rows=some_rows(n))
+
+
+@pytest.mark.parametrize("m", [9, 33, 64])
+@pytest.mark.parametrize("lo,hi,e", [(0, 7, 100), (7, 120, 60), (100, 150, 0), (130, 228, -60), (228, 253, -100)])
+def test_mx_wlinear_tiles_of_every_block_scale(fos, m, lo, hi, e):
+    """E8M0 codes from 0 (2^-127, where the weights are below bf16's normal range) to the
+    largest whose products with E2M1 are finite."""
+    n, k = 1200, 640
+    g = np.random.RandomState(m)
+    data = g.randint(0, 256, (n, k // 2)).astype(np.uint8)
+    scales = g.randint(lo, hi, (n, k // 32)).astype(np.uint8)
+    x = T.to_gpu_bf16(F.f32_to_bf16_bits(np.ldexp(g.randn(m, k), e).astype(np.float32)))
+    y = fos.mx_wlinear_fwd(x, fos.MXFP4Tensor(dev(data), dev(scales)), out_dtype=torch.float32)
+    T.check_linear(y, x, data, scales, None, rows=some_rows(n))
 
 
 # ------------------------------------------------------------------ attention
