@@ -256,3 +256,22 @@ def test_every_call_runs_on_the_device_of_its_tensors(fos, monkeypatch):
     for f in calls:
         f()
     assert not devices.entered
+
+
+@FMTS
+def test_decode_batch_of_several_launches(fos, fmt):
+    """64 kv heads and 1030 sequences are more segments than a launch counts (65536): the
+    second one starts at sequence 1024.  Long sequences on both sides of it leave partial
+    results."""
+    lens = np.random.RandomState(3).randint(0, 20, 1030)
+    lens[[0, 500, 1022, 1023, 1024, 1027, 1029]] = 700, 24000, 0, 1500, 1300, 900, 600
+    T.run_decode(fos, fmt, 1030, 64, 64, 32, 16, lens, seed=51)
+
+
+@FMTS
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [(800, 800, 32, [40, 0, 600]), (300, 300, 160, [30, 5, 300]),
+                                           (1036, 518, 128, [17, 270]), (5100, 300, 160, [3, 290])])
+def test_decode_more_head_groups_than_fit_at_once(fos, fmt, Hq, Hkv, D, lens):
+    """Head groups that are more than the workgroups the GPU holds (256 to 768, by head dim):
+    one workgroup of each walks every sequence."""
+    T.run_decode(fos, fmt, len(lens), Hq, Hkv, D, 16, lens, seed=52)
