@@ -275,3 +275,18 @@ def test_decode_more_head_groups_than_fit_at_once(fos, fmt, Hq, Hkv, D, lens):
     """Head groups that are more than the workgroups the GPU holds (256 to 768, by head dim):
     one workgroup of each walks every sequence."""
     T.run_decode(fos, fmt, len(lens), Hq, Hkv, D, 16, lens, seed=52)
+
+
+def test_decode_infinities_where_masked(fos, monkeypatch):
+    """Infinities of either sign, alone, together and beside NaN, past the length, before the
+    window and in foreign pages of a bf16 cache leave no trace, at every offset of the length
+    inside a tile."""
+    inf, nan = float("inf"), float("nan")
+    for values in ((inf,), (-inf,), (inf, -inf), (inf, nan, -inf, 3.0e38)):
+        def fill(cache):
+            for x in (cache.k, cache.v):
+                x.view(-1)[:] = torch.tensor(values, device=DEV).bfloat16().repeat(
+                    -(-x.numel() // len(values)))[:x.numel()]
+        monkeypatch.setattr(T, "fill_garbage", fill)
+        T.run_decode(fos, "bf16", 40, 2, 2, 64, 16, list(range(90, 130)), window=45, seed=15)
+        T.run_decode(fos, "bf16", 7, 6, 3, 96, 16, [90, 16, 1, 333, 700, 64, 65], holes=True, seed=8)
