@@ -27,7 +27,7 @@
 // read the same pages at the same time.  A sequence that fell to several runs leaves partial
 // (m, l, o) in the workspace, and the last workgroup to finish joins them (of many, in two
 // levels) in their order: no second launch, nobody waits, and the order of every sum
-// depends on the lengths alone.
+// depends on the lengths and the call's sizes (heads, dim, batch, width of the table) alone.
 //
 // Bound and figures (K and V bytes over the time of a launch).  bf16: memory; 32 sequences
 // of up to 8192 tokens, 32 heads over 8 of 128: 90 us, 6.0 TB/s of 6.8 that a plain read

@@ -1,6 +1,7 @@
 // Weight-only quantized linear layer: bf16 activations times a 4-bit weight record,
 //   y[m][n] = t * sum_k x[m][k] E(w[n][k]) D(s[n][k / block]) + bias[n].
-// The weight is read once; its bytes bound the call (x and y are small beside it).
+// The weight is read once for each tile of activation rows (up to 64); with few rows its
+// bytes bound the call (x and y are small beside it).
 // Measured, a launch included (1.8 us when empty), where a plain read of the weight takes
 // 5.5 us: 1 x 12288 x 4096 NVFP4 8.0 us, 16 x 12288 x 4096 9.0 us; 1 x 256 x 256 2.8 us.  With more rows the
 // conversions and the passage through LDS bound it: 61 x 4099 x 4112 12.3 us, 64 x 12288 x
@@ -10,7 +11,7 @@
 // are exact in bf16, products are exact in fp32, and every sum is fp32; y is rounded once.
 // Two kernels, by the number of activation rows (shape_of): few on 4x4x4 products, where a
 // lane keeps a weight row to itself, and more on 16x16x32 tiles, where a weight is
-// converted once for up to 64 activation rows.
+// converted once for the 16, 32 or 64 activation rows of a tile.
 #include "serving.hpp"
 
 namespace fos {

@@ -403,14 +403,16 @@ fos_status fos_mx_qlinear_fwd(const uint8_t* a_data, const uint8_t* a_scales,
  *   Y[m][n] = RN( t_w * sum_k X[m][k] * (E*D)_w[n][k] + bias[n] )
  * with exact products, fp32 sums (in an unspecified order that is the same for every
  * call of the same shape), and one rounding to the output type.  Made for few rows
- * (M = 1 is a token of one sequence, 64 a large batch); any M is accepted.  2D records
+ * (M = 1 is a token of one sequence, 64 a large batch); more are accepted.  2D records
  * work (they carry one scale per 16 values too); a record made with the Hadamard
  * transform needs an activation that carries the same transform.
  *   X: bf16, row m at x_bf16 + m * x_stride elements, 16-byte aligned, x_stride >= K
  *   and a multiple of 8 (both for M > 1).  w_data [N][K/2] 16-byte aligned, w_scales
  *   [N][K/16] 4-byte aligned.  bias_bf16 [N] or NULL.  y [M][N] of out_dtype
  *   (FOS_OUT_F32: 4-byte aligned, FOS_OUT_BF16: 2-byte).
- *   M >= 0 (0: nothing is launched), N >= 1, K >= 16 and K % 16 == 0.
+ *   M >= 0 (0: nothing is launched), N >= 1, K >= 16 and K % 16 == 0, each below 2^31;
+ *   FOS_E_SHAPE also where a launch would take 2^32 work-items and more (N from about
+ *   2^28 on, M*N from about 2^34).
  * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_HIP. */
 fos_status fos_wlinear_fwd(const void* x_bf16, int64_t x_stride, const uint8_t* w_data,
                            const uint8_t* w_scales, const float* w_tensor_scale,
