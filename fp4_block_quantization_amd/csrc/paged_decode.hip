@@ -32,8 +32,9 @@
 // Bound and figures (K and V bytes over the time of a launch).  bf16: memory; 32 sequences
 // of up to 8192 tokens, 32 heads over 8 of 128: 90 us, 6.0 TB/s of 6.8 that a plain read
 // reaches.  NVFP4: the loads and the conversions of their step share the time; 16 x up to
-// 32768 tokens, 64 heads over 8 of 128: 61 us, 5.0 TB/s (55 us with the arithmetic left
-// out).  Few tokens (1 x 200): 6 us, of which an empty launch is 2.
+// 32768 tokens, 64 heads over 8 of 128: 63 us, 4.9 TB/s (55 us with the arithmetic left
+// out; VALU work in 62% of the cycles).  Few tokens (1 x 200): 6.5 us, of which an empty
+// launch is 2.
 #include <cfloat>
 
 #include "serving.hpp"

@@ -3,9 +3,9 @@
 // The weight is read once for each tile of activation rows (up to 64); with few rows its
 // bytes bound the call (x and y are small beside it).
 // Measured, a launch included (1.8 us when empty), where a plain read of the weight takes
-// 5.5 us: 1 x 12288 x 4096 NVFP4 8.0 us, 16 x 12288 x 4096 9.0 us; 1 x 256 x 256 2.8 us.  With more rows the
-// conversions and the passage through LDS bound it: 61 x 4099 x 4112 12.3 us, 64 x 12288 x
-// 4096 17 us.
+// 5.5 us: 1 x 12288 x 4096 NVFP4 8.0 to 8.4 us, 16 x 12288 x 4096 9.1 us; 1 x 256 x 256 2.8
+// us.  With more rows the conversions and the passage through LDS bound it: 61 x 4099 x 4112
+// 12.2 us (of 256 CUs 172 have work), 64 x 12288 x 4096 17 us.
 //
 // Matrix form: E2M1 x E4M3 has at most 6 significant bits and E2M1 x 2^e two, so weights
 // are exact in bf16, products are exact in fp32, and every sum is fp32; y is rounded once.

@@ -607,7 +607,8 @@ def wlinear_fwd(x: torch.Tensor, wq: NVFP4Tensor, bias: Optional[torch.Tensor] =
                 ) -> torch.Tensor:
     """Y = X deq(W)^T (+ bias) for a bf16 activation X [M, K], which is not quantized, and
     a weight record W [N, K]: the layer of a decode step (M = the sequences of the
-    batch; made for up to 64).  X's rows may be strided.  ``bias``: bf16 [N];
+    batch; made for up to 64; from several hundred on, ``dequantize`` and a dense product
+    are faster).  X's rows may be strided.  ``bias``: bf16 [N];
     ``out``: optional [M, N] destination of ``out_dtype`` (bf16 or fp32)."""
     if wq.hadamard_seed is not None:
         raise ValueError("the weight record carries a Hadamard transform that x does not")
