@@ -16,9 +16,12 @@
 //                       (v_mfma_scale_f32_32x32x64_f8f6f4, both operands E2M1): the
 //                       packed bytes and E8M0 scales go to the MFMA as they are, with
 //                       no conversion; 256x256 tiles, K staged through LDS in 256-wide
-//                       double-buffered stages as in the NVFP4 qlinear kernel.
+//                       double-buffered stages as in the NVFP4 qlinear kernel; ends in a
+//                       plain store or an epilogue, with a gate's rows as there.
 #include "device_common.hpp"
+#include "feedforward.hpp"
 #include "gemm_common.hpp"
+#include "gemm_epilogue.hpp"
 #include "kernels.hpp"
 
 namespace fos {
@@ -162,6 +165,7 @@ struct MxOperands {
   __amdgpu_buffer_rsrc_t a, sa, b, sb;
   uint32_t oa[2], ob[2];      // per-lane data offsets for even / odd row-groups
   uint32_t osa, osb;          // per-lane scale offsets
+  uint32_t ou[2], osu;        // with a gate: of the other projection's rows
   uint32_t group_stride;      // bytes between data row-groups (8 rows)
   uint32_t scale_stride;      // bytes between scale row-groups (32 rows)
 };
@@ -169,6 +173,7 @@ struct MxOperands {
 // This wave's share of one stage: 64 rows of each operand, 8 + 8 data copies (8 rows
 // of 128 bytes each) and 2 + 2 scale copies (32 rows of 8 bytes each), issued as two
 // halves of 10 copies (half j: data row-groups 4j..4j+3 and scale row-group j).
+template <bool kGate>
 __device__ __forceinline__ void mx_stage_load_half(MxStage& st, const MxOperands& p, int sc,
                                                    int wave, int j) {
   const int od = sc * kMxRowBytes, os = sc * kMxRowScales;
@@ -176,15 +181,22 @@ __device__ __forceinline__ void mx_stage_load_half(MxStage& st, const MxOperands
   for (int q = 4 * j; q < 4 * j + 4; ++q) {
     const int so = od + q * (int)p.group_stride;
     dma16(p.a, st.a + (64 * wave + 8 * q) * kMxRowBytes, p.oa[q & 1], so);
-    dma16(p.b, st.b + (64 * wave + 8 * q) * kMxRowBytes, p.ob[q & 1], so);
+    // with a gate, row-groups 4 to 7 are the other projection's
+    if (kGate && j)
+      dma16(p.b, st.b + (64 * wave + 8 * q) * kMxRowBytes, p.ou[q & 1],
+            od + (q - 4) * (int)p.group_stride);
+    else
+      dma16(p.b, st.b + (64 * wave + 8 * q) * kMxRowBytes, p.ob[q & 1], so);
   }
   const int so = os + j * (int)p.scale_stride;
   dma4(p.sa, st.sa + (64 * wave + 32 * j) * kMxRowScales, p.osa, so);
-  dma4(p.sb, st.sb + (64 * wave + 32 * j) * kMxRowScales, p.osb, so);
+  if (kGate && j) dma4(p.sb, st.sb + (64 * wave + 32 * j) * kMxRowScales, p.osu, os);
+  else dma4(p.sb, st.sb + (64 * wave + 32 * j) * kMxRowScales, p.osb, so);
 }
+template <bool kGate>
 __device__ __forceinline__ void mx_stage_load(MxStage& st, const MxOperands& p, int sc, int wave) {
-  mx_stage_load_half(st, p, sc, wave, 0);
-  mx_stage_load_half(st, p, sc, wave, 1);
+  mx_stage_load_half<kGate>(st, p, sc, wave, 0);
+  mx_stage_load_half<kGate>(st, p, sc, wave, 1);
 }
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -207,7 +219,7 @@ __device__ __forceinline__ i32x8 mx_operand(const uint8_t* base, int row, int g)
 // stream for hundreds of cycles while the matrix pipe idles; left to itself the
 // scheduler also reads each operand right before its first use and waits for it.)
 constexpr int NKS = kMxSuper / 64;
-template <bool kLoad>
+template <bool kLoad, bool kGate>
 __device__ __forceinline__ void mx_stage_mma(const MxStage& st, f32x16 (&acc)[4][4], int ra,
                                              int rb, int h, MxStage& next, const MxOperands& p,
                                              int next_sc, int wave) {
@@ -240,7 +252,7 @@ __device__ __forceinline__ void mx_stage_mma(const MxStage& st, f32x16 (&acc)[4]
       }
     }
     const bool copies = kLoad && s < 2;
-    if (copies) mx_stage_load_half(next, p, next_sc, wave, s);
+    if (copies) mx_stage_load_half<kGate>(next, p, next_sc, wave, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -282,10 +294,13 @@ __device__ __forceinline__ void mx_stage_mma(const MxStage& st, f32x16 (&acc)[4]
   __builtin_amdgcn_sched_barrier(0);
 }
 
+template <int kEpi>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
 void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ as,
                     const uint8_t* __restrict__ bd, const uint8_t* __restrict__ bs, int M, int N,
-                    int K, int tiles_m, int tiles_n, uint16_t* __restrict__ y) {
+                    int K, int tiles_m, int tiles_n, void* __restrict__ y, EpilogueArgs e) {
+  constexpr bool kGate = kEpi == kGated;
+  constexpr int kProj = kGate ? 2 : 1;   // weight rows of one column of Y
   __shared__ __attribute__((aligned(16))) MxStage st0;
   __shared__ __attribute__((aligned(16))) MxStage st1;
   const TileCoord tc = tile_of(blockIdx.x, tiles_m, tiles_n);
@@ -299,8 +314,8 @@ void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
   MxOperands p;
   p.a = __builtin_amdgcn_make_buffer_rsrc((void*)ad, 0, (int)((uint32_t)M * kb2), kRsrcWord3);
   p.sa = __builtin_amdgcn_make_buffer_rsrc((void*)as, 0, (int)((uint32_t)M * kb32), kRsrcWord3);
-  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)bd, 0, (int)((uint32_t)N * kb2), kRsrcWord3);
-  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)bs, 0, (int)((uint32_t)N * kb32), kRsrcWord3);
+  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)bd, 0, (int)((uint32_t)(kProj * N) * kb2), kRsrcWord3);
+  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)bs, 0, (int)((uint32_t)(kProj * N) * kb32), kRsrcWord3);
   {
     // data: DMA lane l of row-group q writes LDS slot (l & 7) of local row 64*wave +
     // 8*q + (l >> 3) and fetches the granule the swizzle puts there
@@ -310,13 +325,17 @@ void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
     for (int par = 0; par < 2; ++par) {
       const uint32_t g = slot ^ (((sub >> 1) + 4 * par) & 7);
       p.oa[par] = (uint32_t)(tm * kMxTile + r0) * kb2 + 16 * g;
-      p.ob[par] = (uint32_t)(tn * kMxTile + r0) * kb2 + 16 * g;
+      // with a gate the wave's 64 rows are 32 of the gate and 32 of the other projection
+      p.ob[par] = (uint32_t)(kGate ? tn * (kMxTile / 2) + 32 * wave + sub : tn * kMxTile + r0) * kb2 + 16 * g;
+      p.ou[par] = p.ob[par] + (uint32_t)N * kb2;
     }
     p.group_stride = 8 * kb2;
     // scales: lane l of copy j fetches dword l & 1 of local row 64*wave + 32*j + l/2
     const int srow = 64 * wave + (lane >> 1);
     p.osa = (uint32_t)(tm * kMxTile + srow) * kb32 + 4 * (lane & 1);
-    p.osb = (uint32_t)(tn * kMxTile + srow) * kb32 + 4 * (lane & 1);
+    p.osb = (uint32_t)(kGate ? tn * (kMxTile / 2) + 32 * wave + (lane >> 1) : tn * kMxTile + srow) * kb32 +
+            4 * (lane & 1);
+    p.osu = p.osb + (uint32_t)N * kb32;
     p.scale_stride = 32 * kb32;
   }
 
@@ -329,22 +348,42 @@ void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
   const int ra = (wave >> 1) * 128 + lr;
   const int rb = (wave & 1) * 128 + lr;
   const int nsc = K / kMxSuper;
-  mx_stage_load(st0, p, 0, wave);
+  mx_stage_load<kGate>(st0, p, 0, wave);
   int sc = 0;
   for (; sc + 1 < nsc; sc += 2) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    mx_stage_mma<true>(st0, acc, ra, rb, h, st1, p, sc + 1, wave);
+    mx_stage_mma<true, kGate>(st0, acc, ra, rb, h, st1, p, sc + 1, wave);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     // unconditional (a redundant copy of the last stage when none is left): a branch
     // here lets the compiler sink the previous stage's MFMAs past the barrier
-    mx_stage_mma<true>(st1, acc, ra, rb, h, st0, p, min(sc + 2, nsc - 1), wave);
+    mx_stage_mma<true, kGate>(st1, acc, ra, rb, h, st0, p, min(sc + 2, nsc - 1), wave);
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (sc < nsc) mx_stage_mma<false>(st0, acc, ra, rb, h, st1, p, 0, wave);
-  store_tile(y, M, N, tm, tn, wave, lr, h, 1.0f, acc);
+  if (sc < nsc) mx_stage_mma<false, kGate>(st0, acc, ra, rb, h, st1, p, 0, wave);
+  if constexpr (kEpi == kPlain) {
+    store_tile(static_cast<uint16_t*>(y), M, N, tm, tn, wave, lr, h, 1.0f, acc);
+  } else {
+    static_assert(4 * kStripBytes<4> <= sizeof(MxStage), "the strips take the first stage's place");
+    __syncthreads();   // the other waves have read their operands
+    store_fused<4, 4, kGate>(e, y, reinterpret_cast<float*>(st0.a + wave * kStripBytes<4>), M, N,
+                             tm * kMxTile + (wave >> 1) * 128,
+                             (tn * kMxTile + (wave & 1) * 128) / kProj, lane, 1.0f, acc);
+  }
+}
+
+template <int kEpi>
+hipError_t launch_mx_epi(const uint8_t* ad, const uint8_t* as, const uint8_t* bd,
+                         const uint8_t* bs, int64_t M, int64_t N, int64_t K, void* y,
+                         const EpilogueArgs& e, hipStream_t s) {
+  constexpr int kCols = kEpi == kGated ? kMxTile / 2 : kMxTile;
+  const int tiles_m = (int)((M + kMxTile - 1) / kMxTile);
+  const int tiles_n = (int)((N + kCols - 1) / kCols);
+  mx_gemm_kernel<kEpi><<<tiles_m * tiles_n, 256, 0, s>>>(ad, as, bd, bs, (int)M, (int)N, (int)K,
+                                                         tiles_m, tiles_n, y, e);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -383,11 +422,17 @@ hipError_t launch_mx_dequantize(const uint8_t* data, const uint8_t* scales, int6
 hipError_t launch_mx_gemm(const uint8_t* ad, const uint8_t* as, const uint8_t* bd,
                           const uint8_t* bs, int64_t M, int64_t N, int64_t K, uint16_t* y,
                           hipStream_t s) {
-  const int tiles_m = (int)((M + kMxTile - 1) / kMxTile);
-  const int tiles_n = (int)((N + kMxTile - 1) / kMxTile);
-  mx_gemm_kernel<<<tiles_m * tiles_n, 256, 0, s>>>(ad, as, bd, bs, (int)M, (int)N, (int)K,
-                                                   tiles_m, tiles_n, y);
-  return hipGetLastError();
+  return launch_mx_epi<kPlain>(ad, as, bd, bs, M, N, K, y, EpilogueArgs{}, s);
+}
+
+int64_t mx_epilogue_grid(const QLinearArgs& a) {
+  const int cols = a.gated ? kMxTile / 2 : kMxTile;
+  return ((a.M + kMxTile - 1) / kMxTile) * ((a.N + cols - 1) / cols);
+}
+
+hipError_t launch_mx_epilogue(const QLinearArgs& a, hipStream_t s) {
+  return (a.gated ? launch_mx_epi<kGated> : launch_mx_epi<kFused>)(
+      a.xd, a.xs, a.wd, a.ws, a.M, a.N, a.K, a.y, a.e, s);
 }
 
 }  // namespace fos

@@ -24,8 +24,15 @@
 //     from L2 into registers, three register stages deep.
 // Workgroups are remapped so that each XCD (dispatched round-robin) runs a contiguous
 // group of 4 tile-rows x all tile-columns.
+//
+// Both kernels end in a plain store or in the epilogue of gemm_epilogue.hpp (kEpi).  With a
+// gate, a tile of 256 weight rows holds 128 rows of the gate and the 128 of the other
+// projection that belong to the same columns of Y, 32 of each in turn: a wave has both
+// factors of every product in its own accumulators.
 #include "device_common.hpp"
+#include "feedforward.hpp"
 #include "gemm_common.hpp"
+#include "gemm_epilogue.hpp"
 #include "kernels.hpp"
 
 namespace fos {
@@ -128,13 +135,14 @@ __device__ __forceinline__ void mma_stage(const Stage<TI, TJ>& st, f32x16 (&acc)
 
 // Workgroup = 4 waves in a 2x2 arrangement; each wave owns TI x TJ MFMA tiles of
 // 32x32, so the workgroup tile is (64*TI) x (64*TJ); WAVES_PER_EU waves share a SIMD.
-template <int TI, int TJ, int STAGES, int WAVES_PER_EU>
+template <int TI, int TJ, int STAGES, int WAVES_PER_EU, int kEpi>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
                           amdgpu_waves_per_eu(WAVES_PER_EU, WAVES_PER_EU)))
 void qlinear_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restrict__ xs,
                     const float* __restrict__ xt, const uint8_t* __restrict__ wd,
                     const uint8_t* __restrict__ ws, const float* __restrict__ wt, int M, int N,
-                    int K, int tiles_m, int tiles_n, uint16_t* __restrict__ y) {
+                    int K, int tiles_m, int tiles_n, void* __restrict__ y, EpilogueArgs e) {
+  constexpr int kProj = kEpi == kGated ? 2 : 1;   // weight rows of one column of Y
   constexpr int kWM = 32 * TI, kWN = 32 * TJ;     // wave tile
   constexpr int kBM = 2 * kWM, kBN = 2 * kWN;     // workgroup tile
   // ---- tile assignment: contiguous range per XCD, grouped along M inside it
@@ -144,15 +152,15 @@ void qlinear_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restrict__ 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 31, h = lane >> 5;
   const int m0 = tm * kBM + (wave >> 1) * kWM;
-  const int n0 = tn * kBN + (wave & 1) * kWN;
+  const int n0 = (tn * kBN + (wave & 1) * kWN) / kProj;
   const uint32_t kb2 = K / 2, kb16 = K / 16;
   const uint32_t sh = 16 * h;   // this lane's scale byte pair within the dword
 
   Operands<TI, TJ> p;
   p.a = __builtin_amdgcn_make_buffer_rsrc((void*)xd, 0, (int)((uint32_t)M * kb2), kRsrcWord3);
   p.sa = __builtin_amdgcn_make_buffer_rsrc((void*)xs, 0, (int)((uint32_t)M * kb16), kRsrcWord3);
-  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)wd, 0, (int)((uint32_t)N * kb2), kRsrcWord3);
-  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)ws, 0, (int)((uint32_t)N * kb16), kRsrcWord3);
+  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)wd, 0, (int)((uint32_t)(kProj * N) * kb2), kRsrcWord3);
+  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)ws, 0, (int)((uint32_t)(kProj * N) * kb16), kRsrcWord3);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const uint32_t r = m0 + 32 * i + lr;
@@ -161,7 +169,7 @@ void qlinear_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restrict__ 
   }
 #pragma unroll
   for (int n = 0; n < TJ; ++n) {
-    const uint32_t c = n0 + 32 * n + lr;
+    const uint32_t c = kEpi == kGated ? n0 + 32 * (n >> 1) + (n & 1) * N + lr : n0 + 32 * n + lr;
     p.ob[n] = c * kb2 + 16 * h;
     p.osb[n] = c * kb16;
   }
@@ -214,6 +222,12 @@ void qlinear_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restrict__ 
   // ---- epilogue: lane (lr, h) holds, for accumulator element a, row
   // (a & 3) + 8 * (a >> 2) + 4 * h and column lr of each 32x32 tile.
   const float s = xt[0] * wt[0];
+  if constexpr (kEpi != kPlain) {
+    __shared__ __attribute__((aligned(16))) uint8_t strips[4 * kStripBytes<TJ>];
+    store_fused<TI, TJ, kEpi == kGated>(
+        e, y, reinterpret_cast<float*>(strips + wave * kStripBytes<TJ>), M, N, m0, n0, lane, s, acc);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
 #pragma unroll
@@ -223,7 +237,8 @@ void qlinear_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restrict__ 
 #pragma unroll
       for (int a = 0; a < 16; ++a) {
         const int row = m0 + 32 * i + (a & 3) + 8 * (a >> 2) + 4 * h;
-        if (row < M) y[(int64_t)row * N + col] = (uint16_t)f32_to_bf16_rne(acc[i][n][a] * s);
+        if (row < M)
+          static_cast<uint16_t*>(y)[(int64_t)row * N + col] = (uint16_t)f32_to_bf16_rne(acc[i][n][a] * s);
       }
     }
   }
@@ -256,6 +271,7 @@ struct LdsStage {
 struct LdsOperands {
   __amdgpu_buffer_rsrc_t a, sa, b, sb;
   uint32_t oa[2], ob[2];      // per-lane offsets for even / odd row-groups
+  uint32_t ou[2];             // with a gate: of the other projection's rows
   uint32_t osa, osb;          // per-lane scale-row offsets
   uint32_t group_stride;      // bytes between row-groups (8 rows)
 };
@@ -265,12 +281,18 @@ struct LdsOperands {
 // 8*q rows further on; the granule swizzle only depends on q's parity, so the
 // per-lane offset is one of two values and the rest is a scalar offset.  Part j < 8
 // copies row-group j of both operands, part 8 both scale blocks.
+template <bool kGate>
 __device__ __forceinline__ void stage_load_part(LdsStage& st, const LdsOperands& p, int sc,
                                                 int wave, int j) {
   if (j < 8) {
     const int so = sc * kRowBytes + j * (int)p.group_stride;
     dma16(p.a, st.a + (64 * wave + 8 * j) * kRowBytes, p.oa[j & 1], so);
-    dma16(p.b, st.b + (64 * wave + 8 * j) * kRowBytes, p.ob[j & 1], so);
+    // with a gate, row-groups 4 to 7 are the other projection's
+    if (kGate && j >= 4)
+      dma16(p.b, st.b + (64 * wave + 8 * j) * kRowBytes, p.ou[j & 1],
+            sc * kRowBytes + (j - 4) * (int)p.group_stride);
+    else
+      dma16(p.b, st.b + (64 * wave + 8 * j) * kRowBytes, p.ob[j & 1], so);
   } else {
     const int os = sc * kRowScales;
     dma16(p.sa, st.sa + 64 * wave * kRowScales, p.osa, os);
@@ -278,9 +300,10 @@ __device__ __forceinline__ void stage_load_part(LdsStage& st, const LdsOperands&
   }
 }
 constexpr int kLoadParts = 9;
+template <bool kGate>
 __device__ __forceinline__ void stage_load(LdsStage& st, const LdsOperands& p, int sc, int wave) {
 #pragma unroll
-  for (int j = 0; j < kLoadParts; ++j) stage_load_part(st, p, sc, wave, j);
+  for (int j = 0; j < kLoadParts; ++j) stage_load_part<kGate>(st, p, sc, wave, j);
 }
 
 template <bool kHi>
@@ -313,7 +336,7 @@ __device__ __forceinline__ void group_scales(const uint2 (&sc)[4], int gq, h2 (&
 // in k-steps 0-8, right after the k-step's first MFMA, which leaves seven k-steps for
 // them to land.  (Issued in one burst, they hold up the wave's in-order instruction
 // stream while the matrix pipe idles.)
-template <bool kLoad>
+template <bool kLoad, bool kGate>
 __device__ __forceinline__ void stage_mma(const LdsStage& st, f32x16 (&acc)[4][4], int ra,
                                           int rb, int h, LdsStage& next, const LdsOperands& p,
                                           int next_sc, int wave) {
@@ -365,7 +388,7 @@ __device__ __forceinline__ void stage_mma(const LdsStage& st, f32x16 (&acc)[4][4
       }
     }
     const bool copies = kLoad && s < kLoadParts;
-    if (copies) stage_load_part(next, p, next_sc, wave, s);
+    if (copies) stage_load_part<kGate>(next, p, next_sc, wave, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -389,11 +412,15 @@ __device__ __forceinline__ void stage_mma(const LdsStage& st, f32x16 (&acc)[4][4
   }
 }
 
+template <int kEpi>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
 void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restrict__ xs,
                         const float* __restrict__ xt, const uint8_t* __restrict__ wd,
                         const uint8_t* __restrict__ ws, const float* __restrict__ wt, int M,
-                        int N, int K, int tiles_m, int tiles_n, uint16_t* __restrict__ y) {
+                        int N, int K, int tiles_m, int tiles_n, void* __restrict__ y,
+                        EpilogueArgs e) {
+  constexpr bool kGate = kEpi == kGated;
+  constexpr int kProj = kGate ? 2 : 1;   // weight rows of one column of Y
   __shared__ __attribute__((aligned(16))) LdsStage st0;
   __shared__ __attribute__((aligned(16))) LdsStage st1;
   // ---- tile assignment: contiguous range per XCD, grouped along M inside it
@@ -410,8 +437,8 @@ void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restric
   LdsOperands p;
   p.a = __builtin_amdgcn_make_buffer_rsrc((void*)xd, 0, (int)((uint32_t)M * kb2), kRsrcWord3);
   p.sa = __builtin_amdgcn_make_buffer_rsrc((void*)xs, 0, (int)((uint32_t)M * kb16), kRsrcWord3);
-  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)wd, 0, (int)((uint32_t)N * kb2), kRsrcWord3);
-  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)ws, 0, (int)((uint32_t)N * kb16), kRsrcWord3);
+  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)wd, 0, (int)((uint32_t)(kProj * N) * kb2), kRsrcWord3);
+  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)ws, 0, (int)((uint32_t)(kProj * N) * kb16), kRsrcWord3);
   {
     // DMA lane l of row-group q writes LDS slot (l & 7) of local row 64*wave + 8*q +
     // (l >> 3); it fetches the granule that the swizzle puts in that slot:
@@ -422,11 +449,16 @@ void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restric
     for (int par = 0; par < 2; ++par) {
       const uint32_t g = slot ^ (((sub >> 1) + 4 * par) & 7);
       p.oa[par] = (uint32_t)(tm * kTileRows + r0) * kb2 + 16 * g;
-      p.ob[par] = (uint32_t)(tn * kTileRows + r0) * kb2 + 16 * g;
+      // with a gate the wave's 64 rows are 32 of the gate and 32 of the other projection
+      p.ob[par] = (uint32_t)(kGate ? tn * (kTileRows / 2) + 32 * wave + sub : tn * kTileRows + r0) * kb2 + 16 * g;
+      p.ou[par] = p.ob[par] + (uint32_t)N * kb2;
     }
     p.group_stride = 8 * kb2;
     p.osa = (uint32_t)(tm * kTileRows + 64 * wave + lane) * kb16;
-    p.osb = (uint32_t)(tn * kTileRows + 64 * wave + lane) * kb16;
+    bool up;
+    const int r = gated_row(64 * wave + lane, up);
+    p.osb = (uint32_t)(kGate ? tn * (kTileRows / 2) + r + (up ? N : 0)
+                             : tn * kTileRows + 64 * wave + lane) * kb16;
   }
 
   f32x16 acc[4][4];
@@ -442,50 +474,57 @@ void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restric
   // (so every wave's copies have landed and the other stage is no longer read), then
   // multiply while copying the next super-chunk into the other stage.  A single-exit
   // loop keeps the 256 accumulator registers in place.
-  stage_load(st0, p, 0, wave);
+  stage_load<kGate>(st0, p, 0, wave);
   int sc = 0;
   for (; sc + 1 < nsc; sc += 2) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    stage_mma<true>(st0, acc, ra, rb, h, st1, p, sc + 1, wave);
+    stage_mma<true, kGate>(st0, acc, ra, rb, h, st1, p, sc + 1, wave);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     // unconditional (a redundant copy of the last super-chunk when none is left): a
     // branch here lets the compiler sink the previous stage's MFMAs past the barrier
-    stage_mma<true>(st1, acc, ra, rb, h, st0, p, min(sc + 2, nsc - 1), wave);
+    stage_mma<true, kGate>(st1, acc, ra, rb, h, st0, p, min(sc + 2, nsc - 1), wave);
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (sc < nsc) stage_mma<false>(st0, acc, ra, rb, h, st1, p, 0, wave);
+  if (sc < nsc) stage_mma<false, kGate>(st0, acc, ra, rb, h, st1, p, 0, wave);
 
-  store_tile(y, M, N, tm, tn, wave, lr, h, xt[0] * wt[0], acc);
+  if constexpr (kEpi == kPlain) {
+    store_tile(static_cast<uint16_t*>(y), M, N, tm, tn, wave, lr, h, xt[0] * wt[0], acc);
+  } else {
+    static_assert(4 * kStripBytes<4> <= sizeof(LdsStage), "the strips take the first stage's place");
+    __syncthreads();   // the other waves have read their operands
+    store_fused<4, 4, kGate>(e, y, reinterpret_cast<float*>(st0.a + wave * kStripBytes<4>), M, N,
+                             tm * kTileRows + (wave >> 1) * 128,
+                             (tn * kTileRows + (wave & 1) * 128) / kProj, lane, xt[0] * wt[0], acc);
+  }
 }
 
-hipError_t launch_lds(const uint8_t* xd, const uint8_t* xs, const float* xt, const uint8_t* wd,
+// Output columns of a workgroup's tile.
+constexpr int tile_cols(bool gated) { return gated ? kTileRows / 2 : kTileRows; }
+
+template <int kEpi>
+hipError_t launch_epi(const uint8_t* xd, const uint8_t* xs, const float* xt, const uint8_t* wd,
                       const uint8_t* ws, const float* wt, int64_t M, int64_t N, int64_t K,
-                      uint16_t* y, hipStream_t s) {
+                      void* y, const EpilogueArgs& e, hipStream_t s) {
+  const int cols = tile_cols(kEpi == kGated);
   const int tiles_m = (int)((M + kTileRows - 1) / kTileRows);
-  const int tiles_n = (int)((N + kTileRows - 1) / kTileRows);
-  qlinear_lds_kernel<<<tiles_m * tiles_n, 256, 0, s>>>(xd, xs, xt, wd, ws, wt, (int)M, (int)N,
-                                                       (int)K, tiles_m, tiles_n, y);
-  return hipGetLastError();
-}
-
-template <int TI, int TJ, int STAGES, int WPE>
-hipError_t launch_cfg(const uint8_t* xd, const uint8_t* xs, const float* xt, const uint8_t* wd,
-                      const uint8_t* ws, const float* wt, int64_t M, int64_t N, int64_t K,
-                      uint16_t* y, hipStream_t s) {
-  constexpr int kBM = 64 * TI, kBN = 64 * TJ;
-  const int tiles_m = (int)((M + kBM - 1) / kBM);
-  const int tiles_n = (int)((N + kBN - 1) / kBN);
-  qlinear_kernel<TI, TJ, STAGES, WPE><<<tiles_m * tiles_n, 256, 0, s>>>(
-      xd, xs, xt, wd, ws, wt, (int)M, (int)N, (int)K, tiles_m, tiles_n, y);
+  const int tiles_n = (int)((N + cols - 1) / cols);
+  // K in whole 256-wide super-chunks: LDS-staged kernel; otherwise (K % 64 == 0) the
+  // register-staged kernel
+  if (K % kSuper == 0)
+    qlinear_lds_kernel<kEpi><<<tiles_m * tiles_n, 256, 0, s>>>(
+        xd, xs, xt, wd, ws, wt, (int)M, (int)N, (int)K, tiles_m, tiles_n, y, e);
+  else
+    qlinear_kernel<4, 4, 3, 1, kEpi><<<tiles_m * tiles_n, 256, 0, s>>>(
+        xd, xs, xt, wd, ws, wt, (int)M, (int)N, (int)K, tiles_m, tiles_n, y, e);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Both kernels tile the output in 256 x 256 blocks (launch_cfg<4, 4, ...>: 64 * 4).
+// Both kernels tile the output in 256 x 256 blocks (qlinear_kernel<4, 4, ...>: 64 * 4).
 int64_t qlinear_grid(int64_t M, int64_t N) {
   static_assert(64 * 4 == kTileRows, "both qlinear kernels use the same output tile");
   return ((M + kTileRows - 1) / kTileRows) * ((N + kTileRows - 1) / kTileRows);
@@ -494,10 +533,17 @@ int64_t qlinear_grid(int64_t M, int64_t N) {
 hipError_t launch_qlinear(const uint8_t* xd, const uint8_t* xs, const float* xt,
                           const uint8_t* wd, const uint8_t* ws, const float* wt, int64_t M,
                           int64_t N, int64_t K, uint16_t* y, hipStream_t s) {
-  // K in whole 256-wide super-chunks: LDS-staged kernel; otherwise (K % 64 == 0) the
-  // register-staged kernel
-  if (K % kSuper == 0) return launch_lds(xd, xs, xt, wd, ws, wt, M, N, K, y, s);
-  return launch_cfg<4, 4, 3, 1>(xd, xs, xt, wd, ws, wt, M, N, K, y, s);
+  return launch_epi<kPlain>(xd, xs, xt, wd, ws, wt, M, N, K, y, EpilogueArgs{}, s);
+}
+
+int64_t qlinear_epilogue_grid(const QLinearArgs& a) {
+  const int cols = tile_cols(a.gated);
+  return ((a.M + kTileRows - 1) / kTileRows) * ((a.N + cols - 1) / cols);
+}
+
+hipError_t launch_qlinear_epilogue(const QLinearArgs& a, hipStream_t s) {
+  return (a.gated ? launch_epi<kGated> : launch_epi<kFused>)(
+      a.xd, a.xs, a.xt, a.wd, a.ws, a.wt, a.M, a.N, a.K, a.y, a.e, s);
 }
 
 }  // namespace fos

@@ -2,7 +2,7 @@
 // key-value cache, paged attention of one new token) and the device helpers they share.
 #pragma once
 
-#include "device_common.hpp"
+#include "activation.hpp"
 
 namespace fos {
 
@@ -64,7 +64,7 @@ __device__ __forceinline__ void reset_counter(uint32_t* counter) {
     __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Weight-only linear: y[m][n] = t * sum_k x[m][k] deq(w)[n][k] (+ bias[n]).
+// Weight-only linear: y[m][n] = t * sum_k x[m][k] deq(w)[n][k] (+ bias[n]), or an epilogue of it.
 struct WLinearArgs {
   const uint16_t* x;       // bf16, row m at x + m * x_stride
   int64_t x_stride;        // elements
@@ -73,8 +73,10 @@ struct WLinearArgs {
   const float* wt;         // device fp32 (NVFP4) or null (MXFP4)
   const uint16_t* bias;    // bf16 [N] or null
   void* y;                 // [M][N] bf16 or fp32
-  int64_t M, N, K;
+  int64_t M, N, K;         // N: weight rows, with a gate two for each column of y
   bool mx, f32_out;
+  bool fused, gated;       // an epilogue other than the bias
+  EpilogueArgs e;          // its activation, residual and pre-activation
 };
 int64_t wlinear_threads(const WLinearArgs& a);   // work-items of the launch
 hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s);

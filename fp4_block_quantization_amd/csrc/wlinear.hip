@@ -12,6 +12,9 @@
 // Two kernels, by the number of activation rows (shape_of): few on 4x4x4 products, where a
 // lane keeps a weight row to itself, and more on 16x16x32 tiles, where a weight is
 // converted once for the 16, 32 or 64 activation rows of a tile.
+//
+// With a gate, half of a workgroup's weight rows are the gate's and half the other
+// projection's of the same columns of y: both factors of a product are joined in one place.
 #include "serving.hpp"
 
 namespace fos {
@@ -56,6 +59,36 @@ __device__ __forceinline__ f32x2 scale_values(uint32_t w) {
   }
 }
 
+// Weight row of a workgroup's local row l of `rows`, whose first is l0 (with a gate: whose
+// first gate row is l0 / 2); rows past the end read the last row again.
+template <bool kEpi>
+__device__ __forceinline__ int64_t weight_row(const WLinearArgs& a, int64_t l0, int l, int rows) {
+  if (!kEpi || !a.gated) return min(l0 + l, a.N - 1);
+  const int64_t half = a.N / 2;
+  const bool up = l >= rows / 2;
+  return min(l0 / 2 + (up ? l - rows / 2 : l), half - 1) + (up ? half : 0);
+}
+
+// Stores y[m][n] of an epilogue from the sum of weight row n (with a gate: and of row
+// n + N / 2), the tensor scale applied.
+__device__ __forceinline__ void finish(const WLinearArgs& a, int64_t m, int64_t n, float z, float up) {
+  const int64_t cols = a.gated ? a.N / 2 : a.N;
+  if (a.bias) {
+    z += bf16_lo(a.bias[n]);
+    if (a.gated) up += bf16_lo(a.bias[cols + n]);
+  }
+  if (a.e.preact) {
+    a.e.preact[m * a.N + n] = (uint16_t)pack_bf16x2(z, z);
+    if (a.gated) a.e.preact[m * a.N + cols + n] = (uint16_t)pack_bf16x2(up, up);
+  }
+  float y = activate(a.e.act, z);
+  if (a.gated) y *= up;
+  if (a.e.residual) y += bf16_lo(a.e.residual[m * a.e.residual_stride + n]);
+  const int64_t at = m * cols + n;
+  if (a.f32_out) static_cast<float*>(a.y)[at] = y;
+  else static_cast<uint16_t*>(a.y)[at] = (uint16_t)pack_bf16x2(y, y);
+}
+
 // ---- more activation rows: 16x16x32 tiles -------------------------------------------
 // A wave takes 16 NT weight rows (A operand) by 16 MT activation rows (B operand) and walks
 // the inner dimension in chunks of 128; the waves of a workgroup share the tile and split
@@ -65,7 +98,7 @@ __device__ __forceinline__ f32x2 scale_values(uint32_t w) {
 // each (18.8 us at 16 x 12288 x 4096), so weights and activations are loaded in memory
 // order and go through the wave's own LDS.  16-byte units are stored at (unit ^ key of the
 // row), so that the 16 rows of an operand are read from different banks.
-template <bool kMX, bool kEven, int NT, int MT, int KW>
+template <bool kMX, bool kEven, int NT, int MT, int KW, bool kEpi>
 __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a) {
   constexpr int kBlock = kMX ? 32 : 16;
   constexpr int kTileN = 16 * NT, kTileM = 16 * MT;
@@ -93,7 +126,7 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
   const uint8_t* sp[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int64_t row = min(n0 + 16 * n + wr, a.N - 1);
+    const int64_t row = weight_row<kEpi>(a, n0, 16 * n + wr, kTileN);
     wp[n] = a.wd + row * (K / 2) + 16 * wu;
     sp[n] = a.ws + row * (K / kBlock) + 32 / kBlock * wu;
   }
@@ -201,6 +234,27 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
 #pragma unroll
     for (int m = 0; m < MT; ++m) sums[n * MT + m][lane] = acc[n][m];
   __syncthreads();
+  if constexpr (kEpi) {
+    auto joined = [&](int l, int m, int c) {       // rows l .. l + 3, activation row 16 m + c
+      const int tile = (l >> 4) * MT + m, ln = ((l & 15) << 2) | c;
+      f32x4 v = reinterpret_cast<f32x4(*)[64]>(mem[0])[tile][ln];
+#pragma unroll
+      for (int w = 1; w < KW; ++w) v += reinterpret_cast<f32x4(*)[64]>(mem[w])[tile][ln];
+      return v * t;
+    };
+    const int rows = a.gated ? kTileN / 2 : kTileN;
+    const int64_t c0 = a.gated ? n0 / 2 : n0, cols = a.gated ? a.N / 2 : a.N;
+    for (int i = threadIdx.x; i < rows / 4 * kTileM; i += 64 * KW) {
+      const int l = 4 * (i / kTileM), mi = i % kTileM;
+      if (m0 + mi >= a.M) continue;
+      const f32x4 z = joined(l, mi >> 4, mi & 15);
+      const f32x4 up = a.gated ? joined(l + rows, mi >> 4, mi & 15) : f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c0 + l + k < cols) finish(a, m0 + mi, c0 + l + k, z[k], up[k]);
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < NT * MT * 64; i += 64 * KW) {
     const int tile = i >> 6, ln = i & 63;
     f32x4 v = reinterpret_cast<f32x4(*)[64]>(mem[0])[tile][ln];
@@ -247,7 +301,7 @@ __device__ __forceinline__ float sum_over_quads(float v) {
 // are one aligned load.  kMany: more than four activation rows, blockIdx.y counts the fours
 // (apart, because what it takes in registers costs two rows a lane their fourth wave on a
 // SIMD: 9.2 us instead of 7.8 at 1 x 4096 x 12288).
-template <bool kMX, bool kEven, int R, int KW, bool kMany>
+template <bool kMX, bool kEven, int R, int KW, bool kMany, bool kEpi>
 __global__ __launch_bounds__(64 * KW, R == 2 && !kMany ? 4 : 3) void wlinear_quad_kernel(WLinearArgs a) {
   constexpr int kBlock = kMX ? 32 : 16;
   constexpr int kRows = 4 * R;
@@ -266,7 +320,7 @@ __global__ __launch_bounds__(64 * KW, R == 2 && !kMany ? 4 : 3) void wlinear_qua
   const uint8_t* sp[R];
 #pragma unroll
   for (int j = 0; j < R; ++j) {         // rows past N read the last row again
-    const int64_t row = min(n0 + 4 * j + i, a.N - 1);
+    const int64_t row = weight_row<kEpi>(a, n0, 4 * j + i, kRows);
     wp[j] = a.wd + row * (K / 2) + 16 * g;
     sp[j] = a.ws + row * (K / kBlock) + 32 / kBlock * g;
   }
@@ -359,6 +413,22 @@ __global__ __launch_bounds__(64 * KW, R == 2 && !kMany ? 4 : 3) void wlinear_qua
       if (g == 0) sums[wave][4 * j + i][c] = v;
     }
   __syncthreads();
+  if constexpr (kEpi) {
+    auto joined = [&](int n, int m) {
+      float v = sums[0][n][m];
+#pragma unroll
+      for (int w = 1; w < KW; ++w) v += sums[w][n][m];
+      return v * t;
+    };
+    const int rows = a.gated ? kRows / 2 : kRows;
+    const int64_t c0 = a.gated ? n0 / 2 : n0, cols = a.gated ? a.N / 2 : a.N;
+    for (int e = threadIdx.x; e < rows * M; e += 64 * KW) {
+      const int n = e % rows, m = e / rows;
+      if (c0 + n < cols)
+        finish(a, m0 + m, c0 + n, joined(n, m), a.gated ? joined(n + rows, m) : 0.0f);
+    }
+    return;
+  }
   for (int e = threadIdx.x; e < kRows * M; e += 64 * KW) {
     const int n = e % kRows, m = e / kRows;
     if (n0 + n >= a.N) continue;
@@ -424,23 +494,33 @@ int64_t tiles_of(const WLinearArgs& a, const Shape& h) {
   return ((a.N + 16 * h.nt - 1) / (16 * h.nt)) * ((a.M + 16 * h.mt - 1) / (16 * h.mt));
 }
 
+template <int NT, int MT, int KW, bool kEpi>
+void launch_tile(const WLinearArgs& a, uint32_t grid, hipStream_t s) {
+  if (a.mx) wlinear_tile_kernel<true, true, NT, MT, KW, kEpi><<<grid, 64 * KW, 0, s>>>(a);
+  else if (a.K % 32 == 0) wlinear_tile_kernel<false, true, NT, MT, KW, kEpi><<<grid, 64 * KW, 0, s>>>(a);
+  else wlinear_tile_kernel<false, false, NT, MT, KW, kEpi><<<grid, 64 * KW, 0, s>>>(a);
+}
 template <int NT, int MT, int KW>
 bool launch_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
   if (h.nt != NT || h.mt != MT || h.kw != KW) return false;
   const uint32_t grid = (uint32_t)tiles_of(a, h);
-  if (a.mx) wlinear_tile_kernel<true, true, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
-  else if (a.K % 32 == 0) wlinear_tile_kernel<false, true, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
-  else wlinear_tile_kernel<false, false, NT, MT, KW><<<grid, 64 * KW, 0, s>>>(a);
+  if (a.fused) launch_tile<NT, MT, KW, true>(a, grid, s);
+  else launch_tile<NT, MT, KW, false>(a, grid, s);
   return true;
 }
 
+template <int R, int KW, bool kMany, bool kEpi>
+void launch_quad(const WLinearArgs& a, dim3 grid, hipStream_t s) {
+  if (a.mx) wlinear_quad_kernel<true, true, R, KW, kMany, kEpi><<<grid, 64 * KW, 0, s>>>(a);
+  else if (a.K % 32 == 0) wlinear_quad_kernel<false, true, R, KW, kMany, kEpi><<<grid, 64 * KW, 0, s>>>(a);
+  else wlinear_quad_kernel<false, false, R, KW, kMany, kEpi><<<grid, 64 * KW, 0, s>>>(a);
+}
 template <int R, int KW, bool kMany>
 bool launch_quad_if(const WLinearArgs& a, const Shape& h, hipStream_t s) {
   if (h.nt != R || h.mt != 0 || h.kw != KW || (a.M > 4) != kMany) return false;
   const dim3 grid((uint32_t)((a.N + 4 * R - 1) / (4 * R)), (uint32_t)((a.M + 3) / 4));
-  if (a.mx) wlinear_quad_kernel<true, true, R, KW, kMany><<<grid, 64 * KW, 0, s>>>(a);
-  else if (a.K % 32 == 0) wlinear_quad_kernel<false, true, R, KW, kMany><<<grid, 64 * KW, 0, s>>>(a);
-  else wlinear_quad_kernel<false, false, R, KW, kMany><<<grid, 64 * KW, 0, s>>>(a);
+  if (a.fused) launch_quad<R, KW, kMany, true>(a, grid, s);
+  else launch_quad<R, KW, kMany, false>(a, grid, s);
   return true;
 }
 

@@ -7,8 +7,8 @@ module raises.
 
 Low-level functions carry the C names (fos_quantize, fos_dequantize, ...) and take
 device tensors; ``quantize`` / ``dequantize`` / ``qlinear_fwd`` allocate the outputs.
-The calls that serve one token at a time run on their tensors' device; all others want it to
-be the current one (``torch.cuda.device``).
+The calls that serve one token at a time and those of the feed-forward path run on their
+tensors' device; all others want it to be the current one (``torch.cuda.device``).
 """
 from __future__ import annotations
 
@@ -30,6 +30,8 @@ FOS_BLOCK_1D, FOS_BLOCK_2D = 0, 1
 FOS_OUT_ROWWISE, FOS_OUT_COLWISE = 1, 2
 FOS_OUT_F32, FOS_OUT_BF16 = 0, 1
 FOS_KV_BF16, FOS_KV_NVFP4 = 0, 1
+FOS_ACT_NONE, FOS_ACT_RELU, FOS_ACT_GELU, FOS_ACT_GELU_TANH, FOS_ACT_SILU = range(5)
+FOS_RECORD_NONE, FOS_RECORD_NVFP4, FOS_RECORD_MXFP4 = range(3)
 
 
 class FosError(RuntimeError):
@@ -55,6 +57,14 @@ class FosKVCache(ctypes.Structure):
                 ("v_tensor_scale", ctypes.c_void_p)]
 
 
+class FosEpilogue(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("activation", ctypes.c_uint32),
+                ("gated", ctypes.c_uint32), ("out_dtype", ctypes.c_uint32),
+                ("bias_bf16", ctypes.c_void_p), ("residual_bf16", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("preact_bf16", ctypes.c_void_p),
+                ("reserved", ctypes.c_uint64)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m fp4_block_quantization_amd.build`")
@@ -62,6 +72,7 @@ def _load() -> ctypes.CDLL:
     P, I64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
     cfgp = ctypes.POINTER(FosQuantConfig)
     cachep = ctypes.POINTER(FosKVCache)
+    epip, INT = ctypes.POINTER(FosEpilogue), ctypes.c_int
     sigs = {
         "fos_abi_version": ([], ctypes.c_int),
         "fos_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -94,6 +105,16 @@ def _load() -> ctypes.CDLL:
         "fos_paged_decode_counter_bytes": ([], SZ),
         "fos_paged_decode": ([cachep, P, I64, I64, I64, P, I64, I64, P, ctypes.c_float, I64, P, P,
                               P, SZ, P], ctypes.c_int),
+        "fos_rmsnorm_fwd": ([P, I64, P, I64, P, I64, I64, ctypes.c_double, P, P, P, INT, INT, P, P, P,
+                             INT, P, SZ, P], INT),
+        "fos_rmsnorm_bwd_workspace_bytes": ([I64, I64], SZ),
+        "fos_rmsnorm_bwd": ([P, P, P, P, P, I64, I64, P, P, P, SZ, P], INT),
+        "fos_qlinear_epilogue_fwd": ([P] * 6 + [I64, I64, I64, epip, P, P], INT),
+        "fos_mx_qlinear_epilogue_fwd": ([P] * 4 + [I64, I64, I64, epip, P, P], INT),
+        "fos_wlinear_epilogue_fwd": ([P, I64, P, P, P, I64, I64, I64, epip, P, P], INT),
+        "fos_mx_wlinear_epilogue_fwd": ([P, I64, P, P, I64, I64, I64, epip, P, P], INT),
+        "fos_epilogue_bwd_workspace_bytes": ([I64, I64, INT], SZ),
+        "fos_epilogue_bwd": ([P, P, I64, I64, INT, INT, P, P, P, P, SZ, P], INT),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -845,3 +866,367 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
                 int(window), out.data_ptr(), None if lse is None else lse.data_ptr(),
                 ws.data_ptr(), ws.numel(), stream), "fos_paged_decode")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- feed-forward path
+# The norm in front of a product, products with an epilogue, and their backward passes.  Like
+# the serving calls they run on their tensors' device and marshal raw addresses; outputs and
+# workspaces are allocated in the call (in a capture: in the graph's memory).
+
+_ACTIVATIONS = {"none": FOS_ACT_NONE, "relu": FOS_ACT_RELU, "gelu": FOS_ACT_GELU,
+                "gelu_tanh": FOS_ACT_GELU_TANH, "silu": FOS_ACT_SILU}
+_RECORDS = {"bf16": FOS_RECORD_NONE, "nvfp4": FOS_RECORD_NVFP4, "mxfp4": FOS_RECORD_MXFP4}
+
+
+def _activation(name: str) -> int:
+    code = _ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(map(repr, _ACTIVATIONS))}")
+    return code
+
+
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _call(dev: int, name: str, *args) -> None:
+    """The C entry point on the current stream of device ``dev``."""
+    fn = getattr(_lib, name)
+    if dev != _current_device():
+        fn = _on(dev, fn)
+    _check(fn(*args, _raw_stream(dev)), name)
+
+
+def _rows_of(t: torch.Tensor, M: int, K: int, dev: int, what: str) -> int:
+    """The row stride of a bf16 [M, K] tensor with contiguous rows."""
+    s = t.stride()
+    if (len(s) != 2 or t.shape != (M, K) or t.dtype != _BF16 or t.get_device() != dev
+            or (s[1] != 1 and K > 1)):
+        raise ValueError(f"{what} must be bf16 [{M}, {K}] with contiguous rows, on one device with "
+                         "the other tensors")
+    return s[0] if M > 1 else K
+
+
+def _whole(t: torch.Tensor, shape, dtype, dev: int, what: str) -> torch.Tensor:
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)}, on one device "
+                         "with the other tensors")
+    return t
+
+
+@dataclass
+class RMSNormOutput:
+    """What ``rmsnorm_fwd`` computes: h bf16 [M, K], the sum with the residual (x itself
+    without one); rstd fp32 [M]; the output as y (bf16 [M, K]), as a record, or both."""
+    h: torch.Tensor
+    rstd: torch.Tensor
+    y: Optional[torch.Tensor] = None
+    record: Union[NVFP4Tensor, MXFP4Tensor, None] = None
+
+
+def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                residual: Optional[torch.Tensor] = None, format: str = "bf16", rule: str = "4/6",
+                tensor_scale: Optional[torch.Tensor] = None, return_y: bool = False,
+                h: Optional[torch.Tensor] = None) -> RMSNormOutput:
+    """RMS norm of the rows of x (bf16 [M, K]; rows may be strided), after the addition of
+    ``residual`` (bf16 [M, K], strided too): h = x + residual rounded to bf16, y = h / rms(h)
+    * weight.  ``format`` "bf16" returns y; "nvfp4" and "mxfp4" its record, the same as
+    ``quantize(y, rule)`` or ``mx_quantize(y)``, without y in memory (``return_y``: y too, as
+    its column-wise record needs for the weight's gradient).  ``tensor_scale``: fp32 [1], the
+    NVFP4 scale to use (delayed scaling; one pass over x); by default that of y is computed.
+    ``h``: optional destination of the sum, for instance ``residual`` itself; only with a
+    residual.  K a multiple of 16 (MXFP4: 32), at most 65536."""
+    if x.dim() != 2 or x.get_device() < 0:
+        raise ValueError("x must be a 2-D bfloat16 CUDA tensor with contiguous rows")
+    M, K = x.shape
+    dev = x.get_device()
+    stride = _rows_of(x, M, K, dev, "x")
+    _whole(weight, (K,), _BF16, dev, "weight")
+    code = _RECORDS.get(format)
+    if code is None:
+        raise ValueError("format must be 'bf16', 'nvfp4' or 'mxfp4'")
+    if rule not in _KV_RULES:
+        raise ValueError("rule must be '4/6' or '6'")
+    if tensor_scale is not None:
+        if format != "nvfp4":
+            raise ValueError("only an NVFP4 record has a tensor scale")
+        if tensor_scale.numel() != 1 or tensor_scale.dtype != _F32 or tensor_scale.get_device() != dev:
+            raise ValueError("tensor_scale must be a one-element fp32 tensor on x's device")
+    r_stride = 0
+    if residual is not None:
+        r_stride = _rows_of(residual, M, K, dev, "residual")
+        h = x.new_empty(M, K) if h is None else _whole(h, (M, K), _BF16, dev, "h")
+    elif h is not None:
+        raise ValueError("h is a destination for the sum with a residual")
+    rstd = x.new_empty(M, dtype=_F32)
+    y = x.new_empty(M, K) if format == "bf16" or return_y else None
+    data = scales = t = ws = record = None
+    if code != FOS_RECORD_NONE:
+        data = x.new_empty(M, K // 2, dtype=_U8)
+        scales = x.new_empty(M, K // (16 if format == "nvfp4" else 32), dtype=_U8)
+        if format == "nvfp4":
+            t = tensor_scale
+            if t is None:
+                t = x.new_empty(1, dtype=_F32)
+                ws = x.new_empty(int(_lib.fos_quantize_workspace_bytes()), dtype=_U8)
+            record = NVFP4Tensor(data, scales, t)
+        else:
+            record = MXFP4Tensor(data, scales)
+    _call(dev, "fos_rmsnorm_fwd", x.data_ptr(), stride, _address(residual), r_stride,
+          weight.data_ptr(), M, K, eps, _address(h), rstd.data_ptr(), _address(y), code,
+          _KV_RULES[rule], _address(data), _address(scales), _address(t),
+          int(tensor_scale is not None), _address(ws), 0 if ws is None else ws.numel())
+    return RMSNormOutput(x if h is None else h, rstd, y, record)
+
+
+def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                dh: Optional[torch.Tensor] = None, need_dweight: bool = True
+                ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Backward of ``rmsnorm_fwd`` from the gradient dy of its output (quantization counts as
+    the identity) and its h and rstd.  ``dh``: the gradient that reaches h past the norm.
+    Returns the gradient of x, which is the residual's too (bf16 [M, K]), and that of the
+    weight (fp32 [K], or None)."""
+    if dy.dim() != 2 or dy.get_device() < 0:
+        raise ValueError("dy must be a contiguous 2-D bfloat16 CUDA tensor")
+    M, K = dy.shape
+    dev = dy.get_device()
+    _whole(dy, (M, K), _BF16, dev, "dy")
+    _whole(h, (M, K), _BF16, dev, "h")
+    _whole(weight, (K,), _BF16, dev, "weight")
+    _whole(rstd, (M,), _F32, dev, "rstd")
+    if dh is not None:
+        _whole(dh, (M, K), _BF16, dev, "dh")
+    dx = dy.new_empty(M, K)
+    dw = ws = None
+    if need_dweight:
+        dw = dy.new_empty(K, dtype=_F32)
+        ws = dy.new_empty(int(_lib.fos_rmsnorm_bwd_workspace_bytes(M, K)), dtype=_U8)
+    _call(dev, "fos_rmsnorm_bwd", dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+          _address(dh), M, K, dx.data_ptr(), _address(dw), _address(ws),
+          0 if ws is None else ws.numel())
+    return dx, dw
+
+
+def _epilogue(M: int, W: int, gated: bool, like: torch.Tensor, dev: int, bias, activation, residual,
+              out_dtype, return_preact: bool, out):
+    """The C struct, the output and the kept pre-activation of a product with W weight rows."""
+    act = _activation(activation)
+    if out_dtype not in _OUT_CODE:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    if gated and W % 2:
+        raise ValueError("a gated weight holds as many rows for the gate as for the other projection")
+    N = W // 2 if gated else W
+    if bias is not None:
+        _whole(bias, (W,), _BF16, dev, "bias")
+    stride = 0 if residual is None else _rows_of(residual, M, N, dev, "residual")
+    if out is None:
+        out = like.new_empty(M, N, dtype=out_dtype)
+    else:
+        _whole(out, (M, N), out_dtype, dev, "out")
+    preact = like.new_empty(M, W, dtype=_BF16) if return_preact else None
+    e = FosEpilogue(ctypes.sizeof(FosEpilogue), act, int(gated), _OUT_CODE[out_dtype],
+                    _address(bias), _address(residual), stride, _address(preact), 0)
+    return N, e, out, preact
+
+
+def _check_product_records(xq, wq, block: int):
+    """(device, M, W, K) of two records blocked along K."""
+    xd, wd = xq.data, wq.data
+    dev = xd.get_device()
+    if dev < 0 or xd.dim() != 2 or wd.dim() != 2:
+        raise ValueError("record data must be 2-D CUDA tensors")
+    M, half = xd.shape
+    W, half2 = wd.shape
+    if half != half2:
+        raise ValueError("inner dimensions differ")
+    for r, rows in ((xq, M), (wq, W)):
+        _whole(r.data, (rows, half), _U8, dev, "record data")
+        _whole(r.scales, (rows, 2 * half // block), _U8, dev, "record scales")
+        if block == 16 and (r.tensor_scale.numel() != 1 or r.tensor_scale.dtype != _F32
+                            or r.tensor_scale.get_device() != dev):
+            raise ValueError("tensor_scale must be a one-element fp32 tensor on the record's device")
+    return dev, M, W, 2 * half
+
+
+def _qlinear_epilogue(xq, wq, gated, bias, activation, residual, out_dtype, return_preact, out):
+    if xq.hadamard_seed != wq.hadamard_seed:
+        raise ValueError("one of the records carries a Hadamard transform that the other does not")
+    dev, M, W, K = _check_product_records(xq, wq, 16)
+    N, e, y, z = _epilogue(M, W, gated, xq.data, dev, bias, activation, residual, out_dtype,
+                           return_preact, out)
+    _call(dev, "fos_qlinear_epilogue_fwd", xq.data.data_ptr(), xq.scales.data_ptr(),
+          xq.tensor_scale.data_ptr(), wq.data.data_ptr(), wq.scales.data_ptr(),
+          wq.tensor_scale.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
+    return (y, z) if return_preact else y
+
+
+def _mx_qlinear_epilogue(aq, bq, gated, bias, activation, residual, out_dtype, return_preact, out):
+    dev, M, W, K = _check_product_records(aq, bq, 32)
+    N, e, y, z = _epilogue(M, W, gated, aq.data, dev, bias, activation, residual, out_dtype,
+                           return_preact, out)
+    _call(dev, "fos_mx_qlinear_epilogue_fwd", aq.data.data_ptr(), aq.scales.data_ptr(),
+          bq.data.data_ptr(), bq.scales.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
+    return (y, z) if return_preact else y
+
+
+def qlinear_epilogue_fwd(xq: NVFP4Tensor, wq: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
+                         activation: str = "none", residual: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.bfloat16, return_preact: bool = False,
+                         out: Optional[torch.Tensor] = None):
+    """``qlinear_fwd`` with an epilogue: Y = act(Z) + residual, Z = deq(X) deq(W)^T + bias, in
+    fp32 up to one rounding to ``out_dtype`` (bf16 or fp32).  ``activation``: "none", "relu",
+    "gelu", "gelu_tanh" or "silu".  bias bf16 [N]; residual bf16 [M, N], rows may be strided;
+    ``out``: optional [M, N] destination (for instance the residual itself).
+    ``return_preact``: also Z in bf16, for ``epilogue_bwd`` or ``qlinear_epilogue_bwd``."""
+    return _qlinear_epilogue(xq, wq, False, bias, activation, residual, out_dtype, return_preact, out)
+
+
+def mx_qlinear_epilogue_fwd(aq: MXFP4Tensor, bq: MXFP4Tensor, bias: Optional[torch.Tensor] = None,
+                            activation: str = "none", residual: Optional[torch.Tensor] = None,
+                            out_dtype: torch.dtype = torch.bfloat16, return_preact: bool = False,
+                            out: Optional[torch.Tensor] = None):
+    """``qlinear_epilogue_fwd`` for MXFP4 records (``mx_qlinear_fwd`` with an epilogue)."""
+    return _mx_qlinear_epilogue(aq, bq, False, bias, activation, residual, out_dtype, return_preact, out)
+
+
+def qglu_fwd(xq: NVFP4Tensor, wq: NVFP4Tensor, activation: str = "silu",
+             bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+             return_preact: bool = False, out: Optional[torch.Tensor] = None):
+    """Both projections of a gated feed-forward block in one product: with the weight record
+    W [2N, K] (first the N rows of the gate, then those of the other projection) and
+    Z = deq(X) deq(W)^T + bias, Y [M, N] = act(Z[:, :N]) * Z[:, N:].  The rest as for
+    ``qlinear_epilogue_fwd``; the kept Z [M, 2N] goes to ``qglu_bwd``."""
+    return _qlinear_epilogue(xq, wq, True, bias, activation, None, out_dtype, return_preact, out)
+
+
+def mx_qglu_fwd(aq: MXFP4Tensor, bq: MXFP4Tensor, activation: str = "silu",
+                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                return_preact: bool = False, out: Optional[torch.Tensor] = None):
+    """``qglu_fwd`` for MXFP4 records."""
+    return _mx_qlinear_epilogue(aq, bq, True, bias, activation, None, out_dtype, return_preact, out)
+
+
+def _wlinear_epilogue(x, wq, block, gated, bias, activation, residual, out_dtype, return_preact, out):
+    data, scales = wq.data, wq.scales
+    dev = data.get_device()
+    if dev < 0 or data.dim() != 2 or x.dim() != 2:
+        raise ValueError("x and the record's data must be 2-D CUDA tensors")
+    W, half = data.shape
+    M, K = x.shape[0], 2 * half
+    stride = _rows_of(x, M, K, dev, "x")
+    _whole(data, (W, half), _U8, dev, "record data")
+    _whole(scales, (W, K // block), _U8, dev, "record scales")
+    N, e, y, z = _epilogue(M, W, gated, x, dev, bias, activation, residual, out_dtype,
+                           return_preact, out)
+    if block == 16:
+        t = wq.tensor_scale
+        if wq.hadamard_seed is not None:
+            raise ValueError("the weight record carries a Hadamard transform that x does not")
+        if t.numel() != 1 or t.dtype != _F32 or t.get_device() != dev:
+            raise ValueError("tensor_scale must be a one-element fp32 tensor on x's device")
+        _call(dev, "fos_wlinear_epilogue_fwd", x.data_ptr(), stride, data.data_ptr(),
+              scales.data_ptr(), t.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
+    else:
+        _call(dev, "fos_mx_wlinear_epilogue_fwd", x.data_ptr(), stride, data.data_ptr(),
+              scales.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
+    return (y, z) if return_preact else y
+
+
+def wlinear_epilogue_fwd(x: torch.Tensor, wq: NVFP4Tensor, bias: Optional[torch.Tensor] = None,
+                         activation: str = "none", residual: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.bfloat16, return_preact: bool = False,
+                         out: Optional[torch.Tensor] = None):
+    """``wlinear_fwd`` (few bf16 activation rows) with an epilogue: Y = act(Z) + residual,
+    Z = X deq(W)^T + bias.  Arguments as for ``qlinear_epilogue_fwd``."""
+    return _wlinear_epilogue(x, wq, 16, False, bias, activation, residual, out_dtype, return_preact, out)
+
+
+def mx_wlinear_epilogue_fwd(x: torch.Tensor, wq: MXFP4Tensor, bias: Optional[torch.Tensor] = None,
+                            activation: str = "none", residual: Optional[torch.Tensor] = None,
+                            out_dtype: torch.dtype = torch.bfloat16, return_preact: bool = False,
+                            out: Optional[torch.Tensor] = None):
+    """``wlinear_epilogue_fwd`` for an MXFP4 weight record."""
+    return _wlinear_epilogue(x, wq, 32, False, bias, activation, residual, out_dtype, return_preact, out)
+
+
+def wglu_fwd(x: torch.Tensor, wq: NVFP4Tensor, activation: str = "silu",
+             bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+             return_preact: bool = False, out: Optional[torch.Tensor] = None):
+    """``qglu_fwd`` for few bf16 activation rows (a decode step): both projections of a gated
+    block, the activation and the product, from a weight record [2N, K]."""
+    return _wlinear_epilogue(x, wq, 16, True, bias, activation, None, out_dtype, return_preact, out)
+
+
+def mx_wglu_fwd(x: torch.Tensor, wq: MXFP4Tensor, activation: str = "silu",
+                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                return_preact: bool = False, out: Optional[torch.Tensor] = None):
+    """``wglu_fwd`` for an MXFP4 weight record."""
+    return _wlinear_epilogue(x, wq, 32, True, bias, activation, None, out_dtype, return_preact, out)
+
+
+def _epilogue_bwd(dy, preact, activation, gated, need_dbias, need_scale):
+    act = _activation(activation)
+    if dy.dim() != 2 or dy.get_device() < 0:
+        raise ValueError("dy must be a contiguous 2-D bfloat16 CUDA tensor")
+    M, N = dy.shape
+    dev, W = dy.get_device(), 2 * N if gated else N
+    _whole(dy, (M, N), _BF16, dev, "dy")
+    _whole(preact, (M, W), _BF16, dev, "preact")
+    dz = dy.new_empty(M, W)
+    dbias = dy.new_empty(W, dtype=_F32) if need_dbias else None
+    t = dy.new_empty(1, dtype=_F32) if need_scale else None
+    ws = None
+    if need_dbias or need_scale:
+        ws = dy.new_empty(int(_lib.fos_epilogue_bwd_workspace_bytes(M, N, int(gated))), dtype=_U8)
+    _call(dev, "fos_epilogue_bwd", dy.data_ptr(), preact.data_ptr(), M, N, act, int(gated),
+          dz.data_ptr(), _address(dbias), _address(t), _address(ws), 0 if ws is None else ws.numel())
+    return dz, dbias, t
+
+
+def epilogue_bwd(dy: torch.Tensor, preact: torch.Tensor, activation: str = "none",
+                 gated: bool = False, return_dbias: bool = False,
+                 return_tensor_scale: bool = False):
+    """Backward of an epilogue: dZ (bf16, like preact) from dY (bf16 [M, N]) and the kept
+    pre-activation ([M, N], of a gated block [M, 2N]).  Returns dZ, with ``return_dbias`` also
+    its column sums (fp32), with ``return_tensor_scale`` also the NVFP4 tensor scale of dZ
+    (fp32 [1]).  The residual's gradient is dY itself."""
+    dz, dbias, t = _epilogue_bwd(dy, preact, activation, gated, return_dbias, return_tensor_scale)
+    got = (dz,) + ((dbias,) if return_dbias else ()) + ((t,) if return_tensor_scale else ())
+    return got if len(got) > 1 else dz
+
+
+def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, rounding, sr_seed,
+                 need_dx, need_dw):
+    if not (need_dx or need_dw):
+        raise ValueError("nothing to compute")
+    dz, dbias, t = _epilogue_bwd(dy, preact, activation, gated, return_dbias, True)
+    outputs = (("row",) if need_dx else ()) + (("col",) if need_dw else ())
+    with torch.cuda.device(dz.device):
+        q = quantize(dz, rounding=rounding, outputs=outputs, sr_seed=sr_seed, tensor_scale=t)
+        rows, cols = q if need_dx and need_dw else (q, None) if need_dx else (None, q)
+        dx, dw = qlinear_bwd(rows, cols, xq_t, wq_t, need_dx, need_dw)
+    return (dx, dw, dbias) if return_dbias else (dx, dw)
+
+
+def qlinear_epilogue_bwd(dy: torch.Tensor, preact: torch.Tensor, xq_t: Optional[NVFP4Tensor],
+                         wq_t: Optional[NVFP4Tensor], activation: str = "none",
+                         return_dbias: bool = False, rounding: str = "rne",
+                         sr_seed: Optional[int] = None, need_dx: bool = True, need_dw: bool = True):
+    """Backward of ``qlinear_epilogue_fwd`` down to its operands: ``epilogue_bwd``, dZ
+    quantized in the orientations of the products (``rounding`` and ``sr_seed`` as for
+    ``quantize``), and ``qlinear_bwd`` with the column-wise records of X and W.  Returns
+    (dX, dW), bf16, a skipped one None, with ``return_dbias`` also dbias (fp32).  M and W's
+    rows are multiples of 64 where they are a product's inner dimension, and of 16.  The
+    residual's gradient is dY."""
+    return _product_bwd(dy, preact, xq_t, wq_t, activation, False, return_dbias, rounding, sr_seed,
+                        need_dx, need_dw)
+
+
+def qglu_bwd(dy: torch.Tensor, preact: torch.Tensor, xq_t: Optional[NVFP4Tensor],
+             wq_t: Optional[NVFP4Tensor], activation: str = "silu", return_dbias: bool = False,
+             rounding: str = "rne", sr_seed: Optional[int] = None, need_dx: bool = True,
+             need_dw: bool = True):
+    """Backward of ``qglu_fwd`` down to its operands, as ``qlinear_epilogue_bwd``: dX [M, K]
+    joins both projections' parts, dW [2N, K] and dbias [2N] are in W's order."""
+    return _product_bwd(dy, preact, xq_t, wq_t, activation, True, return_dbias, rounding, sr_seed,
+                        need_dx, need_dw)

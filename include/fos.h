@@ -523,6 +523,138 @@ fos_status fos_paged_decode(const fos_kv_cache* cache, const void* q_bf16, int64
                             float softmax_scale, int64_t window, void* out_bf16, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Feed-forward path -----------------------------------------------------------
+ * What stands between the quantized products of a feed-forward block, in training and in
+ * serving: the RMS norm with the residual's addition whose output is the next product's
+ * record, products with bias, activation, gate and residual in their epilogue, and the
+ * backward passes.  (The Four Over Six documentation page, section "Training", gives the
+ * quantized layer a backward pass; the pages do not fix these operators, the formulas
+ * below do.) */
+
+/* Activations: z; max(z, 0); z F(z) with the standard normal distribution function F;
+ * z s(2 sqrt(2/pi) (z + 0.044715 z^3)) with s(u) = 1 / (1 + e^-u); z s(z). */
+enum {
+  FOS_ACT_NONE = 0, FOS_ACT_RELU = 1, FOS_ACT_GELU = 2, FOS_ACT_GELU_TANH = 3, FOS_ACT_SILU = 4
+};
+
+/* Record that the norm writes beside or instead of its bf16 output. */
+enum { FOS_RECORD_NONE = 0, FOS_RECORD_NVFP4 = 1, FOS_RECORD_MXFP4 = 2 };
+
+/* RMS norm of the rows of x, or of the sum of x and a residual:
+ *   h = RN_bf16(x + residual)   (h = x without a residual)
+ *   rstd = RN_fp32(1 / sqrt(mean_k h[k]^2 + eps)), the mean in fp64
+ *   y = RN_bf16(RN_fp32(RN_fp32(h * rstd) * weight))
+ * and, with FOS_RECORD_NVFP4 or FOS_RECORD_MXFP4, the record of y [rows][cols]: the bytes
+ * that fos_quantize (1D blocks, nearest-even rounding, `rule`) or fos_mx_quantize makes of
+ * it.  For NVFP4 with tensor_scale_given != 0 the call reads the tensor scale (delayed
+ * scaling) and each row is read once; otherwise it computes the scale of y, writes it to
+ * *tensor_scale, and reads h twice.
+ *   x, residual (or NULL): bf16, row strides in elements, at least cols and multiples of 8
+ *   (for rows > 1); weight [cols]; h, y bf16 [rows][cols], contiguous; all 16-byte aligned.
+ *   h, rstd (fp32 [rows]) and y may be NULL, but y not without a record, rstd not where the
+ *   tensor scale is computed, nor h there with a residual.  h may be the memory of x or of
+ *   the residual, if that is contiguous.  data [rows][cols/2] 8-byte aligned, scales
+ *   [rows][cols/16] (MXFP4: [rows][cols/32]), tensor_scale 4-byte aligned.
+ *   rows >= 0, below 2^31; cols a multiple of 16 (MXFP4: of 32) from 16 to 65536; eps
+ *   finite, at least 1e-38.  No rows: a computed tensor scale is 0, nothing else is written.
+ *   workspace: for a computed tensor scale only, as for fos_quantize.
+ * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_WORKSPACE, FOS_E_HIP. */
+fos_status fos_rmsnorm_fwd(const void* x_bf16, int64_t x_stride, const void* residual_bf16,
+                           int64_t residual_stride, const void* weight_bf16, int64_t rows,
+                           int64_t cols, double eps, void* h_bf16, float* rstd, void* y_bf16,
+                           int record, int rule, uint8_t* data, uint8_t* scales,
+                           float* tensor_scale, int tensor_scale_given, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace that fos_rmsnorm_bwd needs for dweight; 0 for sizes that it
+ * refuses. */
+size_t fos_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Backward pass of the norm (quantization of y counts as the identity).  With n = h * rstd
+ * and g = dy * weight:
+ *   dx = RN_bf16(rstd * (g - n * mean_k(g n)) + dh)   the gradient of x and of the residual
+ *   dweight[k] = sum over rows of dy n                fp32, in a fixed order
+ * dh (or NULL): the gradient that reaches h itself, past the norm.
+ *   dy, h, dh, dx bf16 [rows][cols] contiguous, weight [cols], all 16-byte aligned; dx may be
+ *   the memory of dy or dh; rstd fp32 [rows]; dweight fp32 [cols], 16-byte aligned, or NULL
+ *   (then no workspace is needed).  Sizes as for fos_rmsnorm_fwd; no rows: dweight is 0.
+ *   workspace: 16-byte aligned scratch.
+ * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_WORKSPACE, FOS_E_HIP. */
+fos_status fos_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const void* weight_bf16,
+                           const float* rstd, const void* dh_bf16, int64_t rows, int64_t cols,
+                           void* dx_bf16, float* dweight, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* What follows a product Z = deq(X) deq(W)^T + bias in the same kernel, in fp32 up to one
+ * rounding to the output type:
+ *   gated == 0:  Y [M][N] = act(Z) + residual,  W [N][K]
+ *   gated == 1:  Y [M][N] = act(Z_gate) * Z_up,  W [2N][K]: first the N rows of the gate,
+ *                then the N rows of the other projection, and so the columns of Z and bias.
+ * preact: Z rounded to bf16, [M][N] or gated [M][2N], contiguous: what fos_epilogue_bwd
+ * needs.  Pointers may be NULL: without a bias, a residual, a kept Z.  residual: bf16, row
+ * stride in elements, at least N (not with a gate); y may be its memory, if that is
+ * contiguous and the output bf16.  All 2-byte aligned, y to its type; with N % 4 == 0 and
+ * addresses (and the residual's stride) at multiples of four elements, rows are accessed
+ * four values at a time. */
+typedef struct {
+  uint32_t struct_size;       /* must equal sizeof(fos_epilogue)                      */
+  uint32_t activation;        /* FOS_ACT_*                                            */
+  uint32_t gated;             /* 0 or 1                                               */
+  uint32_t out_dtype;         /* FOS_OUT_F32 or FOS_OUT_BF16                          */
+  const void* bias_bf16;      /* [N], gated [2N], or NULL                             */
+  const void* residual_bf16;  /* [M][N] or NULL                                       */
+  int64_t residual_stride;
+  void* preact_bf16;          /* or NULL                                              */
+  uint64_t reserved;          /* 0                                                    */
+} fos_epilogue;               /* host struct, read only during the call               */
+
+/* fos_qlinear_fwd and fos_mx_qlinear_fwd with an epilogue: their operands, sizes and
+ * alignments, where (N + 256) * K / 2 below 2^32 counts the weight's rows (2N with a gate).
+ * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_HIP. */
+fos_status fos_qlinear_epilogue_fwd(const uint8_t* x_data, const uint8_t* x_scales,
+                                    const float* x_tensor_scale, const uint8_t* w_data,
+                                    const uint8_t* w_scales, const float* w_tensor_scale,
+                                    int64_t M, int64_t N, int64_t K, const fos_epilogue* epilogue,
+                                    void* y, void* stream);
+fos_status fos_mx_qlinear_epilogue_fwd(const uint8_t* a_data, const uint8_t* a_scales,
+                                       const uint8_t* b_data, const uint8_t* b_scales, int64_t M,
+                                       int64_t N, int64_t K, const fos_epilogue* epilogue, void* y,
+                                       void* stream);
+
+/* fos_wlinear_fwd and fos_mx_wlinear_fwd with an epilogue (its bias and output type instead
+ * of theirs): the products of a decode step.  Operands, sizes and errors as there, with the
+ * weight's rows (2N with a gate) in the place of N. */
+fos_status fos_wlinear_epilogue_fwd(const void* x_bf16, int64_t x_stride, const uint8_t* w_data,
+                                    const uint8_t* w_scales, const float* w_tensor_scale,
+                                    int64_t M, int64_t N, int64_t K, const fos_epilogue* epilogue,
+                                    void* y, void* stream);
+fos_status fos_mx_wlinear_epilogue_fwd(const void* x_bf16, int64_t x_stride,
+                                       const uint8_t* w_data, const uint8_t* w_scales, int64_t M,
+                                       int64_t N, int64_t K, const fos_epilogue* epilogue, void* y,
+                                       void* stream);
+
+/* Bytes of device workspace that fos_epilogue_bwd needs for dbias and the tensor scale; 0
+ * for sizes that it refuses. */
+size_t fos_epilogue_bwd_workspace_bytes(int64_t M, int64_t N, int gated);
+
+/* Backward pass of an epilogue.  From dY [M][N] and the kept pre-activation Z:
+ *   gated == 0:  dZ = dY act'(Z)
+ *   gated == 1:  dZ_gate = dY Z_up act'(Z_gate),  dZ_up = dY act(Z_gate)
+ *   dbias = column sums of dZ before its rounding to bf16 (fp32, in a fixed order)
+ *   *tensor_scale = RN_fp32(max |dZ rounded| / 2688): what fos_tensor_scale would give for
+ *   dZ, ready for fos_quantize_scaled and then fos_qlinear_bwd.
+ * The gradient of the residual is dY.  relu's slope at 0 is 0.
+ *   dz bf16 [M][N], gated [M][2N]; dbias fp32 (its columns) or NULL; tensor_scale device
+ *   fp32 or NULL.  All contiguous; wide accesses need N % 8 == 0 and 16-byte aligned
+ *   tensors, anything else (2-byte aligned) is read value by value.  dz may be the memory
+ *   of Z.  M >= 0 below 2^31 (0: dbias and the tensor scale are 0), N from 1 to 2^30 - 1.
+ *   workspace: 16-byte aligned scratch, not needed without dbias and tensor_scale.
+ * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_WORKSPACE, FOS_E_HIP. */
+fos_status fos_epilogue_bwd(const void* dy_bf16, const void* preact_bf16, int64_t M, int64_t N,
+                            int activation, int gated, void* dz_bf16, float* dbias,
+                            float* tensor_scale, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

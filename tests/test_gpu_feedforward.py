@@ -1,0 +1,448 @@
+"""GPU tests of the feed-forward operators against fp64 references (oracle/feedforward.py)
+and, for what is stored in 4 bits, the oracle's records bit for bit.
+
+Bounds (u = 2^-24, half a step of fp32).
+
+Norm: a square of a bf16 value is exact in fp64, so the mean of K of them is off by at most
+K 2^-53 and rstd, rounded once to fp32, by (1 + 2^-10) u.  y is then a fixed sequence of fp32
+roundings of h, rstd and w, which the tests repeat bit for bit.
+
+Backward of the norm: n and g carry one rounding (u); a product of the two at most 4 u, the
+sum of K of them K u of the magnitudes more; dx's own terms add 6 u and dh's addition one.
+dw: each term 3 u, and M u of the magnitudes for their sum.
+
+Epilogue: Z is a sum of K exact products, off by at most (K + 8) u S (S the magnitudes; the
+scale and the bias are a few u).  The activations' slopes are at most 1.13 in size.  The
+activation itself: the exponent -z log2 e carries 1.5 |z| u (gelu_tanh: its argument, of
+size at most |u|, is off by 4 u |u|, and s (1 - s) |z| |u| is at most 1.2), the hardware's
+exponential and reciprocal 2 u each, so with s (1 - s) z^2 <= 0.44 an activation is off by
+at most 16 u (1 + |z|); the fit behind gelu by 5 u of a tail that is at most 1 / 2.  A
+rounding to bf16 adds 2^-8 of the value, to fp32 u.
+
+Slopes: the same errors, times at most |z| du/dz where a slope has that factor: 32 u (1 + |z|)
+for |z| below 16, beyond which a slope is 0 or 1 to fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+from fp4_block_quantization_amd import workloads as W
+from oracle import feedforward as FF
+from oracle import formats as F
+from oracle import mxfp4 as MX
+from oracle import nvfp4 as N
+from oracle import serving as S
+from oracle.qlinear import operand_exact
+from test_gpu_parity import assert_same_bytes, bits_of
+from test_gpu_serving import dev, f64, mx_weight, nv_weight, within
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def fos():
+    from fp4_block_quantization_amd import fos as mod
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    return mod
+
+
+def rnd(dtype):
+    return 2.0 ** -8 if dtype == BF16 else U
+
+
+def bits(t):
+    """The bf16 bit patterns of a GPU tensor."""
+    return t.cpu().contiguous().view(torch.int16).numpy().view(np.uint16)
+
+
+# ------------------------------------------------------------------------------- norm
+
+NORM_SHAPES = [(1, 16), (3, 32), (5, 48), (1, 4096), (17, 512), (40, 528), (64, 1040), (1030, 1024),
+               (1100, 2080), (1025, 4096), (9, 4112), (7, 8192), (3, 16384), (2, 16400), (2, 65536),
+               (2500, 96), (9000, 64)]
+
+
+def norm_inputs(m, k, seed, residual):
+    x = W.random_bf16(m, k, seed, "student_t").to(DEV)
+    r = W.random_bf16(m, k, seed + 1, "normal", scale=3.0).to(DEV) if residual else None
+    w = W.random_bf16(1, k, seed + 2, "normal")[0].to(DEV)
+    return x, r, w
+
+
+def check_norm(o, x, r, w, eps):
+    """h, rstd and the bits of y, which are returned (as a CPU bf16 tensor)."""
+    h = x.cpu() if r is None else (x.cpu().float() + r.cpu().float()).to(BF16)
+    assert torch.equal(o.h.cpu(), h)
+    _, rstd = FF.rmsnorm64(h.double().numpy(), w.cpu().double().numpy(), eps)
+    within(o.rstd.cpu().double().numpy(), rstd, (1 + 2.0 ** -10) * U * rstd, "rstd")
+    y = (h.float() * o.rstd.cpu()[:, None] * w.cpu().float()).to(BF16)
+    if o.y is not None:
+        assert torch.equal(o.y.cpu(), y)
+    return y
+
+
+@pytest.mark.parametrize("m,k", NORM_SHAPES)
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_bf16(fos, m, k, residual):
+    x, r, w = norm_inputs(m, k, m + k, residual)
+    check_norm(fos.rmsnorm_fwd(x, w, eps=1e-5, residual=r), x, r, w, 1e-5)
+
+
+@pytest.mark.parametrize("m,k", NORM_SHAPES)
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_nvfp4(fos, m, k, given, residual):
+    x, r, w = norm_inputs(m, k, m + k + 7, residual)
+    t = torch.tensor([0.002], device=DEV) if given else None
+    o = fos.rmsnorm_fwd(x, w, residual=r, format="nvfp4", tensor_scale=t, return_y=not given)
+    y = check_norm(o, x, r, w, 1e-6)
+    want = N.quantize(bits(y), N.Config(), None if t is None else np.float32(0.002))
+    assert np.float32(o.record.tensor_scale.cpu()[0]) == want["t"]
+    assert_same_bytes(o.record.data.cpu().numpy(), want["row_data"], "data")
+    assert_same_bytes(o.record.scales.cpu().numpy(), want["row_scales"], "scales")
+
+
+@pytest.mark.parametrize("m,k", [s for s in NORM_SHAPES if s[1] % 32 == 0])
+def test_norm_mxfp4(fos, m, k):
+    x, r, w = norm_inputs(m, k, m + k + 9, m % 2)
+    o = fos.rmsnorm_fwd(x, w, residual=r, format="mxfp4", return_y=bool(k % 64))
+    want = MX.quantize(bits(check_norm(o, x, r, w, 1e-6)))
+    assert_same_bytes(o.record.data.cpu().numpy(), want["data"], "data")
+    assert_same_bytes(o.record.scales.cpu().numpy(), want["scales"], "scales")
+
+
+def test_norm_rule_six(fos):
+    x, r, w = norm_inputs(33, 160, 3, True)
+    o = fos.rmsnorm_fwd(x, w, residual=r, format="nvfp4", rule="6")
+    want = N.quantize(bits(check_norm(o, x, r, w, 1e-6)), N.Config(rule="6"))
+    assert_same_bytes(o.record.data.cpu().numpy(), want["row_data"], "data")
+    assert_same_bytes(o.record.scales.cpu().numpy(), want["row_scales"], "scales")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4", "mxfp4"])
+@pytest.mark.parametrize("m", [1, 5, 1200])
+def test_norm_strided_rows(fos, fmt, m):
+    k = 320
+    wide = torch.full((m, 2 * k + 48), float("nan"), dtype=BF16, device=DEV)
+    x, r, w = norm_inputs(m, k, 4, True)
+    wide[:, 8:8 + k], wide[:, k + 24:2 * k + 24] = x, r
+    want = fos.rmsnorm_fwd(x, w, residual=r, format=fmt)
+    got = fos.rmsnorm_fwd(wide[:, 8:8 + k], w, residual=wide[:, k + 24:2 * k + 24], format=fmt)
+    assert torch.equal(got.h, want.h) and torch.equal(got.rstd, want.rstd)
+    if fmt == "bf16":
+        assert torch.equal(got.y, want.y)
+    else:
+        assert torch.equal(got.record.data, want.record.data)
+        assert torch.equal(got.record.scales, want.record.scales)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4", "mxfp4"])
+def test_norm_sum_in_place(fos, fmt):
+    """The residual stream updated where it lies, rows around it untouched."""
+    m, k = 37, 544
+    x, r, w = norm_inputs(m, k, 5, True)
+    want = fos.rmsnorm_fwd(x, w, residual=r, format=fmt)
+    stream = torch.full((m + 2, k), 7.0, dtype=BF16, device=DEV)
+    stream[1:-1] = r
+    got = fos.rmsnorm_fwd(x, w, residual=stream[1:-1], format=fmt, h=stream[1:-1])
+    assert torch.equal(stream[1:-1], want.h) and torch.equal(got.rstd, want.rstd)
+    assert (stream[0] == 7).all() and (stream[-1] == 7).all()
+    for a, b in ((got.y, want.y),) if fmt == "bf16" else ((got.record.data, want.record.data),):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4", "mxfp4"])
+def test_norm_extreme_rows(fos, fmt):
+    """A row of zeros, one of values whose squares pass fp32, one of subnormals, one value alone."""
+    k = 96
+    x = torch.zeros(4, k)
+    x[1], x[2] = 1.0e37 * torch.sign(torch.randn(k, generator=torch.Generator().manual_seed(1))), 1e-39
+    x[3, 95] = -5.0
+    x, w = x.to(BF16).to(DEV), W.random_bf16(1, k, 6, "normal")[0].to(DEV)
+    o = fos.rmsnorm_fwd(x, w, eps=1e-30, format=fmt, return_y=True)
+    y = check_norm(o, x, None, w, 1e-30)
+    assert torch.isfinite(y).all() and (o.y[0] == 0).all()
+    if fmt == "nvfp4":
+        want = N.quantize(bits(y), N.Config())
+        assert_same_bytes(o.record.data.cpu().numpy(), want["row_data"], "data")
+    if fmt == "mxfp4":
+        assert_same_bytes(o.record.data.cpu().numpy(), MX.quantize(bits(y))["data"], "data")
+
+
+def test_norm_of_no_rows(fos):
+    x, w = torch.empty(0, 64, dtype=BF16, device=DEV), torch.ones(64, dtype=BF16, device=DEV)
+    for fmt in ("bf16", "nvfp4", "mxfp4"):
+        o = fos.rmsnorm_fwd(x, w, residual=x, format=fmt)
+        assert o.h.shape == (0, 64) and o.rstd.shape == (0,)
+        if fmt == "nvfp4":
+            assert float(o.record.tensor_scale) == 0.0
+    dx, dw = fos.rmsnorm_bwd(x, x, w, torch.empty(0, device=DEV))
+    assert dx.shape == (0, 64) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("m,k", NORM_SHAPES)
+@pytest.mark.parametrize("direct", [False, True])
+def test_norm_bwd(fos, m, k, direct):
+    h, dh, w = norm_inputs(m, k, m + k + 11, direct)
+    dy = W.random_bf16(m, k, m + 1, "normal", scale=0.1).to(DEV)
+    rstd = fos.rmsnorm_fwd(h, w).rstd
+    dx, dw = fos.rmsnorm_bwd(dy, h, w, rstd, dh=dh)
+    ref, rdw, size, sdw = FF.rmsnorm_bwd64(f64(dy), f64(h), f64(w), rstd.cpu().double().numpy(),
+                                           None if dh is None else f64(dh))
+    err = (k + 12) * U * size
+    within(f64(dx), ref, 2.0 ** -8 * (np.abs(ref) + err) + err, "dx")
+    within(dw.cpu().double().numpy(), rdw, (m + 4) * U * sdw, "dw")
+    again = fos.rmsnorm_bwd(dy, h, w, rstd, dh=dh)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+    assert fos.rmsnorm_bwd(dy, h, w, rstd, dh=dh, need_dweight=False)[1] is None
+
+
+# --------------------------------------------------------------------------- epilogue
+
+def product_bound(z, size, act, k, dtype):
+    """(y's error before its rounding is added, for an activation of z)"""
+    return 1.13 * (k + 8) * U * size + 16 * U * (1 + np.abs(z))
+
+
+def check_epilogue(y, z_kept, x, w, bias, act, gated, residual, k):
+    """x, w: operands in fp64, scales applied."""
+    z, size = x @ w.T, np.abs(x) @ np.abs(w).T
+    if bias is not None:
+        z, size = z + bias, size + np.abs(bias)
+    ez = (k + 8) * U * size
+    if z_kept is not None:
+        within(f64(z_kept), z, 2.0 ** -8 * (np.abs(z) + ez) + ez + 2.0 ** -133, "preact")
+    ref = FF.epilogue64(z, act, gated, residual)
+    if gated:
+        half = z.shape[1] // 2
+        f = np.abs(FF.activation64(act, z[:, :half])[0])
+        ef = 1.13 * ez[:, :half] + 16 * U * (1 + np.abs(z[:, :half]))
+        err = ef * (np.abs(z[:, half:]) + ez[:, half:]) + f * ez[:, half:] + 2 * U * np.abs(ref)
+    else:
+        err = 1.13 * ez + 16 * U * (1 + np.abs(z))
+        if residual is not None:
+            err = err + 2 * U * (np.abs(ref) + np.abs(residual))
+    within(f64(y), ref, rnd(y.dtype) * (np.abs(ref) + err) + err + 2.0 ** -133, "y")
+
+
+Q_SHAPES = [(1, 1, 64), (16, 16, 64), (3, 130, 256), (130, 100, 256), (256, 256, 256), (257, 300, 512),
+            (100, 515, 320), (300, 128, 1024), (513, 260, 192), (64, 1027, 768), (700, 64, 512)]
+
+
+def nv_act(fos, m, k, seed):
+    return nv_weight(fos, m, k, seed, scale=1.0)
+
+
+@pytest.mark.parametrize("m,n,k", Q_SHAPES)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_qlinear_epilogue(fos, m, n, k, gated, fmt):
+    nv = fmt == "nvfp4"
+    if not nv and k % 256:
+        pytest.skip("MXFP4 products take whole 256s")
+    i = Q_SHAPES.index((m, n, k))
+    act = FF.ACTIVATIONS[(i + 2 * gated + nv) % 5]
+    out = BF16 if (i + gated) % 3 else torch.float32
+    rows = 2 * n if gated else n
+    xd, xs, xt, xq = (nv_act if nv else mx_weight)(fos, m, k, m + k)
+    wd, ws, wt, wq = (nv_weight if nv else mx_weight)(fos, rows, k, n + k)
+    bias = W.random_bf16(1, rows, m, "normal")[0].to(DEV) if i % 2 else None
+    res = W.random_bf16(m, n, n, "normal").to(DEV) if not gated and i % 3 == 0 else None
+    kw = dict(bias=bias, activation=act, out_dtype=out, return_preact=i % 2 == 0)
+    if gated:
+        f = fos.qglu_fwd if nv else fos.mx_qglu_fwd
+    else:
+        f = fos.qlinear_epilogue_fwd if nv else fos.mx_qlinear_epilogue_fwd
+        kw["residual"] = res
+    got = f(xq, wq, **kw)
+    y, z = got if kw["return_preact"] else (got, None)
+    a = operand_exact(xd, xs) * xt if nv else MX.operand_exact(xd, xs)
+    b = operand_exact(wd, ws) * wt if nv else MX.operand_exact(wd, ws)
+    check_epilogue(y, z, a, b, None if bias is None else f64(bias), act, gated,
+                   None if res is None else f64(res), k)
+    again = f(xq, wq, **kw)
+    assert torch.equal(y, again[0] if kw["return_preact"] else again)
+
+
+@pytest.mark.parametrize("k", [256, 320])
+def test_qlinear_epilogue_without_one_is_qlinear(fos, k):
+    _, _, _, xq = nv_act(fos, 260, k, 1)
+    _, _, _, wq = nv_weight(fos, 390, k, 2)
+    want = fos.qlinear_fwd(xq, wq)
+    assert torch.equal(fos.qlinear_epilogue_fwd(xq, wq), want)
+    y, z = fos.qlinear_epilogue_fwd(xq, wq, activation="relu", return_preact=True)
+    assert torch.equal(z, want) and torch.equal(y, want.relu())
+
+
+@pytest.mark.parametrize("n", [256, 258, 131])
+def test_qlinear_epilogue_residual_in_place_and_strided(fos, n):
+    """The residual stream updated where it lies; a residual of odd stride beside NaNs."""
+    m, k = 270, 256
+    _, _, _, xq = nv_act(fos, m, k, 3)
+    _, _, _, wq = nv_weight(fos, n, k, 4)
+    res = W.random_bf16(m, n, 5, "normal").to(DEV)
+    want = fos.qlinear_epilogue_fwd(xq, wq, residual=res)
+    for shift in (0, 1):
+        wide = torch.full((m, n + 3), float("nan"), dtype=BF16, device=DEV)
+        wide[:, shift:shift + n] = res
+        assert torch.equal(fos.qlinear_epilogue_fwd(xq, wq, residual=wide[:, shift:shift + n]), want)
+    stream = torch.full((m + 2, n), 7.0, dtype=BF16, device=DEV)
+    stream[1:-1] = res
+    fos.qlinear_epilogue_fwd(xq, wq, residual=stream[1:-1], out=stream[1:-1])
+    assert torch.equal(stream[1:-1], want)
+    assert (stream[0] == 7).all() and (stream[-1] == 7).all()
+
+
+W_SHAPES = [(1, 1, 32), (1, 256, 256), (1, 4096, 512), (2, 130, 1024), (3, 17, 96), (4, 64, 2080),
+            (5, 33, 1056), (7, 300, 64), (16, 512, 1024), (17, 100, 288), (31, 63, 544),
+            (33, 16, 2048), (61, 259, 1312), (64, 1024, 512), (65, 40, 352), (130, 96, 160),
+            (16, 3, 12320), (1, 6000, 128), (24, 9000, 64), (60, 9000, 64)]
+
+
+@pytest.mark.parametrize("m,n,k", W_SHAPES)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_wlinear_epilogue(fos, m, n, k, gated, fmt):
+    nv = fmt == "nvfp4"
+    i = W_SHAPES.index((m, n, k))
+    act = FF.ACTIVATIONS[(i + 3 * gated + nv) % 5]
+    out = BF16 if (i + gated) % 3 else torch.float32
+    rows = 2 * n if gated else n
+    wd, ws, wt, wq = (nv_weight if nv else mx_weight)(fos, rows, k, n + k)
+    wide = torch.full((m, k + 24), float("nan"), dtype=BF16, device=DEV)
+    wide[:, 8:8 + k] = W.random_bf16(m, k, m + k, "student_t").to(DEV)
+    x = wide[:, 8:8 + k]
+    bias = W.random_bf16(1, rows, m, "normal")[0].to(DEV) if i % 2 else None
+    res = W.random_bf16(m, n, n, "normal").to(DEV) if not gated and i % 3 == 0 else None
+    kw = dict(bias=bias, activation=act, out_dtype=out, return_preact=i % 2 == 0)
+    if gated:
+        f = fos.wglu_fwd if nv else fos.mx_wglu_fwd
+    else:
+        f = fos.wlinear_epilogue_fwd if nv else fos.mx_wlinear_epilogue_fwd
+        kw["residual"] = res
+    got = f(x, wq, **kw)
+    y, z = got if kw["return_preact"] else (got, None)
+    b = operand_exact(wd, ws) * wt if nv else MX.operand_exact(wd, ws)
+    check_epilogue(y, z, f64(x), b, None if bias is None else f64(bias), act, gated,
+                   None if res is None else f64(res), k)
+
+
+@pytest.mark.parametrize("m", [1, 20])
+def test_wlinear_epilogue_residual_in_place(fos, m):
+    n, k = 272, 512
+    _, _, _, wq = mx_weight(fos, n, k, 4)
+    x, res = W.random_bf16(m, k, 1, "normal").to(DEV), W.random_bf16(m, n, 5, "normal").to(DEV)
+    want = fos.mx_wlinear_epilogue_fwd(x, wq, residual=res)
+    stream = torch.full((m + 2, n), 7.0, dtype=BF16, device=DEV)
+    stream[1:-1] = res
+    fos.mx_wlinear_epilogue_fwd(x, wq, residual=stream[1:-1], out=stream[1:-1])
+    assert torch.equal(stream[1:-1], want)
+    assert (stream[0] == 7).all() and (stream[-1] == 7).all()
+
+
+def test_wlinear_epilogue_of_no_rows(fos):
+    _, _, _, wq = nv_weight(fos, 32, 64, 1)
+    x = torch.empty(0, 64, dtype=BF16, device=DEV)
+    assert fos.wlinear_epilogue_fwd(x, wq, activation="silu").shape == (0, 32)
+    y, z = fos.wglu_fwd(x, wq, return_preact=True)
+    assert y.shape == (0, 16) and z.shape == (0, 32)
+
+
+# --------------------------------------------------------------------------- backward
+
+B_SHAPES = [(1, 1), (1, 16), (3, 8), (17, 33), (64, 512), (5, 520), (130, 1000), (300, 72), (2100, 64),
+            (70, 4099), (5000, 8)]
+
+
+@pytest.mark.parametrize("m,n", B_SHAPES)
+@pytest.mark.parametrize("gated", [False, True])
+def test_epilogue_bwd(fos, m, n, gated):
+    act = FF.ACTIVATIONS[(B_SHAPES.index((m, n)) + 2 * gated) % 5]
+    z = W.random_bf16(m, 2 * n if gated else n, m + n, "student_t").to(DEV)
+    dy = W.random_bf16(m, n, m, "normal", scale=0.1).to(DEV)
+    check_bwd(fos, dy, z, act, gated)
+
+
+def check_bwd(fos, dy, z, act, gated):
+    dz, dbias, t = fos.epilogue_bwd(dy, z, act, gated=gated, return_dbias=True, return_tensor_scale=True)
+    d, zz = f64(dy), f64(z)
+    ref = FF.epilogue_bwd64(d, zz, act, gated)
+    half = d.shape[1]
+    gate = zz[:, :half]
+    slope = 32 * U * (1 + np.minimum(np.abs(gate), 16)) + 2 * U * np.abs(FF.activation64(act, gate)[1])
+    if gated:
+        value = 16 * U * (1 + np.abs(gate))
+        err = np.concatenate((np.abs(d * zz[:, half:]) * slope, np.abs(d) * value), 1) + 2 * U * np.abs(ref)
+    else:
+        err = np.abs(d) * slope + 2 * U * np.abs(ref)
+    within(f64(dz), ref, 2.0 ** -8 * (np.abs(ref) + err) + err + 2.0 ** -133, "dz")
+    m = d.shape[0]
+    within(dbias.cpu().double().numpy(), ref.sum(0), (err + (m + 1) * U * np.abs(ref)).sum(0) + 2.0 ** -126,
+           "dbias")
+    assert float(t) == float(N.tensor_scale_from_amax(np.float32(f64(dz).__abs__().max())))
+    assert torch.equal(fos.epilogue_bwd(dy, z, act, gated=gated), dz)
+    again = fos.epilogue_bwd(dy, z, act, gated=gated, return_dbias=True)
+    assert torch.equal(again[0], dz) and torch.equal(again[1], dbias)
+    only = fos.epilogue_bwd(dy, z, act, gated=gated, return_tensor_scale=True)
+    assert torch.equal(only[1], t)
+
+
+@pytest.mark.parametrize("act", FF.ACTIVATIONS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_epilogue_bwd_over_the_whole_range(fos, act, gated):
+    """Every finite bf16 pre-activation (of the gate), from -3.4e38 to 3.4e38."""
+    pat = np.arange(1 << 16, dtype=np.uint32).astype(np.uint16)
+    pat = pat[np.isfinite(F.bf16_bits_to_f32(pat))]
+    z = torch.from_numpy(pat.view(np.int16).copy()).view(BF16).to(DEV).reshape(-1, 16)
+    dy = W.random_bf16(z.shape[0], 16, 1, "normal", scale=0.1).to(DEV)
+    if gated:
+        z = torch.cat((z, torch.full_like(z, 0.5)), 1)
+        # act(z) dY of the largest z passes fp32 where |dY| is above 1
+        assert float(dy.abs().max()) < 1
+    dz = fos.epilogue_bwd(dy, z, act, gated=gated)
+    assert torch.isfinite(dz).all()
+    keep = (z[:, :16].float().abs() < 1e4).all(1)
+    check_bwd(fos, dy[keep].contiguous(), z[keep].contiguous(), act, gated)
+    far = f64(z[~keep][:, :16])
+    want = FF.epilogue_bwd64(f64(dy[~keep]), f64(z[~keep]), act, gated)
+    got = f64(dz[~keep])
+    assert (np.abs(got - want) <= 2.0 ** -7 * np.abs(want) + 1e-36).all(), far
+
+
+def test_epilogue_bwd_unaligned_and_empty(fos):
+    z = W.random_bf16(40, 64, 1, "normal").to(DEV)
+    dy = W.random_bf16(40, 64, 2, "normal").to(DEV)
+    want = fos.epilogue_bwd(dy, z, "silu", return_dbias=True)
+    flat = torch.empty(40 * 64 + 1, dtype=BF16, device=DEV)
+    flat[1:] = z.flatten()
+    got = fos.epilogue_bwd(dy, flat[1:].view(40, 64), "silu", return_dbias=True)
+    assert torch.equal(got[0], want[0])
+    within(got[1].cpu().double().numpy(), want[1].cpu().double().numpy(),
+           2 * 41 * U * np.abs(f64(want[0])).sum(0) * (1 + 2.0 ** -7), "dbias")
+    dz, dbias, t = fos.epilogue_bwd(dy[:0], z[:0], return_dbias=True, return_tensor_scale=True)
+    assert dz.shape == (0, 64) and (dbias == 0).all() and float(t) == 0
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_product_backward(fos, gated):
+    """dX, dW and dbias are the products of the records of dZ, with the given options."""
+    m, n, k = 192, 128, 320
+    rows = 2 * n if gated else n
+    x, w = W.random_bf16(m, k, 1, "normal").to(DEV), W.random_bf16(rows, k, 2, "normal", scale=0.02).to(DEV)
+    xt, wt = fos.quantize(x, outputs=("col",)), fos.quantize(w, outputs=("col",), block="2d")
+    z = W.random_bf16(m, rows, 3, "normal").to(DEV)
+    dy = W.random_bf16(m, n, 4, "normal", scale=1e-3).to(DEV)
+    f = fos.qglu_bwd if gated else fos.qlinear_epilogue_bwd
+    for rounding, seed in (("rne", None), ("sr", 5)):
+        dx, dw, db = f(dy, z, xt, wt, activation="silu", return_dbias=True, rounding=rounding, sr_seed=seed)
+        dz, dbias = fos.epilogue_bwd(dy, z, "silu", gated=gated, return_dbias=True)
+        a, b = fos.quantize(dz, outputs=("row", "col"), rounding=rounding, sr_seed=seed)
+        want = fos.qlinear_bwd(a, b, xt, wt)
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]) and torch.equal(db, dbias)
+    dx, none = f(dy, z, None, wt, activation="silu", need_dw=False)
+    assert none is None and torch.equal(dx, f(dy, z, xt, wt, activation="silu")[0])
+    none, dw = f(dy, z, xt, None, activation="silu", need_dx=False)
+    assert none is None and torch.equal(dw, f(dy, z, xt, wt, activation="silu")[1])
