@@ -105,7 +105,9 @@ struct EpilogueArgs {
   uint16_t* preact;          // bf16 [M][weight rows] or null
   int act;
   bool f32_out;
-  bool wide;                 // four columns of y, residual and preact can be accessed at once
+  bool pair;                 // two columns of y, residual and preact can be accessed at once
 };
+// Largest sizes that the GEMM kernels' epilogue addresses.
+constexpr int64_t kMaxEpilogueCols = 1 << 20, kMaxResidualStride = 1 << 22;
 
 }  // namespace fos

@@ -64,9 +64,9 @@ fos::EpilogueArgs epilogue_args(const fos_epilogue* e, int64_t M, int64_t N, con
   a.preact = static_cast<uint16_t*>(e->preact_bf16);
   a.act = (int)e->activation;
   a.f32_out = e->out_dtype == FOS_OUT_F32;
-  a.wide = N % 4 == 0 && aligned(y, a.f32_out ? 16 : 8) && aligned(e->preact_bf16, 8) &&
+  a.pair = N % 2 == 0 && aligned(y, 4) && aligned(e->preact_bf16, 4) &&
            (!e->residual_bf16 ||
-            (aligned(e->residual_bf16, 8) && (M == 1 || e->residual_stride % 4 == 0)));
+            (aligned(e->residual_bf16, 4) && (M == 1 || e->residual_stride % 2 == 0)));
   return a;
 }
 
@@ -79,6 +79,8 @@ fos_status run_qlinear(const uint8_t* xd, const uint8_t* xs, const float* xt, co
   fos_status st = check_epilogue(e, M, N, y);
   if (st != FOS_OK) return st;
   const int64_t W = e->gated ? 2 * N : N;   // weight rows
+  if (N > fos::kMaxEpilogueCols || (e->residual_bf16 && e->residual_stride > fos::kMaxResidualStride))
+    return FOS_E_SHAPE;
   if (W > kMaxElems / M || K > kMaxElems / M || K > kMaxElems / W) return FOS_E_SHAPE;
   // each packed operand is addressed through one buffer resource (< 4 GiB)
   if ((M + 256) * (K / 2) >= ((int64_t)1 << 32) || (W + 256) * (K / 2) >= ((int64_t)1 << 32))

@@ -1,10 +1,8 @@
-// Epilogue of the GEMM kernels' tiles with bias, activation, gate and residual.
-//
-// A wave's accumulators hold one column and 16 rows of each 32x32 tile a lane; y is written,
-// and the residual read, fastest where a lane has neighbouring columns.  So each strip of 32
-// rows goes through the wave's own LDS as fp32 and comes back four columns to a lane: whole
-// 128- or 256-byte runs of a row a wave instruction, and one short loop that knows the
-// activation instead of 256 unrolled values that each do.
+// Epilogue of the GEMM kernels' tiles with bias, activation, gate and residual, from the
+// accumulators' own layout: element a of lane (lr, h) is row (a & 3) + 8 (a >> 2) + 4h and
+// column lr of a 32x32 tile.  Nothing of it overlaps the products of its own workgroup, and
+// its arithmetic bounds it: at 256 values a lane (the 256x256 tile) silu takes 4 us, most of
+// it the two quarter-rate instructions of a value.
 #pragma once
 
 #include "activation.hpp"
@@ -17,13 +15,6 @@ namespace gemm {
 // kGated too, with gate and other projection in neighbouring 32-column tiles.
 enum { kPlain, kFused, kGated };
 
-// Floats between rows of a strip: a multiple of 4 (16-byte reads) with 4 rows apart half the
-// banks (the two lane halves of a write are 4 rows apart).
-template <int TJ>
-constexpr int kStripStride = 32 * TJ + 8;
-template <int TJ>
-constexpr int kStripBytes = 32 * kStripStride<TJ> * 4;   // of each wave
-
 // Weight row behind row r (0 .. 64 TJ - 1) of a gated tile, without the tile's first column:
 // rows come in groups of 32, gate and other projection in turn; `up` says which.
 __device__ __forceinline__ int gated_row(int r, bool& up) {
@@ -31,112 +22,159 @@ __device__ __forceinline__ int gated_row(int r, bool& up) {
   return ((r >> 6) << 5) | (r & 31);
 }
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// Four columns from `n` of a row; those past N (of which `left` remain) are not touched.
-__device__ __forceinline__ f32x4 load_bf16x4(const uint16_t* p, bool wide, int left) {
-  if (wide) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-    return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-  }
-  f32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < left) v[i] = bf16_lo(p[i]);
-  return v;
-}
-__device__ __forceinline__ void store_bf16x4(uint16_t* p, f32x4 v, bool wide, int left) {
-  const u32x2 w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  if (wide) {
-    *reinterpret_cast<u32x2*>(p) = w;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < left) p[i] = (uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
-}
-__device__ __forceinline__ void store_f32x4(float* p, f32x4 v, bool wide, int left) {
-  if (wide) {
-    *reinterpret_cast<f32x4*>(p) = v;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < left) p[i] = v[i];
+// A wave's rows of a row-major matrix as a buffer resource: what lies outside of it is not
+// stored and reads as zero, which takes care of the last rows.  A column outside gets an
+// offset outside (kNowhere); with at most kMaxEpilogueCols columns and kMaxResidualStride
+// (the host checks) 128 rows end below it.
+constexpr uint32_t kNowhere = 0x80000000u;
+struct RowWindow {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t row_bytes;
+};
+__device__ __forceinline__ RowWindow row_window(const void* p, int64_t first, int rows,
+                                                int64_t stride, int cols, int bytes) {
+  RowWindow w;
+  w.row_bytes = (uint32_t)stride * bytes;
+  w.r = __builtin_amdgcn_make_buffer_rsrc(
+      (char*)p + first * stride * bytes, 0,
+      rows > 0 ? (int)((rows - 1) * w.row_bytes + (uint32_t)cols * bytes) : 0, kRsrcWord3);
+  return w;
 }
 
-// One strip: rows m0 .. m0 + 31, the wave's columns from n0 (of y).
-template <int TJ, bool kGate, int kAct>
-__device__ __forceinline__ void fused_strip(const EpilogueArgs& e, void* y, const float* strip,
-                                            int M, int N, int m0, int n0, int lane,
-                                            f32x4 bias, f32x4 bias_up) {
-  constexpr int kS = kStripStride<TJ>;
-  constexpr int kCols = kGate ? 16 * TJ : 32 * TJ, kAcross = kCols / 4, kRows = 64 / kAcross;
-  const int c = 4 * (lane % kAcross), r0 = lane / kAcross;
-  const int col = kGate ? 64 * (c >> 5) + (c & 31) : c;
-  const int n = n0 + c, left = N - n;
-  if (left <= 0) return;
-  const bool wide = e.wide && left >= 4;
-#pragma unroll 4
-  for (int i = 0; i < 32 / kRows; ++i) {
-    const int r = i * kRows + r0;
-    const int64_t m = m0 + r;
-    f32x4 z = *reinterpret_cast<const f32x4*>(strip + r * kS + col), u = {0, 0, 0, 0};
-    if (m >= M) continue;
-    z += bias;
-    if constexpr (kGate) {
-      u = *reinterpret_cast<const f32x4*>(strip + r * kS + col + 32);
-      u += bias_up;
-    }
-    if (e.preact) {
-      uint16_t* p = e.preact + m * (kGate ? 2 * (int64_t)N : N) + n;
-      store_bf16x4(p, z, wide, left);
-      if constexpr (kGate) store_bf16x4(p + N, u, wide, left);
-    }
-    f32x4 v;
+// Adjacent lanes swap halves of a packed pair: from (row r, row r + 1) of the lane's own
+// column to the even lane's row r, columns (c, c + 1) and the odd lane's row r + 1, columns
+// (c - 1, c), and (unswap) back.
+__device__ __forceinline__ uint32_t swap_pairs(uint32_t p, int odd) {
+  const uint32_t q = __builtin_amdgcn_update_dpp(0u, p, 0xB1, 0xF, 0xF, false);
+  return __builtin_amdgcn_perm(q, p, odd ? 0x03020706u : 0x05040100u);
+}
+
+// The 16 values of one 32x32 tile of bf16 in packed pairs of rows (a, a + 1): stored, or
+// loaded.  `row`: the tile's first row in the window; `col`: the lane's column, kNowhere if
+// there is none.  `pair`: 4-byte accesses of two columns (even columns, 4-byte alignment).
+__device__ __forceinline__ void store_bf16_tile(const RowWindow& w, const uint32_t (&v)[8], int row,
+                                                uint32_t col, int h, int odd, bool pair) {
+  if (pair) {
+    const uint32_t at = col == kNowhere ? col : (row + 4 * h + odd) * w.row_bytes + 2 * (col - odd);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = activate<kAct>(z[k]);
-      if constexpr (kGate) v[k] *= u[k];
-    }
-    if (e.residual) v += load_bf16x4(e.residual + m * e.residual_stride + n, wide, left);
-    if (e.f32_out) store_f32x4(static_cast<float*>(y) + m * N + n, v, wide, left);
-    else store_bf16x4(static_cast<uint16_t*>(y) + m * N + n, v, wide, left);
+    for (int a = 0; a < 16; a += 2)
+      __builtin_amdgcn_raw_buffer_store_b32(swap_pairs(v[a / 2], odd), w.r, at,
+                                            (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
+  } else {
+    const uint32_t at = col == kNowhere ? col : (row + 4 * h) * w.row_bytes + 2 * col;
+#pragma unroll
+    for (int a = 0; a < 16; ++a)
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[a / 2] >> (16 * (a & 1))), w.r, at,
+                                            (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
+  }
+}
+__device__ __forceinline__ void load_bf16_tile(const RowWindow& w, uint32_t (&v)[16], int row,
+                                               uint32_t col, int h, int odd, bool pair) {
+  if (pair) {
+    const uint32_t at = col == kNowhere ? col : (row + 4 * h + odd) * w.row_bytes + 2 * (col - odd);
+#pragma unroll
+    for (int a = 0; a < 16; a += 2)
+      v[a / 2] = __builtin_amdgcn_raw_buffer_load_b32(
+          w.r, at, (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
+  } else {
+    const uint32_t at = col == kNowhere ? col : (row + 4 * h) * w.row_bytes + 2 * col;
+#pragma unroll
+    for (int a = 0; a < 16; ++a)
+      v[a] = __builtin_amdgcn_raw_buffer_load_b16(
+          w.r, at, (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
   }
 }
 
-// The whole tile of a wave: `strip` is its kStripBytes<TJ> of LDS, which no wave reads or
-// writes otherwise any more; s multiplies the sums.
-template <int TI, int TJ, bool kGate>
-__device__ __forceinline__ void store_fused(const EpilogueArgs& e, void* y, float* strip, int M,
-                                            int N, int m0, int n0, int lane, float s,
-                                            const f32x16 (&acc)[TI][TJ]) {
-  constexpr int kS = kStripStride<TJ>;
-  constexpr int kAcross = (kGate ? 16 * TJ : 32 * TJ) / 4;
-  const int lr = lane & 31, h = lane >> 5;
-  const int n = n0 + 4 * (lane % kAcross);
-  f32x4 bias = {0, 0, 0, 0}, bias_up = {0, 0, 0, 0};
-  if (e.bias && n < N) {
-    bias = load_bf16x4(e.bias + n, false, N - n);
-    if (kGate) bias_up = load_bf16x4(e.bias + N + n, false, N - n);
+// The tile of a wave, rows m0 .. and columns n0 .. of y: act(s acc + bias) (times the other
+// projection) + residual.  A tile's residual is on its way while the tile before is computed.
+template <int TI, int TJ, bool kGate, int kAct>
+__device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, int M, int N, int m0,
+                                               int n0, int lane, float s,
+                                               const f32x16 (&acc)[TI][TJ]) {
+  constexpr int kStep = kGate ? 2 : 1, kTiles = TJ / kStep;
+  const int lr = lane & 31, h = lane >> 5, odd = lr & 1;
+  const int rows = min(32 * TI, M - m0);
+  const bool pair = e.pair;
+  const RowWindow wy = row_window(y, m0, rows, N, N, e.f32_out ? 4 : 2);
+  const RowWindow wz = row_window(e.preact, m0, e.preact ? rows : 0, kStep * (int64_t)N, kStep * N, 2);
+  const RowWindow wr = row_window(e.residual, m0, e.residual ? rows : 0, e.residual_stride, N, 2);
+  uint32_t col[kTiles];
+  float bias[kTiles], bias_up[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int n = n0 + 32 * t + lr;
+    col[t] = n < N ? (uint32_t)n : kNowhere;
+    bias[t] = bias_up[t] = 0.0f;
+    if (e.bias && n < N) {
+      bias[t] = bf16_lo(e.bias[n]);
+      if (kGate) bias_up[t] = bf16_lo(e.bias[N + n]);
+    }
   }
+  uint32_t next[16] = {};
+  if (e.residual) load_bf16_tile(wr, next, 0, col[0], h, odd, pair);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    if (m0 + 32 * i >= M) break;
 #pragma unroll
-    for (int t = 0; t < TJ; ++t)
+    for (int t = 0; t < kTiles; ++t) {
+      uint32_t res[16];
 #pragma unroll
-      for (int a = 0; a < 16; ++a)
-        strip[((a & 3) + 8 * (a >> 2) + 4 * h) * kS + 32 * t + lr] = acc[i][t][a] * s;
-    const int m = m0 + 32 * i;
-    switch (e.act) {
-      case kActRelu: fused_strip<TJ, kGate, kActRelu>(e, y, strip, M, N, m, n0, lane, bias, bias_up); break;
-      case kActGelu: fused_strip<TJ, kGate, kActGelu>(e, y, strip, M, N, m, n0, lane, bias, bias_up); break;
-      case kActGeluTanh: fused_strip<TJ, kGate, kActGeluTanh>(e, y, strip, M, N, m, n0, lane, bias, bias_up); break;
-      case kActSilu: fused_strip<TJ, kGate, kActSilu>(e, y, strip, M, N, m, n0, lane, bias, bias_up); break;
-      default: fused_strip<TJ, kGate, kActNone>(e, y, strip, M, N, m, n0, lane, bias, bias_up);
+      for (int a = 0; a < 16; ++a) res[a] = next[a];
+      if (e.residual && (i + 1 < TI || t + 1 < kTiles))
+        load_bf16_tile(wr, next, 32 * (t + 1 < kTiles ? i : i + 1), col[(t + 1) % kTiles], h, odd, pair);
+      float v[16];
+      uint32_t z[8], zu[8];
+#pragma unroll
+      for (int a = 0; a < 16; a += 2) {
+        float g[2], u[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          g[b] = __builtin_fmaf(acc[i][kStep * t][a + b], s, bias[t]);
+          v[a + b] = activate<kAct>(g[b]);
+          if constexpr (kGate) {
+            u[b] = __builtin_fmaf(acc[i][kStep * t + 1][a + b], s, bias_up[t]);
+            v[a + b] *= u[b];
+          }
+        }
+        z[a / 2] = pack_bf16x2(g[0], g[1]);
+        if constexpr (kGate) zu[a / 2] = pack_bf16x2(u[0], u[1]);
+      }
+      if (e.preact) {
+        store_bf16_tile(wz, z, 32 * i, col[t], h, odd, pair);
+        if constexpr (kGate)
+          store_bf16_tile(wz, zu, 32 * i, col[t] == kNowhere ? kNowhere : col[t] + N, h, odd, pair);
+      }
+      if (e.residual) {
+#pragma unroll
+        for (int a = 0; a < 16; a += 2) {
+          const uint32_t r = pair ? swap_pairs(res[a / 2], odd) : res[a] | res[a + 1] << 16;
+          v[a] += bf16_lo(r);
+          v[a + 1] += bf16_hi(r);
+        }
+      }
+      if (e.f32_out) {
+        const uint32_t at = col[t] == kNowhere ? kNowhere : (32 * i + 4 * h) * wy.row_bytes + 4 * col[t];
+#pragma unroll
+        for (int a = 0; a < 16; ++a)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[a]), wy.r, at,
+                                                (int)(((a & 3) + 8 * (a >> 2)) * wy.row_bytes), 0);
+      } else {
+#pragma unroll
+        for (int a = 0; a < 16; a += 2) z[a / 2] = pack_bf16x2(v[a], v[a + 1]);
+        store_bf16_tile(wy, z, 32 * i, col[t], h, odd, pair);
+      }
     }
+  }
+}
+
+template <int TI, int TJ, bool kGate>
+__device__ __forceinline__ void store_fused(const EpilogueArgs& e, void* y, int M, int N, int m0,
+                                            int n0, int lane, float s, const f32x16 (&acc)[TI][TJ]) {
+  switch (e.act) {
+    case kActRelu: store_fused_as<TI, TJ, kGate, kActRelu>(e, y, M, N, m0, n0, lane, s, acc); break;
+    case kActGelu: store_fused_as<TI, TJ, kGate, kActGelu>(e, y, M, N, m0, n0, lane, s, acc); break;
+    case kActGeluTanh: store_fused_as<TI, TJ, kGate, kActGeluTanh>(e, y, M, N, m0, n0, lane, s, acc); break;
+    case kActSilu: store_fused_as<TI, TJ, kGate, kActSilu>(e, y, M, N, m0, n0, lane, s, acc); break;
+    default: store_fused_as<TI, TJ, kGate, kActNone>(e, y, M, N, m0, n0, lane, s, acc);
   }
 }
 

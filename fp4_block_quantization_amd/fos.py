@@ -1203,8 +1203,12 @@ def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, roundi
     outputs = (("row",) if need_dx else ()) + (("col",) if need_dw else ())
     with torch.cuda.device(dz.device):
         q = quantize(dz, rounding=rounding, outputs=outputs, sr_seed=sr_seed, tensor_scale=t)
-        rows, cols = q if need_dx and need_dw else (q, None) if need_dx else (None, q)
-        dx, dw = qlinear_bwd(rows, cols, xq_t, wq_t, need_dx, need_dw)
+    rows, cols = q if need_dx and need_dw else (q, None) if need_dx else (None, q)
+    # the products of fos_qlinear_bwd, on the tiles that suit their shapes (dX of 2048 x 4096
+    # with an inner dimension of 8192 has 128 tiles of 256 x 256, half a GPU)
+    product = lambda a, b: _qlinear_epilogue(a, b, False, None, "none", None, _BF16, False, None)
+    dx = product(rows, wq_t) if need_dx else None
+    dw = product(cols, xq_t) if need_dw else None
     return (dx, dw, dbias) if return_dbias else (dx, dw)
 
 

@@ -593,9 +593,8 @@ fos_status fos_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const void* 
  * preact: Z rounded to bf16, [M][N] or gated [M][2N], contiguous: what fos_epilogue_bwd
  * needs.  Pointers may be NULL: without a bias, a residual, a kept Z.  residual: bf16, row
  * stride in elements, at least N (not with a gate); y may be its memory, if that is
- * contiguous and the output bf16.  All 2-byte aligned, y to its type; with N % 4 == 0 and
- * addresses (and the residual's stride) at multiples of four elements, rows are accessed
- * four values at a time. */
+ * contiguous and the output bf16.  All 2-byte aligned, y to its type; with N (and the
+ * residual's stride) even and 4-byte aligned addresses, two values are accessed at a time. */
 typedef struct {
   uint32_t struct_size;       /* must equal sizeof(fos_epilogue)                      */
   uint32_t activation;        /* FOS_ACT_*                                            */
@@ -609,7 +608,8 @@ typedef struct {
 } fos_epilogue;               /* host struct, read only during the call               */
 
 /* fos_qlinear_fwd and fos_mx_qlinear_fwd with an epilogue: their operands, sizes and
- * alignments, where (N + 256) * K / 2 below 2^32 counts the weight's rows (2N with a gate).
+ * alignments, where (N + 256) * K / 2 below 2^32 counts the weight's rows (2N with a gate);
+ * N at most 2^20, residual_stride at most 2^22.
  * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_HIP. */
 fos_status fos_qlinear_epilogue_fwd(const uint8_t* x_data, const uint8_t* x_scales,
                                     const float* x_tensor_scale, const uint8_t* w_data,

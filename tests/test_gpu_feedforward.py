@@ -267,14 +267,66 @@ def test_qlinear_epilogue(fos, m, n, k, gated, fmt):
     assert torch.equal(y, again[0] if kw["return_preact"] else again)
 
 
-@pytest.mark.parametrize("k", [256, 320])
-def test_qlinear_epilogue_without_one_is_qlinear(fos, k):
-    _, _, _, xq = nv_act(fos, 260, k, 1)
-    _, _, _, wq = nv_weight(fos, 390, k, 2)
+# tiles of 256 x 256, and of 128 x 128 with one K step, in more than half a round of
+# workgroups, and split over K, where sums have another order
+@pytest.mark.parametrize("m,n,k,same", [(2300, 7700, 512, True), (260, 390, 256, True),
+                                        (2050, 2304, 512, True), (260, 390, 768, False)])
+def test_qlinear_epilogue_without_one_is_qlinear(fos, m, n, k, same):
+    x, w = (W.random_bf16(r, k, r, "normal").to(DEV) for r in (m, n))
+    xq, wq = fos.quantize(x), fos.quantize(w)
     want = fos.qlinear_fwd(xq, wq)
-    assert torch.equal(fos.qlinear_epilogue_fwd(xq, wq), want)
+    got = fos.qlinear_epilogue_fwd(xq, wq)
     y, z = fos.qlinear_epilogue_fwd(xq, wq, activation="relu", return_preact=True)
+    assert torch.equal(z, got) and torch.equal(y, got.relu())
+    if same:
+        assert torch.equal(got, want)
+    else:
+        size = fos.dequantize(xq).abs() @ fos.dequantize(wq).abs().t()
+        within(f64(got), f64(want), 2.0 ** -7 * f64(want).__abs__() + 2.1 * (k + 8) * U * f64(size), "y")
+
+
+@pytest.mark.parametrize("m,n,k", [(2300, 7700, 512), (700, 390, 768), (1100, 8200, 256)])
+def test_mx_qlinear_epilogue_without_one_is_mx_qlinear(fos, m, n, k):
+    """The same sums in the same order on tiles of 256 x 256, 128 x 128 and 256 x 128."""
+    aq, bq = (fos.mx_quantize(W.random_bf16(r, k, r, "normal").to(DEV)) for r in (m, n))
+    want = fos.mx_qlinear_fwd(aq, bq)
+    assert torch.equal(fos.mx_qlinear_epilogue_fwd(aq, bq), want)
+    y, z = fos.mx_qlinear_epilogue_fwd(aq, bq, activation="relu", return_preact=True)
     assert torch.equal(z, want) and torch.equal(y, want.relu())
+
+
+# more rows than one 256 x 256 tile of the largest kernels, with every option
+@pytest.mark.parametrize("m,n,k,gated,fmt,act", [
+    (4097, 2100, 512, False, "nvfp4", "gelu"), (4097, 1100, 320, True, "nvfp4", "silu"),
+    (4097, 4400, 512, False, "mxfp4", "gelu_tanh"), (8300, 1100, 256, True, "mxfp4", "silu"),
+    (4097, 2099, 256, False, "nvfp4", "silu"), (4097, 4399, 512, False, "mxfp4", "silu")])
+def test_epilogue_of_many_tiles(fos, m, n, k, gated, fmt, act):
+    """Against fp32 products of the dequantized records, whose own error the bound counts."""
+    rows = 2 * n if gated else n
+    x, w = W.random_bf16(m, k, 1, "normal").to(DEV), W.random_bf16(rows, k, 2, "normal", scale=0.02).to(DEV)
+    bias = W.random_bf16(1, rows, 3, "normal")[0].to(DEV)
+    res = None if gated else W.random_bf16(m, n, 4, "normal").to(DEV)
+    nv = fmt == "nvfp4"
+    xq, wq = (fos.quantize(x), fos.quantize(w)) if nv else (fos.mx_quantize(x), fos.mx_quantize(w))
+    a, b = ((fos.dequantize if nv else fos.mx_dequantize)(q).double() for q in (xq, wq))
+    z, size = a @ b.t() + bias.double(), a.abs() @ b.abs().t() + bias.double().abs()
+    kw = dict(bias=bias, activation=act, return_preact=True)
+    if gated:
+        y, got = (fos.qglu_fwd if nv else fos.mx_qglu_fwd)(xq, wq, **kw)
+    else:
+        y, got = (fos.qlinear_epilogue_fwd if nv else fos.mx_qlinear_epilogue_fwd)(xq, wq, residual=res, **kw)
+    z, size = z.cpu().numpy(), size.cpu().numpy()
+    # a dequantized NVFP4 value carries one rounding more (its block scale times the tensor's)
+    ez = (k + 8 + 4) * U * size
+    within(f64(got), z, 2.0 ** -8 * (np.abs(z) + ez) + ez, "preact")
+    ref = FF.epilogue64(z, act, gated, None if res is None else f64(res))
+    e = 1.13 * ez + 16 * U * (1 + np.abs(z))
+    if gated:
+        f = np.abs(FF.activation64(act, z[:, :n])[0])
+        e = e[:, :n] * (np.abs(z[:, n:]) + ez[:, n:]) + f * ez[:, n:] + 2 * U * np.abs(ref)
+    else:
+        e = e + 2 * U * (np.abs(ref) + np.abs(f64(res)))
+    within(f64(y), ref, 2.0 ** -8 * (np.abs(ref) + e) + e, "y")
 
 
 @pytest.mark.parametrize("n", [256, 258, 131])
@@ -428,7 +480,7 @@ def test_epilogue_bwd_unaligned_and_empty(fos):
 
 @pytest.mark.parametrize("gated", [False, True])
 def test_product_backward(fos, gated):
-    """dX, dW and dbias are the products of the records of dZ, with the given options."""
+    """dX and dW are the products of the records of dZ with the given options."""
     m, n, k = 192, 128, 320
     rows = 2 * n if gated else n
     x, w = W.random_bf16(m, k, 1, "normal").to(DEV), W.random_bf16(rows, k, 2, "normal", scale=0.02).to(DEV)
@@ -440,8 +492,14 @@ def test_product_backward(fos, gated):
         dx, dw, db = f(dy, z, xt, wt, activation="silu", return_dbias=True, rounding=rounding, sr_seed=seed)
         dz, dbias = fos.epilogue_bwd(dy, z, "silu", gated=gated, return_dbias=True)
         a, b = fos.quantize(dz, outputs=("row", "col"), rounding=rounding, sr_seed=seed)
-        want = fos.qlinear_bwd(a, b, xt, wt)
+        want = fos.qlinear_epilogue_fwd(a, wt), fos.qlinear_epilogue_fwd(b, xt)
         assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]) and torch.equal(db, dbias)
+        for got, q, other in ((dx, a, wt), (dw, b, xt)):
+            u, v = (operand_exact(r.data.cpu().numpy(), r.scales.cpu().numpy()) * float(r.tensor_scale)
+                    for r in (q, other))
+            ref, size = u @ v.T, np.abs(u) @ np.abs(v).T
+            err = (u.shape[1] + 8) * U * size
+            within(f64(got), ref, 2.0 ** -8 * (np.abs(ref) + err) + err, "product")
     dx, none = f(dy, z, None, wt, activation="silu", need_dw=False)
     assert none is None and torch.equal(dx, f(dy, z, xt, wt, activation="silu")[0])
     none, dw = f(dy, z, xt, None, activation="silu", need_dx=False)
