@@ -105,7 +105,7 @@ struct EpilogueArgs {
   uint16_t* preact;          // bf16 [M][weight rows] or null
   int act;
   bool f32_out;
-  bool pair;                 // two columns of y, residual and preact can be accessed at once
+  bool pair, quad;           // two, four columns can be accessed at once (quad: of bias, too)
 };
 // Largest sizes that the GEMM kernels' epilogue addresses.
 constexpr int64_t kMaxEpilogueCols = 1 << 20, kMaxResidualStride = 1 << 22;

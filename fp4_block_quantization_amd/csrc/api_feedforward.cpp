@@ -67,6 +67,10 @@ fos::EpilogueArgs epilogue_args(const fos_epilogue* e, int64_t M, int64_t N, con
   a.pair = N % 2 == 0 && aligned(y, 4) && aligned(e->preact_bf16, 4) &&
            (!e->residual_bf16 ||
             (aligned(e->residual_bf16, 4) && (M == 1 || e->residual_stride % 2 == 0)));
+  a.quad = N % 4 == 0 && aligned(y, a.f32_out ? 16 : 8) && aligned(e->preact_bf16, 8) &&
+           aligned(e->bias_bf16, 8) &&
+           (!e->residual_bf16 ||
+            (aligned(e->residual_bf16, 8) && (M == 1 || e->residual_stride % 4 == 0)));
   return a;
 }
 

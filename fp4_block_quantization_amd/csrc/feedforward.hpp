@@ -6,7 +6,7 @@
 
 namespace fos {
 
-constexpr int kMaxNormCols = 65536;      // a workgroup holds a row in registers
+constexpr int kMaxNormCols = 32768;      // a workgroup holds a row in registers
 
 enum : int { kRecordNone, kRecordNVFP4, kRecordMXFP4 };
 

@@ -41,6 +41,17 @@ __device__ __forceinline__ Block pack_block(const float (&v)[16]) {
                           pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]))};
 }
 constexpr Block kZeroBlock = {};
+// The same block, which the compiler takes for another: values unpacked from it are not kept
+// in registers from (or for) elsewhere.
+__device__ __forceinline__ Block again(Block v) {
+  asm volatile("" : "+v"(v.a.x), "+v"(v.a.y), "+v"(v.a.z), "+v"(v.a.w));
+  asm volatile("" : "+v"(v.b.x), "+v"(v.b.y), "+v"(v.b.z), "+v"(v.b.w));
+  return v;
+}
+__device__ __forceinline__ void unpack_again(const Block& b, float (&v)[16]) {
+  const Block c = again(b);
+  unpack16(c.a, c.b, v);
+}
 
 // Sum over the kLanes lanes of a row, in all of them.  `part`: LDS for two rows in turn (one
 // barrier a row), used where a row has more than one wave.
@@ -53,6 +64,7 @@ __device__ __forceinline__ T row_sum(T v, T (*part)[16], int turn) {
     T* p = part[turn & 1];
     if ((threadIdx.x & 63) == 0) p[threadIdx.x >> 6] = v;
     __syncthreads();
+    p += threadIdx.x / kLanes * (kLanes / 64);
     v = p[0];
 #pragma unroll
     for (int w = 1; w < kLanes / 64; ++w) v += p[w];
@@ -75,6 +87,25 @@ void rmsnorm_kernel(NormArgs a, int npartials) {
   __shared__ float2 tab[kNV ? kScaleTableSize : 1];
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int blocks = a.K / 16;
+
+  // the first row is on its way while the scale table is made, in the second launch every
+  // row while the one before is quantized
+  Block h[kBlocks], next[kBlocks];
+  int64_t row = (int64_t)blockIdx.x * kRows + sub;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  auto load_row = [&](Block (&v)[kBlocks], int64_t at) {
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) {
+      const int b = lane + j * kLanes;
+      v[j] = kZeroBlock;
+      if (b < blocks) v[j] = load_block(a.x + at * a.x_stride + 16 * b);
+    }
+  };
+  float next_rstd = 0.0f;
+  if (row < a.M) {
+    load_row(next, row);
+    if (kOut == kOutSecond) next_rstd = a.rstd[row];
+  }
 
   float u6 = 0.0f, u4 = 0.0f;
   if constexpr (kNV) {
@@ -104,14 +135,14 @@ void rmsnorm_kernel(NormArgs a, int npartials) {
 
   uint32_t top = 0;
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.M;
-       row += (int64_t)gridDim.x * kRows, ++turn) {
-    Block h[kBlocks];
+  for (bool first = true; row < a.M; row += step, ++turn, first = false) {
+    float rstd = next_rstd;
+    if (kOut != kOutSecond && !first) load_row(next, row);
 #pragma unroll
-    for (int j = 0; j < kBlocks; ++j) {
-      const int b = lane + j * kLanes;
-      h[j] = kZeroBlock;
-      if (b < blocks) h[j] = load_block(a.x + row * a.x_stride + 16 * b);
+    for (int j = 0; j < kBlocks; ++j) h[j] = next[j];
+    if (kOut == kOutSecond && row + step < a.M) {
+      load_row(next, row + step);
+      next_rstd = a.rstd[row + step];
     }
     if constexpr (kRes) {
       Block r[kBlocks];
@@ -131,10 +162,7 @@ void rmsnorm_kernel(NormArgs a, int npartials) {
         h[j] = pack_block(u);
       }
     }
-    float rstd;
-    if constexpr (kOut == kOutSecond) {
-      rstd = a.rstd[row];
-    } else {
+    if constexpr (kOut != kOutSecond) {
       double ss = 0.0;
 #pragma unroll
       for (int j = 0; j < kBlocks; ++j) {
@@ -161,8 +189,8 @@ void rmsnorm_kernel(NormArgs a, int npartials) {
     for (int j = 0; j < kBlocks; ++j) {
       const int b = lane + j * kLanes;
       float u[16], g[16];
-      unpack16(h[j].a, h[j].b, u);
-      unpack16(w[j].a, w[j].b, g);
+      unpack_again(h[j], u);
+      unpack_again(w[j], g);
 #pragma unroll
       for (int i = 0; i < 16; ++i) u[i] = u[i] * rstd * g[i];
       const Block y = pack_block(u);
@@ -230,7 +258,7 @@ hipError_t launch_norm(NormArgs a, hipStream_t s) {
       a.x_stride = a.K;
       a.r = nullptr;
     }
-    launch_norm_kernel<kLanes, kBlocks, kOutSecond>(a, grid, first, s);
+    launch_norm_kernel<kLanes, kBlocks, kOutSecond>(a, first, first, s);
   }
   return hipGetLastError();
 }
@@ -242,15 +270,41 @@ __global__ void zero_kernel(float* p, int64_t n) {
 }
 
 // ------------------------------------------------------------------ backward
-// A workgroup walks its rows and sums dw in registers; partials[workgroup] is its sum.
+// A workgroup walks its rows, with up to two blocks a lane the next one on its way while one
+// is computed, and sums dw in registers; partials[workgroup] is its sum.
 template <int kLanes, int kBlocks, bool kRes>
-__global__ __launch_bounds__(kLanes > 256 ? kLanes : 256)
+__global__ __launch_bounds__(kLanes > 256 ? kLanes : 256, 2)
 void rmsnorm_bwd_kernel(NormBwdArgs a) {
   constexpr int kThreads = kLanes > 256 ? kLanes : 256, kRows = kThreads / kLanes;
   __shared__ float part[2][16];
   __shared__ float sums[kRows > 1 ? kThreads * 16 : 1];
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int blocks = a.K / 16;
+
+  struct Row {
+    Block h[kBlocks], dy[kBlocks], dh[kRes ? kBlocks : 1];
+    float rstd;
+  };
+  auto load_row = [&](Row& r, int64_t row) {
+    r.rstd = row < a.M ? a.rstd[row] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) {
+      const int b = lane + j * kLanes;
+      r.h[j] = r.dy[j] = kZeroBlock;
+      if constexpr (kRes) r.dh[j] = kZeroBlock;
+      if (b < blocks && row < a.M) {
+        r.h[j] = load_block(a.h + row * a.K + 16 * b);
+        r.dy[j] = load_block(a.dy + row * a.K + 16 * b);
+        if constexpr (kRes) r.dh[j] = load_block(a.dh + row * a.K + 16 * b);
+      }
+    }
+  };
+  constexpr bool kAhead = kBlocks <= 2;
+  Row next;
+  // the same number of rounds for all rows of a workgroup (they share barriers)
+  int64_t first = (int64_t)blockIdx.x * kRows;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  load_row(next, first + sub);
 
   Block w[kBlocks];
   float dw[kBlocks][16];
@@ -264,31 +318,20 @@ void rmsnorm_bwd_kernel(NormBwdArgs a) {
   }
   const float inv_k = 1.0f / (float)a.K;
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + sub; row < a.M;
-       row += (int64_t)gridDim.x * kRows, ++turn) {
-    Block h[kBlocks], dy[kBlocks], dh[kBlocks];
-#pragma unroll
-    for (int j = 0; j < kBlocks; ++j) {
-      const int b = lane + j * kLanes;
-      h[j] = dy[j] = dh[j] = kZeroBlock;
-      if (b < blocks) {
-        h[j] = load_block(a.h + row * a.K + 16 * b);
-        dy[j] = load_block(a.dy + row * a.K + 16 * b);
-        if (kRes) dh[j] = load_block(a.dh + row * a.K + 16 * b);
-      }
-    }
-    const float rstd = a.rstd[row];
+  for (; first < a.M; first += step, ++turn) {
+    const int64_t row = first + sub;
+    Row r = next;
+    if (kAhead && first + step < a.M) load_row(next, row + step);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j) {
       float n[16], d[16], g[16];
-      unpack16(h[j].a, h[j].b, n);
-      unpack16(dy[j].a, dy[j].b, d);
-      unpack16(w[j].a, w[j].b, g);
+      unpack_again(r.h[j], n);
+      unpack_again(r.dy[j], d);
+      unpack_again(w[j], g);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        n[i] *= rstd;
-        const float dn = d[i] * n[i];
+        const float dn = d[i] * (n[i] * r.rstd);
         dw[j][i] += dn;
         dot = __builtin_fmaf(dn, g[i], dot);
       }
@@ -298,21 +341,24 @@ void rmsnorm_bwd_kernel(NormBwdArgs a) {
     for (int j = 0; j < kBlocks; ++j) {
       const int b = lane + j * kLanes;
       float n[16], d[16], g[16];
-      unpack16(h[j].a, h[j].b, n);
-      unpack16(dy[j].a, dy[j].b, d);
-      unpack16(w[j].a, w[j].b, g);
+      unpack_again(r.h[j], n);
+      unpack_again(r.dy[j], d);
+      unpack_again(w[j], g);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        n[i] = rstd * __builtin_fmaf(-c, n[i] * rstd, d[i] * g[i]);
+        n[i] = r.rstd * __builtin_fmaf(-c, n[i] * r.rstd, d[i] * g[i]);
       if constexpr (kRes) {
-        unpack16(dh[j].a, dh[j].b, d);
+        unpack_again(r.dh[j], d);
 #pragma unroll
         for (int i = 0; i < 16; ++i) n[i] += d[i];
       }
-      if (b < blocks) store_block(a.dx + row * a.K + 16 * b, pack_block(n));
+      if (b < blocks && row < a.M) store_block(a.dx + row * a.K + 16 * b, pack_block(n));
     }
+    if (!kAhead && first + step < a.M) load_row(next, row + step);
   }
   if (!a.dw) return;
+  // one workgroup alone has dw itself
+  float* out = gridDim.x == 1 ? a.dw : a.partials + (int64_t)blockIdx.x * a.K;
 #pragma unroll
   for (int j = 0; j < kBlocks; ++j) {
     const int b = lane + j * kLanes;
@@ -321,39 +367,39 @@ void rmsnorm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) sums[i * kThreads + threadIdx.x] = dw[j][i];
       __syncthreads();
-      // thread (lane, sub) joins the rows' sums of 16 / kRows of its lane's values; with more
-      // than 16 rows the first 16 of them do
-      constexpr int kEach = kRows < 16 ? 16 / kRows : 1;
+      // thread (lane, sub) joins the rows' sums of 16 / kRows of its lane's values
+      constexpr int kEach = 16 / kRows;
+      float v[kEach];
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const int i = sub * kEach + e;
-        if (i < 16 && b < blocks) {
-          float v = 0.0f;
+        v[e] = 0.0f;
 #pragma unroll
-          for (int q = 0; q < kRows; ++q) v += sums[i * kThreads + q * kLanes + lane];
-          a.partials[(int64_t)blockIdx.x * a.K + 16 * b + i] = v;
-        }
+        for (int q = 0; q < kRows; ++q) v[e] += sums[(sub * kEach + e) * kThreads + q * kLanes + lane];
+      }
+      if (b < blocks) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) out[16 * b + sub * kEach + e] = v[e];
       }
     } else if (b < blocks) {
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4*>(a.partials + (int64_t)blockIdx.x * a.K + 16 * b + i) =
+        *reinterpret_cast<float4*>(out + 16 * b + i) =
             make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
     }
   }
 }
 
-// dw[k] = sum over n partial rows, in their order within 16 groups, then over the groups:
-// 16 lanes to a row's 64 columns.
+// dw[k] = sum over n partial rows, in their order within 32 groups, then over the groups:
+// 8 lanes to a row's 32 columns.
 __global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ p, int n, int K,
                                                          float* __restrict__ dw) {
-  __shared__ float4 part[16][16];
-  const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int k = (int)blockIdx.x * 64 + 4 * c;
+  __shared__ float4 part[32][8];
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int k = (int)blockIdx.x * 32 + 4 * c;
   float4 v = make_float4(0, 0, 0, 0);
   if (k < K) {
 #pragma unroll 8
-    for (int i = g; i < n; i += 16) {
+    for (int i = g; i < n; i += 32) {
       const float4 q = *reinterpret_cast<const float4*>(p + (int64_t)i * K + k);
       v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
     }
@@ -361,7 +407,7 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict
   part[g][c] = v;
   __syncthreads();
   if (g == 0 && k < K) {
-    for (int i = 1; i < 16; ++i) {
+    for (int i = 1; i < 32; ++i) {
       const float4 q = part[i][c];
       v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
     }
@@ -375,27 +421,23 @@ hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t s) {
   const int grid = norm_bwd_partials(a.M, a.K);
   if (a.dh) rmsnorm_bwd_kernel<kLanes, kBlocks, true><<<grid, kThreads, 0, s>>>(a);
   else rmsnorm_bwd_kernel<kLanes, kBlocks, false><<<grid, kThreads, 0, s>>>(a);
-  if (a.dw) column_sum_kernel<<<(a.K + 63) / 64, 256, 0, s>>>(a.partials, grid, a.K, a.dw);
+  if (a.dw && grid > 1) column_sum_kernel<<<(a.K + 31) / 32, 256, 0, s>>>(a.partials, grid, a.K, a.dw);
   return hipGetLastError();
 }
 
-// Lanes of a row: a wave where its four blocks a lane hold the row, else more waves.
+// Lanes of a row: a wave where its four blocks a lane hold the row, else more waves; few rows
+// get more lanes.
 int lanes_of(int64_t M, int K) {
   if (K <= 512) return 16;
-  if (K > 16384) return 1024;
+  if (K > 16384) return 512;
   return K > 4096 || M < 1024 ? 256 : 64;
 }
-
-// Calls f<kLanes, kBlocks>(a, s) for the row length.
-#define FOS_NORM_DISPATCH(F)                                                   \
-  const int lanes = lanes_of(a.M, a.K);                                        \
-  const int per = (a.K / 16 + lanes - 1) / lanes;                              \
-  if (lanes == 16) return per <= 1 ? F<16, 1>(a, s) : F<16, 2>(a, s);          \
-  if (lanes == 64) return per <= 2 ? F<64, 2>(a, s) : F<64, 4>(a, s);          \
-  if (lanes == 256)                                                            \
-    return per <= 1 ? F<256, 1>(a, s) : per <= 2 ? F<256, 2>(a, s)             \
-         : per <= 3 ? F<256, 3>(a, s) : F<256, 4>(a, s);                       \
-  return per <= 2 ? F<1024, 2>(a, s) : F<1024, 4>(a, s);
+// Two blocks a lane where it can be.
+int bwd_lanes_of(int64_t M, int K) {
+  if (K <= 512) return 16;
+  if (M < 1024 && K <= 8192) return 256;
+  return K <= 2048 ? 64 : K <= 4096 ? 128 : K <= 8192 ? 256 : 512;
+}
 
 }  // namespace
 
@@ -405,13 +447,24 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s) {
     zero_kernel<<<1, 64, 0, s>>>(a.t, 1);
     return hipGetLastError();
   }
-  FOS_NORM_DISPATCH(launch_norm)
+  const int lanes = lanes_of(a.M, a.K), per = (a.K / 16 + lanes - 1) / lanes;
+  switch (lanes) {
+    case 16: return per <= 1 ? launch_norm<16, 1>(a, s) : launch_norm<16, 2>(a, s);
+    case 64: return per <= 2 ? launch_norm<64, 2>(a, s) : launch_norm<64, 4>(a, s);
+    case 256:
+      return per <= 1 ? launch_norm<256, 1>(a, s) : per <= 2 ? launch_norm<256, 2>(a, s)
+           : per <= 3 ? launch_norm<256, 3>(a, s) : launch_norm<256, 4>(a, s);
+    default: return launch_norm<512, 4>(a, s);
+  }
 }
 
+// Workgroups of the backward pass, each with a partial dw: what runs at once (two waves to a
+// SIMD), but at least four rounds of rows to each, down to one workgroup to a CU.
 int norm_bwd_partials(int64_t M, int K) {
-  const int lanes = lanes_of(M, K), rows = lanes > 256 ? 1 : 256 / lanes;
-  const int64_t groups = (M + rows - 1) / rows;
-  return (int)(groups < 512 ? groups : 512);
+  const int lanes = bwd_lanes_of(M, K), rows = lanes > 256 ? 1 : 256 / lanes;
+  const int64_t groups = (M + rows - 1) / rows, most = lanes > 256 ? 256 : 512;
+  const int64_t want = groups / 4 < 256 ? 256 : groups / 4 < most ? groups / 4 : most;
+  return (int)(groups < want ? groups : want);
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t s) {
@@ -420,7 +473,14 @@ hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t s) {
     zero_kernel<<<(a.K + 255) / 256, 256, 0, s>>>(a.dw, a.K);
     return hipGetLastError();
   }
-  FOS_NORM_DISPATCH(launch_bwd)
+  const int lanes = bwd_lanes_of(a.M, a.K), per = (a.K / 16 + lanes - 1) / lanes;
+  switch (lanes) {
+    case 16: return per <= 1 ? launch_bwd<16, 1>(a, s) : launch_bwd<16, 2>(a, s);
+    case 64: return launch_bwd<64, 2>(a, s);
+    case 128: return launch_bwd<128, 2>(a, s);
+    case 256: return per <= 1 ? launch_bwd<256, 1>(a, s) : launch_bwd<256, 2>(a, s);
+    default: return per <= 2 ? launch_bwd<512, 2>(a, s) : launch_bwd<512, 4>(a, s);
+  }
 }
 
 }  // namespace fos

@@ -69,24 +69,78 @@ __device__ __forceinline__ int64_t weight_row(const WLinearArgs& a, int64_t l0, 
   return min(l0 / 2 + (up ? l - rows / 2 : l), half - 1) + (up ? half : 0);
 }
 
-// Stores y[m][n] of an epilogue from the sum of weight row n (with a gate: and of row
-// n + N / 2), the tensor scale applied.
-__device__ __forceinline__ void finish(const WLinearArgs& a, int64_t m, int64_t n, float z, float up) {
-  const int64_t cols = a.gated ? a.N / 2 : a.N;
+// What an epilogue adds to the sums of kCols columns from n of row m, read while the sums are
+// on their way.  With `quad`, four columns are accessed at once.
+template <int kCols>
+struct Addends {
+  float bias[kCols], bias_up[kCols], residual[kCols];
+};
+template <int kCols>
+__device__ __forceinline__ void load_columns(float (&v)[kCols], const uint16_t* p, int left, bool quad) {
+  if (kCols == 4 && quad) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+    v[0] = bf16_lo(w.x); v[1 % kCols] = bf16_hi(w.x);
+    v[2 % kCols] = bf16_lo(w.y); v[3 % kCols] = bf16_hi(w.y);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) v[k] = k < left ? bf16_lo(p[k]) : 0.0f;
+}
+template <int kCols>
+__device__ __forceinline__ Addends<kCols> load_addends(const WLinearArgs& a, int64_t m, int64_t n, int left) {
+  Addends<kCols> d = {};
   if (a.bias) {
-    z += bf16_lo(a.bias[n]);
-    if (a.gated) up += bf16_lo(a.bias[cols + n]);
+    load_columns(d.bias, a.bias + n, left, a.e.quad);
+    if (a.gated) load_columns(d.bias_up, a.bias + a.N / 2 + n, left, a.e.quad);
+  }
+  if (a.e.residual) load_columns(d.residual, a.e.residual + m * a.e.residual_stride + n, left, a.e.quad);
+  return d;
+}
+template <int kCols>
+__device__ __forceinline__ void store_columns(uint16_t* p, const float (&v)[kCols], int left, bool quad) {
+  if (kCols == 4 && quad) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1 % kCols]), pack_bf16x2(v[2 % kCols], v[3 % kCols])};
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kCols; ++k)
+    if (k < left) p[k] = (uint16_t)pack_bf16x2(v[k], v[k]);
+}
+
+// Stores y[m][n ..] of an epilogue from the sums z of weight rows n .. (with a gate: and `up`
+// of rows n + N / 2 ..), the tensor scale applied; `left` columns remain.
+template <int kCols>
+__device__ __forceinline__ void finish(const WLinearArgs& a, int64_t m, int64_t n, int left,
+                                       float (&z)[kCols], float (&up)[kCols], const Addends<kCols>& d) {
+  const int64_t cols = a.gated ? a.N / 2 : a.N;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    z[k] += d.bias[k];
+    up[k] += d.bias_up[k];
   }
   if (a.e.preact) {
-    a.e.preact[m * a.N + n] = (uint16_t)pack_bf16x2(z, z);
-    if (a.gated) a.e.preact[m * a.N + cols + n] = (uint16_t)pack_bf16x2(up, up);
+    store_columns(a.e.preact + m * a.N + n, z, left, a.e.quad);
+    if (a.gated) store_columns(a.e.preact + m * a.N + cols + n, up, left, a.e.quad);
   }
-  float y = activate(a.e.act, z);
-  if (a.gated) y *= up;
-  if (a.e.residual) y += bf16_lo(a.e.residual[m * a.e.residual_stride + n]);
-  const int64_t at = m * cols + n;
-  if (a.f32_out) static_cast<float*>(a.y)[at] = y;
-  else static_cast<uint16_t*>(a.y)[at] = (uint16_t)pack_bf16x2(y, y);
+  float y[kCols];
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    y[k] = activate(a.e.act, z[k]);
+    if (a.gated) y[k] *= up[k];
+    y[k] += d.residual[k];
+  }
+  if (!a.f32_out) {
+    store_columns(static_cast<uint16_t*>(a.y) + m * cols + n, y, left, a.e.quad);
+    return;
+  }
+  float* p = static_cast<float*>(a.y) + m * cols + n;
+  if (kCols == 4 && a.e.quad) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{y[0], y[1 % kCols], y[2 % kCols], y[3 % kCols]};
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kCols; ++k)
+    if (k < left) p[k] = y[k];
 }
 
 // ---- more activation rows: 16x16x32 tiles -------------------------------------------
@@ -233,28 +287,34 @@ __global__ __launch_bounds__(64 * KW, 2) void wlinear_tile_kernel(WLinearArgs a)
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int m = 0; m < MT; ++m) sums[n * MT + m][lane] = acc[n][m];
-  __syncthreads();
   if constexpr (kEpi) {
-    auto joined = [&](int l, int m, int c) {       // rows l .. l + 3, activation row 16 m + c
-      const int tile = (l >> 4) * MT + m, ln = ((l & 15) << 2) | c;
+    const int rows = a.gated ? kTileN / 2 : kTileN;
+    const int64_t c0 = a.gated ? n0 / 2 : n0, cols = a.gated ? a.N / 2 : a.N;
+    auto joined = [&](float (&z)[4], int l, int m) {   // weight rows l .. l + 3, activation row m
+      const int tile = (l >> 4) * MT + (m >> 4), ln = ((l & 15) << 2) | (m & 15);
       f32x4 v = reinterpret_cast<f32x4(*)[64]>(mem[0])[tile][ln];
 #pragma unroll
       for (int w = 1; w < KW; ++w) v += reinterpret_cast<f32x4(*)[64]>(mem[w])[tile][ln];
-      return v * t;
-    };
-    const int rows = a.gated ? kTileN / 2 : kTileN;
-    const int64_t c0 = a.gated ? n0 / 2 : n0, cols = a.gated ? a.N / 2 : a.N;
-    for (int i = threadIdx.x; i < rows / 4 * kTileM; i += 64 * KW) {
-      const int l = 4 * (i / kTileM), mi = i % kTileM;
-      if (m0 + mi >= a.M) continue;
-      const f32x4 z = joined(l, mi >> 4, mi & 15);
-      const f32x4 up = a.gated ? joined(l + rows, mi >> 4, mi & 15) : f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (c0 + l + k < cols) finish(a, m0 + mi, c0 + l + k, z[k], up[k]);
+      for (int k = 0; k < 4; ++k) z[k] = v[k] * t;
+    };
+    bool first = true;
+    for (int i = threadIdx.x; first || i < rows / 4 * kTileM; i += 64 * KW, first = false) {
+      const int l = 4 * (i / kTileM), m = i % kTileM;
+      const int left = (int)min((int64_t)4, cols - c0 - l);
+      const bool in = i < rows / 4 * kTileM && m0 + m < a.M && left > 0;
+      Addends<4> d = {};
+      if (in) d = load_addends<4>(a, m0 + m, c0 + l, left);
+      if (first) __syncthreads();                      // every wave's sums are there
+      if (!in) continue;
+      float z[4], up[4] = {};
+      joined(z, l, m);
+      if (a.gated) joined(up, l + rows, m);
+      finish<4>(a, m0 + m, c0 + l, left, z, up, d);
     }
     return;
   }
+  __syncthreads();
   for (int i = threadIdx.x; i < NT * MT * 64; i += 64 * KW) {
     const int tile = i >> 6, ln = i & 63;
     f32x4 v = reinterpret_cast<f32x4(*)[64]>(mem[0])[tile][ln];
@@ -412,23 +472,27 @@ __global__ __launch_bounds__(64 * KW, R == 2 && !kMany ? 4 : 3) void wlinear_qua
       const float v = sum_over_quads(acc[j][c]);
       if (g == 0) sums[wave][4 * j + i][c] = v;
     }
-  __syncthreads();
   if constexpr (kEpi) {
+    const int rows = a.gated ? kRows / 2 : kRows;
+    const int64_t c0 = a.gated ? n0 / 2 : n0, cols = a.gated ? a.N / 2 : a.N;
     auto joined = [&](int n, int m) {
       float v = sums[0][n][m];
 #pragma unroll
       for (int w = 1; w < KW; ++w) v += sums[w][n][m];
       return v * t;
     };
-    const int rows = a.gated ? kRows / 2 : kRows;
-    const int64_t c0 = a.gated ? n0 / 2 : n0, cols = a.gated ? a.N / 2 : a.N;
-    for (int e = threadIdx.x; e < rows * M; e += 64 * KW) {
-      const int n = e % rows, m = e / rows;
-      if (c0 + n < cols)
-        finish(a, m0 + m, c0 + n, joined(n, m), a.gated ? joined(n + rows, m) : 0.0f);
-    }
+    static_assert(4 * kRows <= 64 * KW, "a thread to each value");
+    const int e = threadIdx.x, n = e % rows, m = e / rows;
+    const bool in = m < M && c0 + n < cols;
+    Addends<1> d = {};
+    if (in) d = load_addends<1>(a, m0 + m, c0 + n, 1);
+    __syncthreads();                                   // every wave's sums are there
+    if (!in) return;
+    float z[1] = {joined(n, m)}, up[1] = {a.gated ? joined(n + rows, m) : 0.0f};
+    finish<1>(a, m0 + m, c0 + n, 1, z, up, d);
     return;
   }
+  __syncthreads();
   for (int e = threadIdx.x; e < kRows * M; e += 64 * KW) {
     const int n = e % kRows, m = e / kRows;
     if (n0 + n >= a.N) continue;

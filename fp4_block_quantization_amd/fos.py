@@ -875,6 +875,7 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
 
 _ACTIVATIONS = {"none": FOS_ACT_NONE, "relu": FOS_ACT_RELU, "gelu": FOS_ACT_GELU,
                 "gelu_tanh": FOS_ACT_GELU_TANH, "silu": FOS_ACT_SILU}
+_SCALE_WORKSPACE = int(_lib.fos_quantize_workspace_bytes())
 _RECORDS = {"bf16": FOS_RECORD_NONE, "nvfp4": FOS_RECORD_NVFP4, "mxfp4": FOS_RECORD_MXFP4}
 
 
@@ -935,17 +936,18 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     its column-wise record needs for the weight's gradient).  ``tensor_scale``: fp32 [1], the
     NVFP4 scale to use (delayed scaling; one pass over x); by default that of y is computed.
     ``h``: optional destination of the sum, for instance ``residual`` itself; only with a
-    residual.  K a multiple of 16 (MXFP4: 32), at most 65536."""
-    if x.dim() != 2 or x.get_device() < 0:
+    residual.  K a multiple of 16 (MXFP4: 32), at most 32768."""
+    strides, dev = x.stride(), x.get_device()
+    if len(strides) != 2 or strides[1] != 1 or x.dtype != _BF16 or dev < 0:
         raise ValueError("x must be a 2-D bfloat16 CUDA tensor with contiguous rows")
     M, K = x.shape
-    dev = x.get_device()
-    stride = _rows_of(x, M, K, dev, "x")
-    _whole(weight, (K,), _BF16, dev, "weight")
-    code = _RECORDS.get(format)
+    if (weight.shape != (K,) or weight.dtype != _BF16 or weight.get_device() != dev
+            or not weight.is_contiguous()):
+        raise ValueError("weight must be a contiguous bf16 [K] tensor on x's device")
+    code, rule_code = _RECORDS.get(format), _KV_RULES.get(rule)
     if code is None:
         raise ValueError("format must be 'bf16', 'nvfp4' or 'mxfp4'")
-    if rule not in _KV_RULES:
+    if rule_code is None:
         raise ValueError("rule must be '4/6' or '6'")
     if tensor_scale is not None:
         if format != "nvfp4":
@@ -959,23 +961,28 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     elif h is not None:
         raise ValueError("h is a destination for the sum with a residual")
     rstd = x.new_empty(M, dtype=_F32)
-    y = x.new_empty(M, K) if format == "bf16" or return_y else None
+    y = x.new_empty(M, K) if code == FOS_RECORD_NONE or return_y else None
     data = scales = t = ws = record = None
     if code != FOS_RECORD_NONE:
         data = x.new_empty(M, K // 2, dtype=_U8)
-        scales = x.new_empty(M, K // (16 if format == "nvfp4" else 32), dtype=_U8)
-        if format == "nvfp4":
+        scales = x.new_empty(M, K // (16 if code == FOS_RECORD_NVFP4 else 32), dtype=_U8)
+        if code == FOS_RECORD_NVFP4:
             t = tensor_scale
             if t is None:
                 t = x.new_empty(1, dtype=_F32)
-                ws = x.new_empty(int(_lib.fos_quantize_workspace_bytes()), dtype=_U8)
+                ws = x.new_empty(_SCALE_WORKSPACE, dtype=_U8)
             record = NVFP4Tensor(data, scales, t)
         else:
             record = MXFP4Tensor(data, scales)
-    _call(dev, "fos_rmsnorm_fwd", x.data_ptr(), stride, _address(residual), r_stride,
-          weight.data_ptr(), M, K, eps, _address(h), rstd.data_ptr(), _address(y), code,
-          _KV_RULES[rule], _address(data), _address(scales), _address(t),
-          int(tensor_scale is not None), _address(ws), 0 if ws is None else ws.numel())
+    call = _lib.fos_rmsnorm_fwd
+    if dev != _current_device():
+        call = _on(dev, call)
+    _check(call(x.data_ptr(), strides[0] if M > 1 else K,
+                None if residual is None else residual.data_ptr(), r_stride, weight.data_ptr(), M, K,
+                eps, None if h is None else h.data_ptr(), rstd.data_ptr(),
+                None if y is None else y.data_ptr(), code, rule_code, _address(data),
+                _address(scales), _address(t), 0 if tensor_scale is None else 1, _address(ws),
+                0 if ws is None else _SCALE_WORKSPACE, _raw_stream(dev)), "fos_rmsnorm_fwd")
     return RMSNormOutput(x if h is None else h, rstd, y, record)
 
 
@@ -1199,11 +1206,16 @@ def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, roundi
                  need_dx, need_dw):
     if not (need_dx or need_dw):
         raise ValueError("nothing to compute")
-    dz, dbias, t = _epilogue_bwd(dy, preact, activation, gated, return_dbias, True)
     outputs = (("row",) if need_dx else ()) + (("col",) if need_dw else ())
-    with torch.cuda.device(dz.device):
-        q = quantize(dz, rounding=rounding, outputs=outputs, sr_seed=sr_seed, tensor_scale=t)
-    rows, cols = q if need_dx and need_dw else (q, None) if need_dx else (None, q)
+    cfg = make_config(rounding=rounding, outputs=outputs, sr_seed=sr_seed)
+    dz, dbias, t = _epilogue_bwd(dy, preact, activation, gated, return_dbias, True)
+    (M, W), dev = dz.shape, dz.get_device()
+    record = lambda r, c: NVFP4Tensor(dz.new_empty(r, c // 2, dtype=_U8), dz.new_empty(r, c // 16, dtype=_U8), t)
+    rows = record(M, W) if need_dx else None
+    cols = record(W, M) if need_dw else None
+    _call(dev, "fos_quantize_scaled", ctypes.byref(cfg), dz.data_ptr(), M, W, t.data_ptr(),
+          *((rows.data.data_ptr(), rows.scales.data_ptr()) if need_dx else (None, None)),
+          *((cols.data.data_ptr(), cols.scales.data_ptr()) if need_dw else (None, None)))
     # the products of fos_qlinear_bwd, on the tiles that suit their shapes (dX of 2048 x 4096
     # with an inner dimension of 8192 has 128 tiles of 256 x 256, half a GPU)
     product = lambda a, b: _qlinear_epilogue(a, b, False, None, "none", None, _BF16, False, None)

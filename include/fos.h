@@ -555,7 +555,7 @@ enum { FOS_RECORD_NONE = 0, FOS_RECORD_NVFP4 = 1, FOS_RECORD_MXFP4 = 2 };
  *   tensor scale is computed, nor h there with a residual.  h may be the memory of x or of
  *   the residual, if that is contiguous.  data [rows][cols/2] 8-byte aligned, scales
  *   [rows][cols/16] (MXFP4: [rows][cols/32]), tensor_scale 4-byte aligned.
- *   rows >= 0, below 2^31; cols a multiple of 16 (MXFP4: of 32) from 16 to 65536; eps
+ *   rows >= 0, below 2^31; cols a multiple of 16 (MXFP4: of 32) from 16 to 32768; eps
  *   finite, at least 1e-38.  No rows: a computed tensor scale is 0, nothing else is written.
  *   workspace: for a computed tensor scale only, as for fos_quantize.
  * Errors: FOS_E_NULL, FOS_E_SHAPE, FOS_E_ALIGN, FOS_E_FLAGS, FOS_E_WORKSPACE, FOS_E_HIP. */
@@ -594,7 +594,8 @@ fos_status fos_rmsnorm_bwd(const void* dy_bf16, const void* h_bf16, const void* 
  * needs.  Pointers may be NULL: without a bias, a residual, a kept Z.  residual: bf16, row
  * stride in elements, at least N (not with a gate); y may be its memory, if that is
  * contiguous and the output bf16.  All 2-byte aligned, y to its type; with N (and the
- * residual's stride) even and 4-byte aligned addresses, two values are accessed at a time. */
+ * residual's stride) even and 4-byte aligned addresses, two values are accessed at a time, in
+ * the products of few rows four with multiples of 4 and 8-byte aligned ones (y: 4 values). */
 typedef struct {
   uint32_t struct_size;       /* must equal sizeof(fos_epilogue)                      */
   uint32_t activation;        /* FOS_ACT_*                                            */

@@ -61,7 +61,7 @@ def bits(t):
 # ------------------------------------------------------------------------------- norm
 
 NORM_SHAPES = [(1, 16), (3, 32), (5, 48), (1, 4096), (17, 512), (40, 528), (64, 1040), (1030, 1024),
-               (1100, 2080), (1025, 4096), (9, 4112), (7, 8192), (3, 16384), (2, 16400), (2, 65536),
+               (1100, 2080), (1025, 4096), (9, 4112), (7, 8192), (3, 16384), (2, 16400), (2, 32768), (1027, 2064),
                (2500, 96), (9000, 64)]
 
 
