@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libfos.so")
 
 SOURCES = ["amax.hip", "quantize.hip", "dequantize.hip", "qlinear.hip", "mxfp4.hip", "selftest.hip",
            "wlinear.hip", "kvcache.hip", "paged_decode.hip", "rmsnorm.hip", "epilogue_bwd.hip",
-           "api.cpp", "api_serving.cpp", "api_feedforward.cpp"]
+           "mx_epilogue.hip", "api.cpp", "api_serving.cpp", "api_feedforward.cpp"]
 # measured HBM ceilings for the benchmark (include/fos_ceiling.h), a library of its own
 CEILING_SOURCES = ["ceiling.hip"]
 CEILING_LIB = os.path.join(PKG, "libfos_ceiling.so")

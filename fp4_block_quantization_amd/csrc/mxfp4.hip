@@ -16,14 +16,9 @@
 //                       (v_mfma_scale_f32_32x32x64_f8f6f4, both operands E2M1): the
 //                       packed bytes and E8M0 scales go to the MFMA as they are, with
 //                       no conversion; 256x256 tiles, K staged through LDS in 256-wide
-//                       double-buffered stages as in the NVFP4 qlinear kernel; ends in a
-//                       plain store or an epilogue, with a gate's rows as there.
-//   mx_flow_kernel      the same product with an epilogue on smaller tiles, two workgroups to
-//                       a CU: stages of 128, prefetched further and without a pause.
+//                       double-buffered stages as in the NVFP4 qlinear kernel.
 #include "device_common.hpp"
-#include "feedforward.hpp"
 #include "gemm_common.hpp"
-#include "gemm_epilogue.hpp"
 #include "kernels.hpp"
 
 namespace fos {
@@ -167,7 +162,6 @@ struct MxOperands {
   __amdgpu_buffer_rsrc_t a, sa, b, sb;
   uint32_t oa[2], ob[2];      // per-lane data offsets for even / odd row-groups
   uint32_t osa, osb;          // per-lane scale offsets
-  uint32_t ou[2], osu;        // with a gate: of the other projection's rows
   uint32_t group_stride;      // bytes between data row-groups (8 rows)
   uint32_t scale_stride;      // bytes between scale row-groups (32 rows)
 };
@@ -175,7 +169,6 @@ struct MxOperands {
 // This wave's share of one stage: 64 rows of each operand, 8 + 8 data copies (8 rows
 // of 128 bytes each) and 2 + 2 scale copies (32 rows of 8 bytes each), issued as two
 // halves of 10 copies (half j: data row-groups 4j..4j+3 and scale row-group j).
-template <bool kGate>
 __device__ __forceinline__ void mx_stage_load_half(MxStage& st, const MxOperands& p, int sc,
                                                    int wave, int j) {
   const int od = sc * kMxRowBytes, os = sc * kMxRowScales;
@@ -183,22 +176,15 @@ __device__ __forceinline__ void mx_stage_load_half(MxStage& st, const MxOperands
   for (int q = 4 * j; q < 4 * j + 4; ++q) {
     const int so = od + q * (int)p.group_stride;
     dma16(p.a, st.a + (64 * wave + 8 * q) * kMxRowBytes, p.oa[q & 1], so);
-    // with a gate, row-groups 4 to 7 are the other projection's
-    if (kGate && j)
-      dma16(p.b, st.b + (64 * wave + 8 * q) * kMxRowBytes, p.ou[q & 1],
-            od + (q - 4) * (int)p.group_stride);
-    else
-      dma16(p.b, st.b + (64 * wave + 8 * q) * kMxRowBytes, p.ob[q & 1], so);
+    dma16(p.b, st.b + (64 * wave + 8 * q) * kMxRowBytes, p.ob[q & 1], so);
   }
   const int so = os + j * (int)p.scale_stride;
   dma4(p.sa, st.sa + (64 * wave + 32 * j) * kMxRowScales, p.osa, so);
-  if (kGate && j) dma4(p.sb, st.sb + (64 * wave + 32 * j) * kMxRowScales, p.osu, os);
-  else dma4(p.sb, st.sb + (64 * wave + 32 * j) * kMxRowScales, p.osb, so);
+  dma4(p.sb, st.sb + (64 * wave + 32 * j) * kMxRowScales, p.osb, so);
 }
-template <bool kGate>
 __device__ __forceinline__ void mx_stage_load(MxStage& st, const MxOperands& p, int sc, int wave) {
-  mx_stage_load_half<kGate>(st, p, sc, wave, 0);
-  mx_stage_load_half<kGate>(st, p, sc, wave, 1);
+  mx_stage_load_half(st, p, sc, wave, 0);
+  mx_stage_load_half(st, p, sc, wave, 1);
 }
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -221,7 +207,7 @@ __device__ __forceinline__ i32x8 mx_operand(const uint8_t* base, int row, int g)
 // stream for hundreds of cycles while the matrix pipe idles; left to itself the
 // scheduler also reads each operand right before its first use and waits for it.)
 constexpr int NKS = kMxSuper / 64;
-template <bool kLoad, bool kGate>
+template <bool kLoad>
 __device__ __forceinline__ void mx_stage_mma(const MxStage& st, f32x16 (&acc)[4][4], int ra,
                                              int rb, int h, MxStage& next, const MxOperands& p,
                                              int next_sc, int wave) {
@@ -254,7 +240,7 @@ __device__ __forceinline__ void mx_stage_mma(const MxStage& st, f32x16 (&acc)[4]
       }
     }
     const bool copies = kLoad && s < 2;
-    if (copies) mx_stage_load_half<kGate>(next, p, next_sc, wave, s);
+    if (copies) mx_stage_load_half(next, p, next_sc, wave, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -296,13 +282,10 @@ __device__ __forceinline__ void mx_stage_mma(const MxStage& st, f32x16 (&acc)[4]
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int kEpi>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
 void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ as,
                     const uint8_t* __restrict__ bd, const uint8_t* __restrict__ bs, int M, int N,
-                    int K, int tiles_m, int tiles_n, void* __restrict__ y, EpilogueArgs e) {
-  constexpr bool kGate = kEpi == kGated;
-  constexpr int kProj = kGate ? 2 : 1;   // weight rows of one column of Y
+                    int K, int tiles_m, int tiles_n, uint16_t* __restrict__ y) {
   __shared__ __attribute__((aligned(16))) MxStage st0;
   __shared__ __attribute__((aligned(16))) MxStage st1;
   const TileCoord tc = tile_of(blockIdx.x, tiles_m, tiles_n);
@@ -316,8 +299,8 @@ void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
   MxOperands p;
   p.a = __builtin_amdgcn_make_buffer_rsrc((void*)ad, 0, (int)((uint32_t)M * kb2), kRsrcWord3);
   p.sa = __builtin_amdgcn_make_buffer_rsrc((void*)as, 0, (int)((uint32_t)M * kb32), kRsrcWord3);
-  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)bd, 0, (int)((uint32_t)(kProj * N) * kb2), kRsrcWord3);
-  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)bs, 0, (int)((uint32_t)(kProj * N) * kb32), kRsrcWord3);
+  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)bd, 0, (int)((uint32_t)N * kb2), kRsrcWord3);
+  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)bs, 0, (int)((uint32_t)N * kb32), kRsrcWord3);
   {
     // data: DMA lane l of row-group q writes LDS slot (l & 7) of local row 64*wave +
     // 8*q + (l >> 3) and fetches the granule the swizzle puts there
@@ -327,17 +310,13 @@ void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
     for (int par = 0; par < 2; ++par) {
       const uint32_t g = slot ^ (((sub >> 1) + 4 * par) & 7);
       p.oa[par] = (uint32_t)(tm * kMxTile + r0) * kb2 + 16 * g;
-      // with a gate the wave's 64 rows are 32 of the gate and 32 of the other projection
-      p.ob[par] = (uint32_t)(kGate ? tn * (kMxTile / 2) + 32 * wave + sub : tn * kMxTile + r0) * kb2 + 16 * g;
-      p.ou[par] = p.ob[par] + (uint32_t)N * kb2;
+      p.ob[par] = (uint32_t)(tn * kMxTile + r0) * kb2 + 16 * g;
     }
     p.group_stride = 8 * kb2;
     // scales: lane l of copy j fetches dword l & 1 of local row 64*wave + 32*j + l/2
     const int srow = 64 * wave + (lane >> 1);
     p.osa = (uint32_t)(tm * kMxTile + srow) * kb32 + 4 * (lane & 1);
-    p.osb = (uint32_t)(kGate ? tn * (kMxTile / 2) + 32 * wave + (lane >> 1) : tn * kMxTile + srow) * kb32 +
-            4 * (lane & 1);
-    p.osu = p.osb + (uint32_t)N * kb32;
+    p.osb = (uint32_t)(tn * kMxTile + srow) * kb32 + 4 * (lane & 1);
     p.scale_stride = 32 * kb32;
   }
 
@@ -350,325 +329,22 @@ void mx_gemm_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
   const int ra = (wave >> 1) * 128 + lr;
   const int rb = (wave & 1) * 128 + lr;
   const int nsc = K / kMxSuper;
-  mx_stage_load<kGate>(st0, p, 0, wave);
+  mx_stage_load(st0, p, 0, wave);
   int sc = 0;
   for (; sc + 1 < nsc; sc += 2) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    mx_stage_mma<true, kGate>(st0, acc, ra, rb, h, st1, p, sc + 1, wave);
+    mx_stage_mma<true>(st0, acc, ra, rb, h, st1, p, sc + 1, wave);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     // unconditional (a redundant copy of the last stage when none is left): a branch
     // here lets the compiler sink the previous stage's MFMAs past the barrier
-    mx_stage_mma<true, kGate>(st1, acc, ra, rb, h, st0, p, min(sc + 2, nsc - 1), wave);
+    mx_stage_mma<true>(st1, acc, ra, rb, h, st0, p, min(sc + 2, nsc - 1), wave);
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (sc < nsc) mx_stage_mma<false, kGate>(st0, acc, ra, rb, h, st1, p, 0, wave);
-  if constexpr (kEpi == kPlain) {
-    store_tile(static_cast<uint16_t*>(y), M, N, tm, tn, wave, lr, h, 1.0f, acc);
-  } else {
-    store_fused<4, 4, kGate>(e, y, M, N, tm * kMxTile + (wave >> 1) * 128,
-                             (tn * kMxTile + (wave & 1) * 128) / kProj, lane, 1.0f, acc);
-  }
-}
-
-// ---------------------------------------------------------------- GEMM, stages of 128
-// Y = deq(A) deq(B)^T for a (64 TI) x (64 TJ) tile, TI x TJ MFMA tiles to a wave.  K in stages
-// of 128 (64 bytes of nibbles a row), four in LDS; the E8M0 bytes of four stages (16 a row)
-// are copied at once, apart, and go to registers: a row's scale bytes of one stage are a
-// request of their own to the address unit, as dear as 64 bytes of nibbles.
-//
-// A stage is two k-steps of 64.  While one multiplies, the operands of the next are read from
-// LDS; between the two stands the stage's one barrier, where every wave has read all of this
-// stage (the fourth stage after it is copied to its place at once) and the next one has
-// landed (it had three stages' time).
-constexpr int kStageK = 128;
-constexpr int kStageRowBytes = kStageK / 2;
-constexpr int kScaleStages = 4;                                    // stages of one scale copy
-constexpr int kScaleRowBytes = kScaleStages * kStageK / 32;        // 16
-
-template <int TI, int TJ>
-struct FlowStage {
-  uint8_t a[64 * TI * kStageRowBytes];
-  uint8_t b[64 * TJ * kStageRowBytes];
-};
-template <int TI, int TJ>
-struct FlowScales {
-  uint8_t a[64 * TI * kScaleRowBytes];
-  uint8_t b[64 * TJ * kScaleRowBytes];
-};
-
-struct FlowOperands {
-  __amdgpu_buffer_rsrc_t a, sa, b, sb;
-  uint32_t oa, ob, osa, osb;  // per-lane offsets
-  uint32_t group_stride;      // bytes between row-groups (16 rows)
-};
-
-// Copies of one wave, the same number for each: a quarter of a stage's rows (32 weight rows:
-// of one projection), 16 rows to an instruction, and 64 rows' scales of each operand (where
-// there are fewer of them than waves, two copy the same).
-template <int TI, int TJ>
-__device__ __forceinline__ void flow_load(FlowStage<TI, TJ>& st, const FlowOperands& p, int s, int wave) {
-  const int od = s * kStageRowBytes;
-#pragma unroll
-  for (int q = 0; q < TI; ++q)
-    dma16(p.a, st.a + (16 * TI * wave + 16 * q) * kStageRowBytes, p.oa, od + q * (int)p.group_stride);
-#pragma unroll
-  for (int q = 0; q < TJ; ++q)
-    dma16(p.b, st.b + (16 * TJ * wave + 16 * q) * kStageRowBytes, p.ob, od + q * (int)p.group_stride);
-}
-template <int TI, int TJ>
-__device__ __forceinline__ void flow_load_scales(FlowScales<TI, TJ>& sc, const FlowOperands& p, int c,
-                                                 int wave) {
-  dma16(p.sa, sc.a + 64 * (wave % TI) * kScaleRowBytes, p.osa, c * kScaleRowBytes);
-  dma16(p.sb, sc.b + 64 * (wave % TJ) * kScaleRowBytes, p.osb, c * kScaleRowBytes);
-}
-
-// Granule g (16 bytes, 32 values) of a row of a stage lies at g ^ ((row >> 2) & 3): 16 rows of
-// an operand are read from different banks.
-template <int T>
-__device__ __forceinline__ void flow_operands(const uint8_t* base, int row, int g, i32x8 (&o)[T]) {
-#pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(base + (row + 32 * i) * kStageRowBytes +
-                                                    ((g ^ ((row >> 2) & 3)) << 4));
-    o[i] = i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-  }
-}
-template <int T>
-__device__ __forceinline__ void flow_scales(const uint8_t* base, int row, uint4 (&s)[T]) {
-#pragma unroll
-  for (int i = 0; i < T; ++i)
-    s[i] = *reinterpret_cast<const uint4*>(base + (row + 32 * i) * kScaleRowBytes);
-}
-__device__ __forceinline__ uint32_t scale_word(const uint4& v, int j) {
-  return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
-}
-
-// Byte kByte of the scale words.
-template <int kByte, int TI, int TJ>
-__device__ __forceinline__ void flow_mma(const i32x8 (&A)[TI], const i32x8 (&B)[TJ],
-                                         const int (&xa)[TI], const int (&xb)[TJ],
-                                         f32x16 (&acc)[TI][TJ]) {
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int n = 0; n < TJ; ++n)
-      acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A[i], B[n], acc[i][n], 4, 4,
-                                                                   kByte, xa[i], kByte, xb[n]);
-}
-
-// A workgroup barrier behind a wait for all but the newest kCopies copies of the wave and for
-// all its LDS reads (__syncthreads would wait for every copy).
-template <int kCopies>
-__device__ __forceinline__ void flow_barrier() {
-  static_assert(kCopies < 64, "the counter's range");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt((kCopies & 15) | 7 << 4 | (kCopies >> 4) << 14);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-}
-
-// The order of a phase: one MFMA, then an LDS read and a copy while there are some.
-template <int kMfmas, int kReads, int kCopies>
-__device__ __forceinline__ void flow_schedule() {
-  constexpr int kReadStep = (kReads + kMfmas - 1) / kMfmas, kCopyStep = (kCopies + kMfmas - 1) / kMfmas;
-#pragma unroll
-  for (int m = 0; m < kMfmas; ++m) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (m * kReadStep < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kReadStep, 0);
-    if (m * kCopyStep < kCopies) __builtin_amdgcn_sched_group_barrier(0x020, kCopyStep, 0);
-  }
-}
-
-template <int J, typename T>
-__device__ __forceinline__ T& pick(T& a, T& b, T& c, T& d) {
-  if constexpr (J == 0) return a;
-  if constexpr (J == 1) return b;
-  if constexpr (J == 2) return c;
-  return d;
-}
-
-template <int TI, int TJ, int NS, int kEpi>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
-                          amdgpu_waves_per_eu(2, 2)))
-void mx_flow_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ as,
-                    const uint8_t* __restrict__ bd, const uint8_t* __restrict__ bs, int M, int N,
-                    int K, int tiles_m, int tiles_n, void* __restrict__ y, EpilogueArgs e) {
-  constexpr bool kGate = kEpi == kGated;
-  constexpr int kProj = kGate ? 2 : 1;   // weight rows of one column of Y
-  constexpr int kBM = 64 * TI, kBN = 64 * TJ;
-  static_assert(TJ == 2 && (NS == 2 || NS == 4), "");
-  // objects of their own: the compiler then knows that a copy to one does not touch another
-  __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st0;
-  __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st1;
-  __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st2;
-  __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st3;
-  __shared__ __attribute__((aligned(16))) FlowScales<TI, TJ> sc;
-  const TileCoord tc = tile_of(blockIdx.x, tiles_m, tiles_n);
-  const int tm = tc.tm, tn = tc.tn;
-
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lr = lane & 31, h = lane >> 5;
-  const uint32_t kb2 = K / 2, kb32 = K / 32;
-
-  FlowOperands p;
-  p.a = __builtin_amdgcn_make_buffer_rsrc((void*)ad, 0, (int)((uint32_t)M * kb2), kRsrcWord3);
-  p.sa = __builtin_amdgcn_make_buffer_rsrc((void*)as, 0, (int)((uint32_t)M * kb32), kRsrcWord3);
-  p.b = __builtin_amdgcn_make_buffer_rsrc((void*)bd, 0, (int)((uint32_t)(kProj * N) * kb2), kRsrcWord3);
-  p.sb = __builtin_amdgcn_make_buffer_rsrc((void*)bs, 0, (int)((uint32_t)(kProj * N) * kb32), kRsrcWord3);
-  // the weight row behind row r of the tile
-  auto weight_row = [&](int r) -> uint32_t {
-    if constexpr (!kGate) return tn * kBN + r;
-    bool up;
-    const int g = gated_row(r, up);
-    return tn * (kBN / 2) + g + (up ? N : 0);
-  };
-  {
-    // lane l of row-group q writes LDS slot (l & 3) of local row kBM/4*wave + 16*q + (l >> 2),
-    // and fetches the granule that belongs there
-    const uint32_t sub = lane >> 2, g = (lane & 3) ^ ((lane >> 4) & 3);
-    p.oa = (uint32_t)(tm * kBM + 16 * TI * wave + sub) * kb2 + 16 * g;
-    p.ob = weight_row(16 * TJ * wave + sub) * kb2 + 16 * g;
-    p.group_stride = 16 * kb2;
-    p.osa = (uint32_t)(tm * kBM + 64 * (wave % TI) + lane) * kb32;
-    p.osb = weight_row(64 * (wave % TJ) + lane) * kb32;
-  }
-
-  f32x16 acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int n = 0; n < TJ; ++n) acc[i][n] = f32x16{};
-
-  const int ra = (wave >> 1) * (32 * TI) + lr;
-  const int rb = (wave & 1) * (32 * TJ) + lr;
-  const int stages = K / kStageK, last = stages - 1;
-  constexpr int kMfmas = TI * TJ, kReads = TI + TJ, kCopies = TI + TJ;
-
-  // what is copied past the last stage is the last one again, where nobody reads it
-  flow_load_scales(sc, p, 0, wave);
-  flow_load(st0, p, 0, wave);
-  flow_load(st1, p, min(1, last), wave);
-  if constexpr (NS == 4) {
-    flow_load(st2, p, min(2, last), wave);
-    flow_load(st3, p, min(3, last), wave);
-  }
-  flow_barrier<(NS - 1) * kCopies>();
-  uint4 sa[TI], sb[TJ];
-  i32x8 A[TI], B[TJ], An[TI], Bn[TJ];
-  flow_scales(sc.a, ra, sa);
-  flow_scales(sc.b, rb, sb);
-  flow_operands(st0.a, ra, h, A);
-  flow_operands(st0.b, rb, h, B);
-
-  // Stage S, the J-th of its four.  At its barrier the copies of the NS - 2 stages behind the
-  // next one may be on their way, and those of the scales until they are read (J = 3).
-#define FOS_FLOW_STAGE(S, J)                                                                      \
-  {                                                                                               \
-    FlowStage<TI, TJ>& cur = pick<(J) % NS>(st0, st1, st2, st3);                                  \
-    FlowStage<TI, TJ>& next = pick<((J) + 1) % NS>(st0, st1, st2, st3);                           \
-    int xa[TI], xb[TJ];                                                                           \
-    _Pragma("unroll") for (int i = 0; i < TI; ++i) xa[i] = (int)(scale_word(sa[i], J) >> (8 * h)); \
-    _Pragma("unroll") for (int i = 0; i < TJ; ++i) xb[i] = (int)(scale_word(sb[i], J) >> (8 * h)); \
-    flow_operands(cur.a, ra, 2 + h, An);                                                          \
-    flow_operands(cur.b, rb, 2 + h, Bn);                                                          \
-    flow_mma<0>(A, B, xa, xb, acc);                                                               \
-    flow_schedule<kMfmas, kReads, 0>();                                                           \
-    flow_barrier<(NS - 2) * kCopies + ((J) >= 1 && (J) < NS && (J) < 3 ? 2 : 0)>();                \
-    flow_load(cur, p, min((S) + NS, last), wave);                                  \
-    if (J == 0) flow_load_scales(sc, p, ((S) + 4) / 4, wave);                                     \
-    if (J == 3) {                                                                                 \
-      flow_scales(sc.a, ra, sa);                                                                  \
-      flow_scales(sc.b, rb, sb);                                                                  \
-    }                                                                                             \
-    flow_operands(next.a, ra, h, A);                                                              \
-    flow_operands(next.b, rb, h, B);                                                              \
-    flow_mma<2>(An, Bn, xa, xb, acc);                                                             \
-    flow_schedule<kMfmas, kReads + (J == 3 ? kReads : 0), kCopies + (J == 0 ? 2 : 0)>();            \
-    __builtin_amdgcn_sched_barrier(0);                                                            \
-  }
-  int s = 0;
-  for (; s + 3 < stages; s += 4) {
-    FOS_FLOW_STAGE(s, 0)
-    FOS_FLOW_STAGE(s + 1, 1)
-    FOS_FLOW_STAGE(s + 2, 2)
-    FOS_FLOW_STAGE(s + 3, 3)
-  }
-  if (s < stages) {   // K % 256 == 0: two stages
-    FOS_FLOW_STAGE(s, 0)
-    FOS_FLOW_STAGE(s + 1, 1)
-  }
-#undef FOS_FLOW_STAGE
-  __builtin_amdgcn_s_waitcnt(0);   // no copy outlives the workgroup
-  store_fused<TI, TJ, kGate>(e, y, M, N, tm * kBM + (wave >> 1) * (32 * TI),
-                             (tn * kBN + (wave & 1) * (32 * TJ)) / kProj, lane, 1.0f, acc);
-}
-
-template <int TI, int TJ, int NS, int kEpi>
-hipError_t launch_flow(const QLinearArgs& a, hipStream_t s) {
-  constexpr int kCols = 64 * TJ / (kEpi == kGated ? 2 : 1);
-  const int tiles_m = (int)((a.M + 64 * TI - 1) / (64 * TI));
-  const int tiles_n = (int)((a.N + kCols - 1) / kCols);
-  mx_flow_kernel<TI, TJ, NS, kEpi><<<tiles_m * tiles_n, 256, 0, s>>>(
-      a.xd, a.xs, a.wd, a.ws, (int)a.M, (int)a.N, (int)a.K, tiles_m, tiles_n, a.y, a.e);
-  return hipGetLastError();
-}
-
-template <int kEpi>
-hipError_t launch_gemm(const uint8_t* ad, const uint8_t* as, const uint8_t* bd, const uint8_t* bs,
-                       int64_t M, int64_t N, int64_t K, void* y, const EpilogueArgs& e,
-                       hipStream_t s) {
-  constexpr int kCols = kEpi == kGated ? kMxTile / 2 : kMxTile;
-  const int tiles_m = (int)((M + kMxTile - 1) / kMxTile);
-  const int tiles_n = (int)((N + kCols - 1) / kCols);
-  mx_gemm_kernel<kEpi><<<tiles_m * tiles_n, 256, 0, s>>>(ad, as, bd, bs, (int)M, (int)N, (int)K,
-                                                         tiles_m, tiles_n, y, e);
-  return hipGetLastError();
-}
-
-// Kernel of an epilogue's product, by what a round of workgroups takes (us, measured with
-// silu: fixed, and per 4096 of K): 128 x 128 tiles, two to a CU or (half a round) one, while
-// there are few; 256 x 128, whose epilogues run beside another workgroup's products, for a
-// short K; 256 x 256, which copies least for its products, for a long one (8192 x 8192 x 1024: 72,
-// 67 and 86 us; x 4096: 226, 183 and 175; 512 x 4096 x 4096: 14, 19 and 34).
-struct MxShape {
-  int ti, tj, resident;
-  float half, half_k, full, full_k;
-};
-constexpr MxShape kMxShapes[] = {{2, 2, 512, 3.3f, 10.2f, 3.0f, 26.0f},
-                                 {4, 2, 512, 5.0f, 18.0f, 7.0f, 38.9f},
-                                 {4, 4, 256, 14.0f, 29.7f, 14.0f, 29.7f}};
-int64_t mx_tiles(const QLinearArgs& a, const MxShape& h) {
-  const int64_t cols = a.gated ? 32 * h.tj : 64 * h.tj;
-  return ((a.M + 64 * h.ti - 1) / (64 * h.ti)) * ((a.N + cols - 1) / cols);
-}
-const MxShape& mx_shape(const QLinearArgs& a) {
-  const MxShape* best = nullptr;
-  float least = 0.0f;
-  const float k = (float)a.K / 4096.0f;
-  for (const MxShape& h : kMxShapes) {
-    const int64_t tiles = mx_tiles(a, h), full = tiles / h.resident, rest = tiles % h.resident;
-    float us = (float)full * (h.full + h.full_k * k);
-    if (rest) us += 2 * rest <= h.resident ? h.half + h.half_k * k : h.full + h.full_k * k;
-    if (!best || us < least) {
-      best = &h;
-      least = us;
-    }
-  }
-  return *best;
-}
-
-template <int kEpi>
-hipError_t launch_mx_epi(const QLinearArgs& a, hipStream_t s) {
-  const MxShape& h = mx_shape(a);
-  if (h.tj == 4) return launch_gemm<kEpi>(a.xd, a.xs, a.wd, a.ws, a.M, a.N, a.K, a.y, a.e, s);
-  if (h.ti == 4) return launch_flow<4, 2, 2, kEpi>(a, s);
-  return launch_flow<2, 2, 4, kEpi>(a, s);
+  if (sc < nsc) mx_stage_mma<false>(st0, acc, ra, rb, h, st1, p, 0, wave);
+  store_tile(y, M, N, tm, tn, wave, lr, h, 1.0f, acc);
 }
 
 }  // namespace
@@ -707,13 +383,11 @@ hipError_t launch_mx_dequantize(const uint8_t* data, const uint8_t* scales, int6
 hipError_t launch_mx_gemm(const uint8_t* ad, const uint8_t* as, const uint8_t* bd,
                           const uint8_t* bs, int64_t M, int64_t N, int64_t K, uint16_t* y,
                           hipStream_t s) {
-  return launch_gemm<kPlain>(ad, as, bd, bs, M, N, K, y, EpilogueArgs{}, s);
-}
-
-int64_t mx_epilogue_grid(const QLinearArgs& a) { return mx_tiles(a, mx_shape(a)); }
-
-hipError_t launch_mx_epilogue(const QLinearArgs& a, hipStream_t s) {
-  return a.gated ? launch_mx_epi<kGated>(a, s) : launch_mx_epi<kFused>(a, s);
+  const int tiles_m = (int)((M + kMxTile - 1) / kMxTile);
+  const int tiles_n = (int)((N + kMxTile - 1) / kMxTile);
+  mx_gemm_kernel<<<tiles_m * tiles_n, 256, 0, s>>>(ad, as, bd, bs, (int)M, (int)N, (int)K,
+                                                   tiles_m, tiles_n, y);
+  return hipGetLastError();
 }
 
 }  // namespace fos
