@@ -915,6 +915,17 @@ def _whole(t: torch.Tensor, shape, dtype, dev: int, what: str) -> torch.Tensor:
     return t
 
 
+def _no_overlap(out: torch.Tensor, t: torch.Tensor, what: str, whole: bool = True) -> None:
+    """Refuses an output whose memory t takes a part of, or (not ``whole``) any of: other rows
+    of it would be read after they are written."""
+    a, b = out.data_ptr(), t.data_ptr()
+    if a == b and whole and out.dtype == t.dtype and (out.shape[0] == 1 or out.stride() == t.stride()):
+        return
+    end = lambda x: x.element_size() * ((x.shape[0] - 1) * x.stride(0) + x.shape[1])
+    if out.numel() and a < b + end(t) and b < a + end(out):
+        raise ValueError(f"the output's memory overlaps {what}")
+
+
 @dataclass
 class RMSNormOutput:
     """What ``rmsnorm_fwd`` computes: h bf16 [M, K], the sum with the residual (x itself
@@ -936,7 +947,7 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     its column-wise record needs for the weight's gradient).  ``tensor_scale``: fp32 [1], the
     NVFP4 scale to use (delayed scaling; one pass over x); by default that of y is computed.
     ``h``: optional destination of the sum, for instance ``residual`` itself; only with a
-    residual.  K a multiple of 16 (MXFP4: 32), at most 32768."""
+    residual, and not another part of the memory of either.  K a multiple of 16 (MXFP4: 32), at most 32768."""
     strides, dev = x.stride(), x.get_device()
     if len(strides) != 2 or strides[1] != 1 or x.dtype != _BF16 or dev < 0:
         raise ValueError("x must be a 2-D bfloat16 CUDA tensor with contiguous rows")
@@ -957,7 +968,11 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     r_stride = 0
     if residual is not None:
         r_stride = _rows_of(residual, M, K, dev, "residual")
-        h = x.new_empty(M, K) if h is None else _whole(h, (M, K), _BF16, dev, "h")
+        if h is None:
+            h = x.new_empty(M, K)
+        else:
+            _no_overlap(_whole(h, (M, K), _BF16, dev, "h"), residual, "the residual's in part")
+            _no_overlap(h, x, "x's in part")
     elif h is not None:
         raise ValueError("h is a destination for the sum with a residual")
     rstd = x.new_empty(M, dtype=_F32)
@@ -974,15 +989,10 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             record = NVFP4Tensor(data, scales, t)
         else:
             record = MXFP4Tensor(data, scales)
-    call = _lib.fos_rmsnorm_fwd
-    if dev != _current_device():
-        call = _on(dev, call)
-    _check(call(x.data_ptr(), strides[0] if M > 1 else K,
-                None if residual is None else residual.data_ptr(), r_stride, weight.data_ptr(), M, K,
-                eps, None if h is None else h.data_ptr(), rstd.data_ptr(),
-                None if y is None else y.data_ptr(), code, rule_code, _address(data),
-                _address(scales), _address(t), 0 if tensor_scale is None else 1, _address(ws),
-                0 if ws is None else _SCALE_WORKSPACE, _raw_stream(dev)), "fos_rmsnorm_fwd")
+    _call(dev, "fos_rmsnorm_fwd", x.data_ptr(), strides[0] if M > 1 else K, _address(residual),
+          r_stride, weight.data_ptr(), M, K, eps, _address(h), rstd.data_ptr(), _address(y), code,
+          rule_code, _address(data), _address(scales), _address(t),
+          0 if tensor_scale is None else 1, _address(ws), 0 if ws is None else _SCALE_WORKSPACE)
     return RMSNormOutput(x if h is None else h, rstd, y, record)
 
 
@@ -1030,14 +1040,23 @@ def _epilogue(M: int, W: int, gated: bool, like: torch.Tensor, dev: int, bias, a
         out = like.new_empty(M, N, dtype=out_dtype)
     else:
         _whole(out, (M, N), out_dtype, dev, "out")
+        if residual is not None:
+            _no_overlap(out, residual, "the residual's in part")
     preact = like.new_empty(M, W, dtype=_BF16) if return_preact else None
     e = FosEpilogue(ctypes.sizeof(FosEpilogue), act, int(gated), _OUT_CODE[out_dtype],
                     _address(bias), _address(residual), stride, _address(preact), 0)
     return N, e, out, preact
 
 
+def _check_kind(q, block: int) -> None:
+    if not isinstance(q, NVFP4Tensor if block == 16 else MXFP4Tensor):
+        raise ValueError(f"an {'NVFP4' if block == 16 else 'MXFP4'} record is needed here")
+
+
 def _check_product_records(xq, wq, block: int):
     """(device, M, W, K) of two records blocked along K."""
+    _check_kind(xq, block)
+    _check_kind(wq, block)
     xd, wd = xq.data, wq.data
     dev = xd.get_device()
     if dev < 0 or xd.dim() != 2 or wd.dim() != 2:
@@ -1056,9 +1075,9 @@ def _check_product_records(xq, wq, block: int):
 
 
 def _qlinear_epilogue(xq, wq, gated, bias, activation, residual, out_dtype, return_preact, out):
+    dev, M, W, K = _check_product_records(xq, wq, 16)
     if xq.hadamard_seed != wq.hadamard_seed:
         raise ValueError("one of the records carries a Hadamard transform that the other does not")
-    dev, M, W, K = _check_product_records(xq, wq, 16)
     N, e, y, z = _epilogue(M, W, gated, xq.data, dev, bias, activation, residual, out_dtype,
                            return_preact, out)
     _call(dev, "fos_qlinear_epilogue_fwd", xq.data.data_ptr(), xq.scales.data_ptr(),
@@ -1083,7 +1102,8 @@ def qlinear_epilogue_fwd(xq: NVFP4Tensor, wq: NVFP4Tensor, bias: Optional[torch.
     """``qlinear_fwd`` with an epilogue: Y = act(Z) + residual, Z = deq(X) deq(W)^T + bias, in
     fp32 up to one rounding to ``out_dtype`` (bf16 or fp32).  ``activation``: "none", "relu",
     "gelu", "gelu_tanh" or "silu".  bias bf16 [N]; residual bf16 [M, N], rows may be strided;
-    ``out``: optional [M, N] destination (for instance the residual itself).
+    ``out``: optional [M, N] destination (for instance the residual itself, not rows shifted
+    against it).
     ``return_preact``: also Z in bf16, for ``epilogue_bwd`` or ``qlinear_epilogue_bwd``."""
     return _qlinear_epilogue(xq, wq, False, bias, activation, residual, out_dtype, return_preact, out)
 
@@ -1114,6 +1134,7 @@ def mx_qglu_fwd(aq: MXFP4Tensor, bq: MXFP4Tensor, activation: str = "silu",
 
 
 def _wlinear_epilogue(x, wq, block, gated, bias, activation, residual, out_dtype, return_preact, out):
+    _check_kind(wq, block)
     data, scales = wq.data, wq.scales
     dev = data.get_device()
     if dev < 0 or data.dim() != 2 or x.dim() != 2:
@@ -1125,6 +1146,8 @@ def _wlinear_epilogue(x, wq, block, gated, bias, activation, residual, out_dtype
     _whole(scales, (W, K // block), _U8, dev, "record scales")
     N, e, y, z = _epilogue(M, W, gated, x, dev, bias, activation, residual, out_dtype,
                            return_preact, out)
+    if out is not None:
+        _no_overlap(out, x, "x's", whole=False)
     if block == 16:
         t = wq.tensor_scale
         if wq.hadamard_seed is not None:
@@ -1144,7 +1167,8 @@ def wlinear_epilogue_fwd(x: torch.Tensor, wq: NVFP4Tensor, bias: Optional[torch.
                          out_dtype: torch.dtype = torch.bfloat16, return_preact: bool = False,
                          out: Optional[torch.Tensor] = None):
     """``wlinear_fwd`` (few bf16 activation rows) with an epilogue: Y = act(Z) + residual,
-    Z = X deq(W)^T + bias.  Arguments as for ``qlinear_epilogue_fwd``."""
+    Z = X deq(W)^T + bias.  Arguments as for ``qlinear_epilogue_fwd``; ``out`` shares no
+    memory with x."""
     return _wlinear_epilogue(x, wq, 16, False, bias, activation, residual, out_dtype, return_preact, out)
 
 

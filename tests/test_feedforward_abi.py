@@ -3,11 +3,13 @@ documented status before any HIP call (the pointers are never dereferenced), and
 binding refuses tensors that the library could not address."""
 import contextlib
 import ctypes
+import types
 
 import pytest
 import torch
 
 from fp4_block_quantization_amd import fos
+from test_serving_abi import Devices
 
 F = ctypes.c_void_p(0x100000)
 BIG = ctypes.c_void_p(0x1000000)
@@ -172,7 +174,9 @@ def test_binding_refuses_cpu_tensors_and_bad_names():
                           torch.zeros(1))
     mx = fos.MXFP4Tensor(rec.data, torch.zeros(32, 2, dtype=torch.uint8))
     for call in (lambda: fos.rmsnorm_fwd(x, w), lambda: fos.rmsnorm_bwd(x, x, w, torch.zeros(4)),
-                 lambda: fos.qlinear_epilogue_fwd(rec, rec), lambda: fos.mx_qlinear_epilogue_fwd(mx, mx),
+                 lambda: fos.qlinear_epilogue_fwd(rec, rec), lambda: fos.qlinear_epilogue_fwd(rec, mx),
+                 lambda: fos.qglu_fwd(mx, rec), lambda: fos.mx_qglu_fwd(mx, rec), lambda: fos.wglu_fwd(x, mx),
+                 lambda: fos.mx_wglu_fwd(x, rec), lambda: fos.mx_qlinear_epilogue_fwd(mx, mx),
                  lambda: fos.qglu_fwd(rec, rec), lambda: fos.mx_qglu_fwd(mx, mx),
                  lambda: fos.wlinear_epilogue_fwd(x, rec), lambda: fos.mx_wlinear_epilogue_fwd(x, mx),
                  lambda: fos.wglu_fwd(x, rec), lambda: fos.mx_wglu_fwd(x, mx),
@@ -180,3 +184,32 @@ def test_binding_refuses_cpu_tensors_and_bad_names():
                  lambda: fos.qglu_bwd(x, x, None, None), lambda: fos.qlinear_epilogue_bwd(x, x, rec, rec)):
         with refused():
             call()
+
+
+def test_binding_refuses_outputs_that_overlap_what_is_read():
+    flat = torch.zeros(8 * 64, dtype=torch.bfloat16)
+    t = flat.view(8, 64)
+    ok = fos._no_overlap
+    ok(t[1:4], t[1:4], "it")                             # in place
+    ok(t[0:4], t[4:8], "it"), ok(t[4:8], t[0:4], "it")    # side by side
+    ok(t[:0], t[:0], "it")
+    ok(t[:, :32], t[:, :32], "it")                       # equal rows of a wider tensor
+    for out, other in ((t[0:4], t[1:5]), (t[1:5], t[0:4]), (t[0:4], t[3:7]),
+                       (flat[:256].view(8, 32), t[:, :32]), (flat[:256].view(8, 32), t[:, 32:]),
+                       (t[0:1], t.view(torch.int16)[0:1]), (flat[8:72].view(1, 64), t[0:1])):
+        with refused():
+            ok(out, other, "it")
+    with refused():
+        ok(t[1:4], t[1:4], "it", whole=False)
+
+
+def test_calls_run_with_their_device_current(monkeypatch):
+    devices = Devices(monkeypatch, current=1)
+    seen = []
+    entry = lambda *args: seen.append((devices.current, args)) or fos.FOS_OK
+    monkeypatch.setattr(fos, "_lib", types.SimpleNamespace(fos_entry=entry))
+    monkeypatch.setattr(fos, "_raw_stream", lambda index: 100 + index)
+    fos._call(3, "fos_entry", 7)
+    fos._call(1, "fos_entry", 8)
+    assert seen == [(3, (7, 103)), (1, (8, 101))]
+    assert devices.entered == [3] and devices.current == 1

@@ -504,3 +504,260 @@ def test_product_backward(fos, gated):
     assert none is None and torch.equal(dx, f(dy, z, xt, wt, activation="silu")[0])
     none, dw = f(dy, z, xt, None, activation="silu", need_dx=False)
     assert none is None and torch.equal(dw, f(dy, z, xt, wt, activation="silu")[1])
+
+
+# ------------------------------------------------------------------- refusals on the device
+
+def test_binding_refuses_what_the_library_could_not_address(fos):
+    """Wrong shapes, types and overlaps are refused on the host, before any launch."""
+    x, r, w = norm_inputs(8, 64, 1, True)
+    rec, up = fos.quantize(x.repeat(2, 1)), fos.quantize(x.repeat(4, 1))
+    mx = fos.mx_quantize(torch.cat((x, x, x, x), 1))
+    y = torch.zeros(16, 32, dtype=BF16, device=DEV)
+    short = fos.NVFP4Tensor(rec.data, rec.scales[:, :2].contiguous(), rec.tensor_scale)
+    turned = fos.NVFP4Tensor(rec.data, rec.scales, rec.tensor_scale, hadamard_seed=3)
+    calls = [
+        lambda: fos.rmsnorm_fwd(x, w[:32]), lambda: fos.rmsnorm_fwd(x.float(), w),
+        lambda: fos.rmsnorm_fwd(x, w.float()), lambda: fos.rmsnorm_fwd(x.T, w),
+        lambda: fos.rmsnorm_fwd(x, w, residual=r[:4]), lambda: fos.rmsnorm_fwd(x, w, format="fp8"),
+        lambda: fos.rmsnorm_fwd(x, w, rule="5"), lambda: fos.rmsnorm_fwd(x, w, h=r),
+        lambda: fos.rmsnorm_fwd(x, w, tensor_scale=rec.tensor_scale),
+        lambda: fos.rmsnorm_fwd(x, w, format="nvfp4", tensor_scale=rec.tensor_scale.double()),
+        lambda: fos.rmsnorm_fwd(x[1:5], w, residual=r[:4], h=x[:4]),
+        lambda: fos.rmsnorm_fwd(x[:4], w, residual=r[1:5], h=r[:4]),
+        lambda: fos.rmsnorm_bwd(x, r, w, torch.ones(4, device=DEV)),
+        lambda: fos.rmsnorm_bwd(x, r[:4], w, torch.ones(8, device=DEV)),
+        lambda: fos.rmsnorm_bwd(x, r, w, torch.ones(8, device=DEV), dh=x[:4]),
+        lambda: fos.qlinear_epilogue_fwd(rec, mx), lambda: fos.qlinear_epilogue_fwd(rec, short),
+        lambda: fos.qlinear_epilogue_fwd(rec, turned), lambda: fos.wlinear_epilogue_fwd(x, turned),
+        lambda: fos.qlinear_epilogue_fwd(rec, up, bias=w), lambda: fos.qlinear_epilogue_fwd(rec, up, activation="tanh"),
+        lambda: fos.qlinear_epilogue_fwd(rec, up, residual=y[:, :16]),
+        lambda: fos.qlinear_epilogue_fwd(rec, up, out=y.float()),
+        lambda: fos.qlinear_epilogue_fwd(rec, up, out_dtype=torch.float16),
+        lambda: fos.qlinear_epilogue_fwd(rec, rec, residual=torch.zeros(17, 16, dtype=BF16, device=DEV)[1:],
+                                         out=y.view(-1)[:128].view(16, 8)),
+        lambda: fos.qlinear_epilogue_fwd(rec, up, residual=torch.cat((y, y))[1:17], out=y.T),
+        lambda: fos.qglu_fwd(rec, fos.NVFP4Tensor(up.data[:15], up.scales[:15], up.tensor_scale)),
+        lambda: fos.wlinear_epilogue_fwd(x[:, :32], rec), lambda: fos.mx_wlinear_epilogue_fwd(x, mx),
+        lambda: fos.wlinear_epilogue_fwd(x.repeat(1, 2)[:, :64].T, rec),
+        lambda: fos.epilogue_bwd(y, y[:8]), lambda: fos.epilogue_bwd(y, y, gated=True),
+        lambda: fos.epilogue_bwd(y.float(), y), lambda: fos.epilogue_bwd(y[:, :16], y[:, :16].contiguous()),
+        lambda: fos.qlinear_epilogue_bwd(y, y, None, None, need_dx=False, need_dw=False)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    rows = torch.zeros(18, 32, dtype=BF16, device=DEV)
+    for out in (rows[1:17], rows[2:18]):
+        with pytest.raises(ValueError, match="overlaps"):
+            fos.qlinear_epilogue_fwd(rec, up, residual=rows[:16], out=out)
+    same = torch.zeros(16, 64, dtype=BF16, device=DEV)
+    square = fos.quantize(torch.ones(64, 64, dtype=BF16, device=DEV))
+    with pytest.raises(ValueError, match="overlaps"):
+        fos.wlinear_epilogue_fwd(same, square, residual=same, out=same)
+    with pytest.raises(fos.FosError):                    # K of 96: not a multiple of 64
+        a = fos.quantize(torch.ones(16, 96, dtype=BF16, device=DEV))
+        fos.qlinear_epilogue_fwd(a, a)
+    with pytest.raises(fos.FosError):
+        fos.rmsnorm_fwd(x, w, eps=0.0)
+    with pytest.raises(fos.FosError):
+        fos.rmsnorm_fwd(x[:, :40].contiguous(), w[:40].contiguous())
+
+
+# --------------------------------------------------------------- together, as they are used
+
+class Block:
+    """A gated feed-forward block on NVFP4 records with its backward pass."""
+
+    def __init__(self, fos, m, k, hidden, seed):
+        self.fos, self.hidden = fos, hidden
+        self.x, self.r, self.w = norm_inputs(m, k, seed, True)
+        self.dout = W.random_bf16(m, k, seed + 3, "normal", scale=0.05).to(DEV)
+        self.in_w = W.random_bf16(2 * hidden, k, seed + 4, "normal", scale=k ** -0.5).to(DEV)
+        self.out_w = W.random_bf16(k, hidden, seed + 5, "normal", scale=hidden ** -0.5).to(DEV)
+        self.win, self.win_t = fos.quantize(self.in_w, block="2d", outputs=("row", "col"))
+        self.wout, self.wout_t = fos.quantize(self.out_w, block="2d", outputs=("row", "col"))
+
+    def inputs(self, seed):
+        m, k = self.x.shape
+        for t, s in ((self.x, 0), (self.r, 1), (self.dout, 2)):
+            t.copy_(W.random_bf16(m, k, seed + s, "normal", scale=(1.0, 3.0, 0.05)[s]))
+
+    def forward(self):
+        f = self.fos
+        n = f.rmsnorm_fwd(self.x, self.w, residual=self.r, format="nvfp4", return_y=True)
+        y, z = f.qglu_fwd(n.record, self.win, return_preact=True)
+        a, at = f.quantize(y, outputs=("row", "col"))
+        out = f.qlinear_epilogue_fwd(a, self.wout, residual=n.h)
+        return dict(n=n, y=y, z=z, a=a, at=at, out=out)
+
+    def backward(self, s):
+        f = self.fos
+        dq, dqt = f.quantize(self.dout, outputs=("row", "col"))
+        da, dw_out = f.qlinear_bwd(dq, dqt, s["at"], self.wout_t)
+        xt = f.quantize(s["n"].y, outputs=("col",))
+        dx, dw_in, db = f.qglu_bwd(da, s["z"], xt, self.win_t, return_dbias=True)
+        dh, dw = f.rmsnorm_bwd(dx, s["n"].h, self.w, s["n"].rstd, dh=self.dout)
+        return dict(da=da, dw_out=dw_out, dx=dx, dw_in=dw_in, db=db, dh=dh, dw=dw)
+
+    def run(self):
+        s = self.forward()
+        g = self.backward(s)
+        n = s["n"]
+        return [n.h, n.rstd, n.y, n.record.data, n.record.scales, n.record.tensor_scale, s["y"], s["z"],
+                s["out"], *g.values()]
+
+
+def values_of(q):
+    return operand_exact(q.data.cpu().numpy(), q.scales.cpu().numpy()) * float(q.tensor_scale)
+
+
+@pytest.mark.parametrize("m,k,hidden", [(64, 128, 64), (192, 320, 448), (320, 1024, 192)])
+def test_block_forward_and_backward(fos, m, k, hidden):
+    """Every stage against the references, from what the stage before it gave."""
+    b = Block(fos, m, k, hidden, m)
+    s = b.forward()
+    g = b.backward(s)
+    n = s["n"]
+    yb = check_norm(n, b.x, b.r, b.w, 1e-6)
+    assert torch.equal(n.y.cpu(), yb)
+    q = fos.quantize(n.y)
+    assert torch.equal(n.record.data, q.data) and torch.equal(n.record.scales, q.scales)
+    assert torch.equal(n.record.tensor_scale, q.tensor_scale)
+    check_epilogue(s["y"], s["z"], values_of(n.record), values_of(b.win), None, "silu", True, None, k)
+    check_epilogue(s["out"], None, values_of(s["a"]), values_of(b.wout), None, "none", False, f64(n.h), hidden)
+    check_bwd(fos, g["da"], s["z"], "silu", True)
+    dz, db, t = fos.epilogue_bwd(g["da"], s["z"], "silu", gated=True, return_dbias=True, return_tensor_scale=True)
+    assert torch.equal(db, g["db"])
+    rows, cols = fos.quantize(dz, outputs=("row", "col"))
+    xt = fos.quantize(n.y, outputs=("col",))
+    for got, u, v in ((g["dx"], rows, b.win_t), (g["dw_in"], cols, xt)):
+        u, v = values_of(u), values_of(v)
+        err = (u.shape[1] + 8) * U * (np.abs(u) @ np.abs(v).T)
+        within(f64(got), u @ v.T, 2.0 ** -8 * (np.abs(u @ v.T) + err) + err, "product")
+    ref, rdw, size, sdw = FF.rmsnorm_bwd64(f64(g["dx"]), f64(n.h), f64(b.w), n.rstd.cpu().double().numpy(),
+                                           f64(b.dout))
+    err = (k + 12) * U * size
+    within(f64(g["dh"]), ref, 2.0 ** -8 * (np.abs(ref) + err) + err, "dh")
+    within(g["dw"].cpu().double().numpy(), rdw, (m + 4) * U * sdw, "dw")
+
+
+def same(got, want):
+    return all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want, strict=True))
+
+
+def test_block_replayed_from_graphs(fos):
+    """The whole step, forward and backward, captured and replayed with new inputs and eager
+    work between; a second graph of it, captured meanwhile, replays beside the first."""
+    blocks = [Block(fos, 192, 320, 448, 1), Block(fos, 128, 512, 320, 2)]
+    graphs, outs, sides = [], [], [torch.cuda.Stream() for _ in blocks]
+    for b, side in zip(blocks, sides):
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(b.run())
+        graphs.append(g)
+    for i in range(4):
+        for b in blocks:
+            b.inputs(10 * i + 5)
+        torch.cuda.synchronize()
+        for g, side in zip(graphs, sides):          # at the same time, on streams of their own
+            with torch.cuda.stream(side):
+                g.replay()
+        torch.cuda.synchronize()
+        for b, got in zip(blocks, outs):
+            assert same(got, b.run()), i
+        torch.cuda.synchronize()
+
+
+def test_backward_captured_while_eager_results_live(fos):
+    """The forward pass ran eagerly; the backward pass of what it left is captured."""
+    b = Block(fos, 128, 256, 192, 3)
+    s = b.forward()
+    want = b.backward(s)
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        got = b.backward(s)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got.values(), want.values())
+        assert same(b.backward(s).values(), want.values())
+
+
+def test_decode_block_on_two_streams(fos):
+    """The few-row path (norm, gated product, product with the residual in place), issued on
+    two streams at once, gives each its own results."""
+    k, hidden, m = 1024, 768, 3
+    _, _, _, win = nv_weight(fos, 2 * hidden, k, 1)
+    _, _, _, wout = mx_weight(fos, k, hidden, 2)
+    _, _, w = norm_inputs(1, k, 3, False)
+    xs = [W.random_bf16(m, k, 7 + i, "normal").to(DEV) for i in range(2)]
+
+    def step(x, h):
+        n = fos.rmsnorm_fwd(x, w)
+        u = fos.wglu_fwd(n.y, win, activation="gelu_tanh")
+        fos.mx_wlinear_epilogue_fwd(u, wout, residual=h, out=h)
+        t = fos.rmsnorm_fwd(h, w, format="nvfp4")
+        return h, t.record.data, t.record.scales, t.record.tensor_scale
+
+    want = [step(x, x.clone()) for x in xs]
+    hs = [[x.clone() for _ in range(20)] for x in xs]
+    sides = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(20):
+        for j, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                got[j].append(step(xs[j], hs[j][i]))
+    torch.cuda.synchronize()
+    for j in range(2):
+        for g in got[j]:
+            assert same(g, want[j])
+
+
+# ------------------------------------------------------------------------- past 32 bits
+
+def test_rows_past_32_bit_offsets(fos):
+    """More than 2^31 elements: the last rows are those of a call on them alone."""
+    m, k = 66000, 32768
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(m, k, dtype=BF16, device=DEV).normal_(generator=gen)
+    w = W.random_bf16(1, k, 2, "normal")[0].to(DEV)
+    t = torch.full((1,), 2.0 ** -6, device=DEV)
+    last = slice(m - 3, m)
+    n = fos.rmsnorm_fwd(x, w, format="nvfp4", tensor_scale=t, return_y=True)
+    few = fos.rmsnorm_fwd(x[last], w, format="nvfp4", tensor_scale=t, return_y=True)
+    assert same([n.rstd[last], n.y[last], n.record.data[last], n.record.scales[last]],
+                [few.rstd, few.y, few.record.data, few.record.scales])
+    y = n.y
+    del n
+    dx, _ = fos.rmsnorm_bwd(y, x, w, fos.rmsnorm_fwd(x, w).rstd)
+    assert torch.equal(dx[last], fos.rmsnorm_bwd(y[last], x[last], w, few.rstd)[0])
+    del dx
+    dz = fos.epilogue_bwd(y, x, "silu")
+    assert torch.equal(dz[last], fos.epilogue_bwd(y[last], x[last], "silu"))
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_outputs_past_32_bit_offsets(fos, fmt):
+    m, n, k = 140000, 16400, 256
+    nv = fmt == "nvfp4"
+    a, b = (W.random_bf16(r, k, s, "normal").to(DEV) for r, s in ((m, 1), (n, 2)))
+    make = fos.quantize if nv else fos.mx_quantize
+    f = fos.qlinear_epilogue_fwd if nv else fos.mx_qlinear_epilogue_fwd
+    aq, bq = make(a), make(b)
+    res = torch.zeros(m, n, dtype=BF16, device=DEV)
+    last = slice(m - 5, m)
+    res[last] = W.random_bf16(5, n, 3, "normal").to(DEV)
+    f(aq, bq, activation="silu", residual=res, out=(y := res))
+    want = W.random_bf16(5, n, 3, "normal")
+    if nv:
+        u, v = operand_exact(aq.data[last].cpu().numpy(), aq.scales[last].cpu().numpy()), values_of(bq)
+        u = u * float(aq.tensor_scale)
+    else:
+        u, v = (MX.operand_exact(q.cpu().numpy(), s.cpu().numpy())
+                for q, s in ((aq.data[last], aq.scales[last]), (bq.data, bq.scales)))
+    check_epilogue(y[last], None, u, v, None, "silu", False, f64(want), k)
