@@ -1,7 +1,8 @@
 """Decode steps of one transformer layer on 4-bit records: the projections are
 weight-only products with NVFP4 records, the keys and values go to a paged cache (NVFP4 or
 bf16), every sequence's new token attends over its pages, and the MLP's weights are MXFP4
-records.  The step's launches are captured once and replayed for every token.
+records; activation and residual are added in the products' epilogues.  The step's launches
+are captured once and replayed for every token.
 
     python examples/decode_step.py --cache nvfp4 --batch 16 --prompt 1000 --steps 64
 """
@@ -19,8 +20,8 @@ def random_bf16(rows, cols, scale, gen, device):
     return (scale * torch.randn(rows, cols, generator=gen)).to(device, torch.bfloat16)
 
 
-def normed(x):
-    return torch.nn.functional.rms_norm(x, x.shape[-1:], eps=1e-6)
+def normed(x, weight=None):
+    return fos.rmsnorm_fwd(x, x.new_ones(x.shape[1]) if weight is None else weight).y
 
 
 class Layer:
@@ -37,10 +38,11 @@ class Layer:
         self.w_up = fos.mx_quantize(weight(hidden, width))
         self.w_down = fos.mx_quantize(weight(width, hidden))
         self.b_qkv = random_bf16(1, qkv, 0.1, gen, device)[0]
+        self.norm_in, self.norm_mlp = torch.ones(2, width, dtype=torch.bfloat16, device=device)
 
     def project(self, x):
         """q, k, v of x: views of one product, no copies."""
-        qkv = fos.wlinear_fwd(normed(x), self.w_qkv, bias=self.b_qkv)
+        qkv = fos.wlinear_fwd(normed(x, self.norm_in), self.w_qkv, bias=self.b_qkv)
         sizes = [self.q_heads, self.kv_heads, self.kv_heads]
         return [t.unflatten(1, (-1, self.head_dim))
                 for t in qkv.split([n * self.head_dim for n in sizes], dim=1)]
@@ -51,9 +53,9 @@ class Layer:
         q, k, v = self.project(x)
         fos.kv_append(cache, k, v, slots)
         a = fos.paged_decode(q, cache, table, lens, ws=ws)
-        h = x + fos.wlinear_fwd(a.flatten(1), self.w_out)
-        u = torch.nn.functional.silu(fos.mx_wlinear_fwd(normed(h), self.w_up))
-        y = h + fos.mx_wlinear_fwd(u, self.w_down)
+        h = fos.wlinear_epilogue_fwd(a.flatten(1), self.w_out, residual=x)
+        u = fos.mx_wlinear_epilogue_fwd(normed(h, self.norm_mlp), self.w_up, activation="silu")
+        y = fos.mx_wlinear_epilogue_fwd(u, self.w_down, residual=h)
         return y, dict(q=q, k=k, v=v, attention=a, h=h, u=u)
 
 
