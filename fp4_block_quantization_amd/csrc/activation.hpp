@@ -46,7 +46,7 @@ __device__ __forceinline__ float sigmoid(float u) {
 
 template <int kAct>
 __device__ __forceinline__ float activate(float z) {
-  if constexpr (kAct == kActRelu) return fmaxf(z, 0.0f);
+  if constexpr (kAct == kActRelu) return z < 0.0f ? 0.0f : z;   // a NaN stays, which fmaxf drops
   if constexpr (kAct == kActGelu) {
     float e;
     const float q = normal_tail(z, e);
@@ -70,14 +70,15 @@ __device__ __forceinline__ float activate(int act, float z) {
 }
 
 // Value and slope.  s(u) and s(-u) come from e^-|u|, which does not overflow; z^2 is taken
-// of a z within +-10^6 (there the slope is 0 or 1).
+// of a z within +-10^6 (there the slope is 0 or 1).  fminf and fmaxf would make a number of a
+// NaN: the value has it from z, and the slope where it depends on z.
 template <int kAct>
 __device__ __forceinline__ void activate_slope(float z, float& f, float& df) {
   if constexpr (kAct == kActNone) {
     f = z;
     df = 1.0f;
   } else if constexpr (kAct == kActRelu) {
-    f = fmaxf(z, 0.0f);
+    f = z < 0.0f ? 0.0f : z;
     df = z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (kAct == kActGelu) {
     float e;
@@ -86,7 +87,7 @@ __device__ __forceinline__ void activate_slope(float z, float& f, float& df) {
     f = z * p;
     df = __builtin_fmaf(fminf(fmaxf(z, -1e6f), 1e6f), e * 0.39894228f, p);   // z / sqrt(2 pi) e^..
   } else {
-    const float zc = fminf(fmaxf(z, -1e6f), 1e6f);
+    const float zc = z > 1e6f ? 1e6f : z < -1e6f ? -1e6f : z;
     const float z2 = zc * zc;
     const float u = kAct == kActSilu ? zc : zc * __builtin_fmaf(z2, kTanhC * kTanhCubic, kTanhC);
     const float du = kAct == kActSilu ? 1.0f : __builtin_fmaf(z2, 3.0f * kTanhC * kTanhCubic, kTanhC);

@@ -348,6 +348,32 @@ def test_qlinear_epilogue_residual_in_place_and_strided(fos, n):
     assert (stream[0] == 7).all() and (stream[-1] == 7).all()
 
 
+@pytest.mark.parametrize("m", [1, 3, 17, 33, 130, 257])
+@pytest.mark.parametrize("n", [256, 131])
+@pytest.mark.parametrize("out", [BF16, torch.float32])
+def test_rows_behind_the_last_are_left_as_they_were(fos, m, n, out):
+    """The rows that a tile has past M, in the memory behind y: not written."""
+    k = 512
+    for nv in (True, False):
+        _, _, _, xq = (nv_act if nv else mx_weight)(fos, m, k, 3)
+        _, _, _, wq = (nv_weight if nv else mx_weight)(fos, 2 * n, k, 4)
+        x = W.random_bf16(m, k, 5, "normal").to(DEV)
+        for call in ((fos.qlinear_epilogue_fwd, fos.qglu_fwd) if nv else
+                     (fos.mx_qlinear_epilogue_fwd, fos.mx_qglu_fwd)):
+            cols = 2 * n if "epilogue" in call.__name__ else n
+            held = torch.full((m + 600, cols), 7.0, dtype=out, device=DEV)
+            call(xq, wq, activation="relu", out_dtype=out, out=held[300:300 + m])
+            assert torch.equal(held[300:300 + m], call(xq, wq, activation="relu", out_dtype=out))
+            assert (held[:300] == 7).all() and (held[300 + m:] == 7).all(), call.__name__
+        for call in ((fos.wlinear_epilogue_fwd, fos.wglu_fwd) if nv else
+                     (fos.mx_wlinear_epilogue_fwd, fos.mx_wglu_fwd)):
+            cols = 2 * n if "epilogue" in call.__name__ else n
+            held = torch.full((m + 600, cols), 7.0, dtype=out, device=DEV)
+            call(x, wq, activation="relu", out_dtype=out, out=held[300:300 + m])
+            assert (held[300:300 + m] != 7).any()
+            assert (held[:300] == 7).all() and (held[300 + m:] == 7).all(), call.__name__
+
+
 W_SHAPES = [(1, 1, 32), (1, 256, 256), (1, 4096, 512), (2, 130, 1024), (3, 17, 96), (4, 64, 2080),
             (5, 33, 1056), (7, 300, 64), (16, 512, 1024), (17, 100, 288), (31, 63, 544),
             (33, 16, 2048), (61, 259, 1312), (64, 1024, 512), (65, 40, 352), (130, 96, 160),
@@ -401,6 +427,44 @@ def test_wlinear_epilogue_of_no_rows(fos):
     assert fos.wlinear_epilogue_fwd(x, wq, activation="silu").shape == (0, 32)
     y, z = fos.wglu_fwd(x, wq, return_preact=True)
     assert y.shape == (0, 16) and z.shape == (0, 32)
+
+
+@pytest.mark.parametrize("act", FF.ACTIVATIONS)
+def test_a_nan_is_kept(fos, act):
+    """A NaN in a bias, a residual or an activation row gives NaN in its column, element or row
+    and nowhere else, and a NaN pre-activation a NaN gradient."""
+    m, n, k = 20, 64, 512
+    _, _, _, xq = nv_act(fos, m, k, 1)
+    _, _, _, wq = nv_weight(fos, n, k, 2)
+    _, _, _, mxq = mx_weight(fos, m, k, 1)
+    _, _, _, mwq = mx_weight(fos, n, k, 2)
+    x = W.random_bf16(m, k, 3, "normal").to(DEV)
+    bias, res = W.random_bf16(1, n, 4, "normal")[0].to(DEV), W.random_bf16(m, n, 5, "normal").to(DEV)
+    nan_bias, nan_res, nan_x = bias.clone(), res.clone(), x.clone()
+    nan_bias[5] = nan_res[3, 7] = nan_x[2, 100] = float("nan")
+    for f, a, w in ((fos.qlinear_epilogue_fwd, xq, wq), (fos.mx_qlinear_epilogue_fwd, mxq, mwq),
+                    (fos.wlinear_epilogue_fwd, x, wq), (fos.mx_wlinear_epilogue_fwd, x, mwq),
+                    (fos.wlinear_epilogue_fwd, x[:2], wq)):
+        r, rn = res[:f(a, w).shape[0]], nan_res[:f(a, w).shape[0]]
+        want = f(a, w, bias=bias, activation=act, residual=r)
+        got = f(a, w, bias=nan_bias, activation=act, residual=rn)
+        bad = rn.isnan()
+        bad[:, 5] = True
+        assert torch.equal(got.isnan(), bad) and torch.equal(got[~bad], want[~bad])
+    for w in (wq, mwq):
+        f = fos.wlinear_epilogue_fwd if w is wq else fos.mx_wlinear_epilogue_fwd
+        want, got = f(x, w, activation=act), f(nan_x, w, activation=act)
+        keep = torch.arange(m, device=DEV) != 2
+        assert got[2].isnan().all() and torch.equal(got[keep], want[keep])
+    z = res.clone()
+    want, got = fos.epilogue_bwd(res, z, act), fos.epilogue_bwd(res, nan_res, act)
+    there = nan_res.isnan()
+    assert torch.equal(got[~there], want[~there])
+    assert act in ("none", "relu") or got[there].isnan().all()      # their slopes do not take z's value
+    g = fos.epilogue_bwd(res[:, :32].contiguous(), nan_res, act, gated=True)
+    assert g[3, 39].isnan() and (act in ("none", "relu") or g[3, 7].isnan())
+    n = fos.rmsnorm_fwd(nan_x, torch.ones(k, dtype=BF16, device=DEV)).y
+    assert n[2].isnan().all() and not n[3:].isnan().any()
 
 
 # --------------------------------------------------------------------------- backward
