@@ -459,13 +459,17 @@ __device__ __forceinline__ void lds_products(LdsStage<TI, TJ>& st0, LdsStage<TI,
                                            blocks - 16 * chunk(i));
 }
 
+constexpr int waves_per_simd(int mfma_tiles, int split) {
+  return mfma_tiles == 16 ? 1 : split == 4 ? 4 : 2;
+}
+
 // Tile (64 TI) x (64 TJ), TI x TJ MFMA tiles to a wave.  4 x 4 fills a CU with one workgroup
-// (LDS and registers); of the smaller ones two run beside each other.  With kSplit = 2 two
-// groups of four waves share one tile, each with every other super-chunk: for so few tiles
-// that a CU has no second one.
+// (LDS and registers); of 2 x 2 two run beside each other.  With a split, kSplit groups of four
+// waves share one tile, each with every kSplit-th super-chunk: for so few tiles that a CU has
+// no second one.
 template <int TI, int TJ, int kEpi, bool kTail, int kSplit>
 __global__ __attribute__((amdgpu_flat_work_group_size(256 * kSplit, 256 * kSplit),
-                          amdgpu_waves_per_eu(TI * TJ == 16 ? 1 : 2, TI * TJ == 16 ? 1 : 2)))
+                          amdgpu_waves_per_eu(waves_per_simd(TI * TJ, kSplit), waves_per_simd(TI * TJ, kSplit))))
 void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restrict__ xs,
                         const float* __restrict__ xt, const uint8_t* __restrict__ wd,
                         const uint8_t* __restrict__ ws, const float* __restrict__ wt, int M,
@@ -531,44 +535,83 @@ void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restric
   } else {
     __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st2;
     __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st3;
-    // two branches, not two sets of pointers: the compiler has to know which stage a copy
-    // goes to, or it waits for it before the next read
+    // branches, not sets of pointers: the compiler has to know which stage a copy goes to, or
+    // it waits for it before the next read
     if (group == 0)
-      lds_products<TI, TJ, 2, kGate, true>(st0, st1, p, acc, ra, rb, h, wave, 0, nsc, blocks);
-    else
-      lds_products<TI, TJ, 2, kGate, true>(st2, st3, p, acc, ra, rb, h, wave, 1, nsc, blocks);
-    // each group gets the other's sums of half of the wave's rows, and finishes those
-    static_assert(TI == 2 && TJ * 256 * sizeof(f32x16) <= sizeof(LdsStage<TI, TJ>),
-                  "the sums take the stages' place");
-    const int at = 64 * wave + lane;
-    f32x16 half[1][TJ];
-    auto give = [&](LdsStage<TI, TJ>& to, int i) {
+      lds_products<TI, TJ, kSplit, kGate, true>(st0, st1, p, acc, ra, rb, h, wave, 0, nsc, blocks);
+    else if (group == 1)
+      lds_products<TI, TJ, kSplit, kGate, true>(st2, st3, p, acc, ra, rb, h, wave, 1, nsc, blocks);
+    if constexpr (kSplit == 4) {
+      __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st4;
+      __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st5;
+      __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st6;
+      __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st7;
+      if (group == 2)
+        lds_products<TI, TJ, 4, kGate, true>(st4, st5, p, acc, ra, rb, h, wave, 2, nsc, blocks);
+      else if (group == 3)
+        lds_products<TI, TJ, 4, kGate, true>(st6, st7, p, acc, ra, rb, h, wave, 3, nsc, blocks);
+      // a wave of the first group sums a tile of Y over the groups (with a gate: waves 0 and 1,
+      // of both projections, whose sums are the neighbouring waves')
+      static_assert(TI == 1 && TJ == 1 && 256 * sizeof(f32x16) <= sizeof(LdsStage<TI, TJ>),
+                    "the sums take the stages' place");
+      __syncthreads();   // every wave has read its operands
+      f32x4* to = reinterpret_cast<f32x4*>(group == 0 ? st0.a : group == 1 ? st2.a : group == 2 ? st4.a : st6.a);
 #pragma unroll
-      for (int n = 0; n < TJ; ++n)
+      for (int q = 0; q < 4; ++q)
+        to[256 * q + 64 * wave + lane] =
+            f32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+      __syncthreads();
+      if (group != 0 || wave >= 4 / kProj) return;
+      f32x16 sum[1][kProj];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          reinterpret_cast<f32x4*>(to.a)[(4 * n + q) * 256 + at] =
-              f32x4{acc[i][n][4 * q], acc[i][n][4 * q + 1], acc[i][n][4 * q + 2], acc[i][n][4 * q + 3]};
-    };
-    auto take = [&](const LdsStage<TI, TJ>& from, int i) {
-#pragma unroll
-      for (int n = 0; n < TJ; ++n)
+      for (int t = 0; t < kProj; ++t)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const f32x4 v = reinterpret_cast<const f32x4*>(from.a)[(4 * n + q) * 256 + at];
+          const int at = 256 * q + 64 * (kProj * wave + t) + lane;
+          f32x4 v = reinterpret_cast<const f32x4*>(st0.a)[at];
+          v += reinterpret_cast<const f32x4*>(st2.a)[at];
+          v += reinterpret_cast<const f32x4*>(st4.a)[at];
+          v += reinterpret_cast<const f32x4*>(st6.a)[at];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) half[0][n][4 * q + k] = acc[i][n][4 * q + k] + v[k];
+          for (int k = 0; k < 4; ++k) sum[0][t][4 * q + k] = v[k];
         }
-    };
-    __syncthreads();   // every wave has read its operands
-    if (group == 0) give(st0, 1);
-    else give(st1, 0);
-    __syncthreads();
-    if (group == 0) take(st1, 0);
-    else take(st0, 1);
-    store_fused<1, TJ, kGate>(e, y, M, N, tm * kBM + (wave >> 1) * (32 * TI) + 32 * group,
-                              (tn * kBN + (wave & 1) * (32 * TJ)) / kProj, lane, xt[0] * wt[0], half);
-    return;
+      store_fused<1, kProj, kGate>(e, y, M, N, tm * kBM + 32 * (kGate ? wave : wave >> 1),
+                                   kGate ? tn * 32 : tn * kBN + 32 * (wave & 1), lane, xt[0] * wt[0], sum);
+      return;
+    } else {
+      // each group gets the other's sums of half of the wave's rows, and finishes those
+      static_assert(TI == 2 && TJ * 256 * sizeof(f32x16) <= sizeof(LdsStage<TI, TJ>),
+                    "the sums take the stages' place");
+      const int at = 64 * wave + lane;
+      f32x16 half[1][TJ];
+      auto give = [&](LdsStage<TI, TJ>& to, int i) {
+#pragma unroll
+        for (int n = 0; n < TJ; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            reinterpret_cast<f32x4*>(to.a)[(4 * n + q) * 256 + at] =
+                f32x4{acc[i][n][4 * q], acc[i][n][4 * q + 1], acc[i][n][4 * q + 2], acc[i][n][4 * q + 3]};
+      };
+      auto take = [&](const LdsStage<TI, TJ>& from, int i) {
+#pragma unroll
+        for (int n = 0; n < TJ; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x4 v = reinterpret_cast<const f32x4*>(from.a)[(4 * n + q) * 256 + at];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) half[0][n][4 * q + k] = acc[i][n][4 * q + k] + v[k];
+          }
+      };
+      __syncthreads();   // every wave has read its operands
+      if (group == 0) give(st0, 1);
+      else give(st1, 0);
+      __syncthreads();
+      if (group == 0) take(st1, 0);
+      else take(st0, 1);
+      store_fused<1, TJ, kGate>(e, y, M, N, tm * kBM + (wave >> 1) * (32 * TI) + 32 * group,
+                                (tn * kBN + (wave & 1) * (32 * TJ)) / kProj, lane, xt[0] * wt[0], half);
+      return;
+    }
   }
 
   if constexpr (kEpi == kPlain) {
@@ -587,7 +630,7 @@ hipError_t launch_lds(const uint8_t* xd, const uint8_t* xs, const float* xt, con
   constexpr int kCols = 64 * TJ / (kEpi == kGated ? 2 : 1), kThreads = 256 * kSplit;
   const int tiles_m = (int)((M + 64 * TI - 1) / (64 * TI));
   const int tiles_n = (int)((N + kCols - 1) / kCols);
-  if constexpr (kEpi == kPlain || kSplit == 2)   // a split clears what is behind K anyway
+  if constexpr (kEpi == kPlain || kSplit > 1)   // a split clears what is behind K anyway
     qlinear_lds_kernel<TI, TJ, kEpi, false, kSplit><<<tiles_m * tiles_n, kThreads, 0, s>>>(
         xd, xs, xt, wd, ws, wt, (int)M, (int)N, (int)K, tiles_m, tiles_n, y, e);
   else if (K % kSuper == 0)
@@ -612,15 +655,19 @@ hipError_t launch_cfg(const uint8_t* xd, const uint8_t* xs, const float* xt, con
 }
 
 // Tile of an epilogue's product, by what a round of workgroups takes (us, measured with silu:
-// fixed, and per 4096 of K): 128 x 128, two workgroups to a CU or one (half a round, or all
+// fixed, and per 4096 of K): 64 x 64 with K split over four groups of waves, while every tile
+// has a CU of its own; 128 x 128, two workgroups to a CU or one (half a round, or all
 // that there is: then of eight waves that split K); 256 x 256, which converts a value for
-// twice as many products, where it fills the GPU (333 x 8198 x 4160: 39 us split, 40 not, 90
-// with 256 x 256; 2048 x 4096 x 4096: 69, 65 and 90; 4096 x 4096 x 4096: -, 125 and 110).
+// twice as many products, where it fills the GPU.  In this order: 16 x 4096 x 4096 14.6, 29.0,
+// 31.5 and 77 us; 256 x 4096 x 4096 16.9, 29.7, 31.9 and 77; 64 x 4096 x 512 7.5, 8.4, 8.9 and
+// 23; 333 x 8198 x 4160 -, 39, 40 and 90; 2048 x 4096 x 4096 -, 69, 65 and 90; 4096 x 4096 x
+// 4096 -, -, 125 and 110.
 struct QShape {
   int t, split, resident;
   float half, half_k, full, full_k;
 };
-constexpr QShape kQShapes[] = {{2, 2, 256, 4.5f, 27.0f, 4.5f, 27.0f},
+constexpr QShape kQShapes[] = {{1, 4, 256, 5.0f, 9.5f, 6.0f, 10.5f},
+                               {2, 2, 256, 4.5f, 27.0f, 4.5f, 27.0f},
                                {2, 1, 512, 4.0f, 33.0f, 3.0f, 60.0f},
                                {4, 1, 256, 15.5f, 84.0f, 15.5f, 84.0f}};
 int64_t tiles_of(const QLinearArgs& a, const QShape& h) {
@@ -634,7 +681,7 @@ const QShape& shape_of(const QLinearArgs& a) {
   for (const QShape& h : kQShapes) {
     const int64_t tiles = tiles_of(a, h), full = tiles / h.resident, rest = tiles % h.resident;
     // no second super-chunk to split, or more than one round
-    if (h.split == 2 && (a.K <= kSuper || tiles > h.resident)) continue;
+    if (h.split > 1 && (a.K <= kSuper || tiles > h.resident)) continue;
     float us = (float)full * (h.full + h.full_k * k);
     if (rest) us += 2 * rest <= h.resident ? h.half + h.half_k * k : h.full + h.full_k * k;
     if (!best || us < least) {
@@ -648,7 +695,7 @@ const QShape& shape_of(const QLinearArgs& a) {
 template <int kEpi>
 hipError_t launch_epi(const QLinearArgs& a, hipStream_t s) {
   const QShape& h = shape_of(a);
-  return (h.split == 2 ? launch_lds<2, 2, kEpi, 2> : h.t == 2 ? launch_lds<2, 2, kEpi> : launch_lds<4, 4, kEpi>)(
+  return (h.split == 4 ? launch_lds<1, 1, kEpi, 4> : h.split == 2 ? launch_lds<2, 2, kEpi, 2> : h.t == 2 ? launch_lds<2, 2, kEpi> : launch_lds<4, 4, kEpi>)(
       a.xd, a.xs, a.xt, a.wd, a.ws, a.wt, a.M, a.N, a.K, a.y, a.e, s);
 }
 

@@ -318,7 +318,10 @@ def test_mx_qlinear_epilogue_without_one_is_mx_qlinear(fos, m, n, k):
 @pytest.mark.parametrize("m,n,k,gated,fmt,act", [
     (4097, 2100, 512, False, "nvfp4", "gelu"), (4097, 1100, 320, True, "nvfp4", "silu"),
     (4097, 4400, 512, False, "mxfp4", "gelu_tanh"), (8300, 1100, 256, True, "mxfp4", "silu"),
-    (4097, 2099, 256, False, "nvfp4", "silu"), (4097, 4399, 512, False, "mxfp4", "silu")])
+    (4097, 2099, 256, False, "nvfp4", "silu"), (4097, 4399, 512, False, "mxfp4", "silu"),
+    # more tiles of 64 x 64 than there are CUs, fewer of 128 x 128: K split over two groups of waves
+    (600, 2000, 832, False, "nvfp4", "silu"), (600, 1100, 576, True, "nvfp4", "gelu"),
+    (2100, 2000, 192, False, "nvfp4", "gelu_tanh"), (2100, 1100, 256, True, "nvfp4", "relu")])
 def test_epilogue_of_many_tiles(fos, m, n, k, gated, fmt, act):
     """Against fp32 products of the dequantized records, whose own error the bound counts."""
     rows = 2 * n if gated else n
