@@ -1,7 +1,7 @@
 // Products of MXFP4 records with an epilogue: Y = act(deq(A) deq(B)^T + bias) + residual, or
 // gated, on the scaled FP4 matrix cores (v_mfma_scale_f32_32x32x64_f8f6f4, both operands
-// E2M1), which take the packed bytes and E8M0 scales as they are.  Sums are those of
-// fos_mx_qlinear_fwd, in its order.
+// E2M1), which take the packed bytes and E8M0 scales as they are.  Sums are taken in
+// the order of fos_mx_qlinear_fwd's, but for the tiles that split K.
 //
 // A workgroup has a (64 TI) x (64 TJ) tile, TI x TJ MFMA tiles to a wave.  K in stages
 // of 128 (64 bytes of nibbles a row), NS of them in LDS: four, or two where two workgroups of
@@ -141,16 +141,107 @@ __device__ __forceinline__ T& pick(T& a, T& b, T& c, T& d) {
   return d;
 }
 
-template <int TI, int TJ, int NS, int kEpi>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
-                          amdgpu_waves_per_eu(TI * TJ == 16 ? 1 : 2, TI * TJ == 16 ? 1 : 2)))
+// The products of this wave's tiles.  With kSplit > 1 a group of four waves has every
+// kSplit-th four stages, all groups as many: those past the last count with scales of 2^-127,
+// whose products are 0 in fp32.
+template <int TI, int TJ, int NS, bool kGate, int kSplit>
+__device__ __forceinline__ void flow_products(FlowStage<TI, TJ>& st0, FlowStage<TI, TJ>& st1,
+                                              FlowStage<TI, TJ>& st2, FlowStage<TI, TJ>& st3,
+                                              FlowScales<TI, TJ>& sc, const FlowOperands& p,
+                                              f32x16 (&acc)[TI][TJ], int ra, int rb, int h,
+                                              int wave, int stages, int group) {
+  static_assert(NS == 2 || NS == 4, "stages take turns within four");
+  constexpr int kMfmas = TI * TJ, kReads = TI + TJ, kCopies = TI + TJ;
+  // the stage behind the group's s-th
+  auto at = [&](int s) { return kSplit == 1 ? s : (s & ~3) * kSplit + 4 * group + (s & 3); };
+  // what is copied past the last stage is the last one again
+  auto load = [&](FlowStage<TI, TJ>& st, int s) {
+    flow_load<TI, TJ, kGate>(st, p, min(at(s), stages - 1), wave);
+  };
+  flow_load_scales(sc, p, at(0) / 4, wave);
+  load(st0, 0);
+  load(st1, 1);
+  if constexpr (NS == 4) {
+    load(st2, 2);
+    load(st3, 3);
+  }
+  flow_barrier<(NS - 1) * kCopies>();
+  uint4 sa[TI], sb[TJ];
+  i32x8 A[TI], B[TJ], An[TI], Bn[TJ];
+  flow_scales(sc.a, ra, sa);
+  flow_scales(sc.b, rb, sb);
+  flow_operands(st0.a, ra, h, A);
+  flow_operands(st0.b, rb, h, B);
+
+  // Stage S, the J-th of its four.  At its barrier the copies of the NS - 2 stages behind the
+  // next one may be on their way, and those of the scales until they are read (J = 3).
+#define FOS_FLOW_STAGE(S, J)                                                                        \
+  {                                                                                                 \
+    FlowStage<TI, TJ>& cur = pick<(J) % NS>(st0, st1, st2, st3);                                    \
+    FlowStage<TI, TJ>& next = pick<((J) + 1) % NS>(st0, st1, st2, st3);                             \
+    int xa[TI], xb[TJ];                                                                             \
+    _Pragma("unroll") for (int i = 0; i < TI; ++i) xa[i] = (int)(scale_word(sa[i], J) >> (8 * h));  \
+    _Pragma("unroll") for (int i = 0; i < TJ; ++i) xb[i] = (int)(scale_word(sb[i], J) >> (8 * h));  \
+    if (kSplit > 1 && at(S) >= stages) {                                                            \
+      _Pragma("unroll") for (int i = 0; i < TI; ++i) xa[i] = 0;                                     \
+      _Pragma("unroll") for (int i = 0; i < TJ; ++i) xb[i] = 0;                                     \
+    }                                                                                               \
+    flow_operands(cur.a, ra, 2 + h, An);                                                            \
+    flow_operands(cur.b, rb, 2 + h, Bn);                                                            \
+    flow_mma<0>(A, B, xa, xb, acc);                                                                 \
+    flow_schedule<kMfmas, kReads, 0>();                                                             \
+    flow_barrier<(NS - 2) * kCopies + ((J) >= 1 && (J) < NS && (J) < 3 ? 2 : 0)>();                 \
+    load(cur, (S) + NS);                                                                            \
+    if (J == 0) flow_load_scales(sc, p, at((S) + 4) / 4, wave);                                     \
+    if (J == 3) {                                                                                   \
+      flow_scales(sc.a, ra, sa);                                                                    \
+      flow_scales(sc.b, rb, sb);                                                                    \
+    }                                                                                               \
+    flow_operands(next.a, ra, h, A);                                                                \
+    flow_operands(next.b, rb, h, B);                                                                \
+    flow_mma<2>(An, Bn, xa, xb, acc);                                                               \
+    flow_schedule<kMfmas, kReads + (J == 3 ? kReads : 0), kCopies + (J == 0 ? 2 : 0)>();            \
+    __builtin_amdgcn_sched_barrier(0);                                                              \
+  }
+  if constexpr (kSplit > 1) {
+    for (int s = 0; s < (stages + 4 * kSplit - 1) / (4 * kSplit) * 4; s += 4) {
+      FOS_FLOW_STAGE(s, 0)
+      FOS_FLOW_STAGE(s + 1, 1)
+      FOS_FLOW_STAGE(s + 2, 2)
+      FOS_FLOW_STAGE(s + 3, 3)
+    }
+  } else {
+    int s = 0;
+    for (; s + 3 < stages; s += 4) {
+      FOS_FLOW_STAGE(s, 0)
+      FOS_FLOW_STAGE(s + 1, 1)
+      FOS_FLOW_STAGE(s + 2, 2)
+      FOS_FLOW_STAGE(s + 3, 3)
+    }
+    if (s < stages) {   // K % 256 == 0: two stages
+      FOS_FLOW_STAGE(s, 0)
+      FOS_FLOW_STAGE(s + 1, 1)
+    }
+  }
+#undef FOS_FLOW_STAGE
+}
+
+constexpr int flow_waves_per_simd(int mfma_tiles, int split) {
+  return mfma_tiles == 16 ? 1 : split == 4 ? 4 : 2;
+}
+
+// With kSplit = 4 four groups of four waves share a tile of 64 x 64, for so few tiles that
+// each has a CU of its own.
+template <int TI, int TJ, int NS, int kEpi, int kSplit>
+__global__ __attribute__((amdgpu_flat_work_group_size(256 * kSplit, 256 * kSplit),
+                          amdgpu_waves_per_eu(flow_waves_per_simd(TI * TJ, kSplit),
+                                              flow_waves_per_simd(TI * TJ, kSplit))))
 void mx_flow_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ as,
                     const uint8_t* __restrict__ bd, const uint8_t* __restrict__ bs, int M, int N,
                     int K, int tiles_m, int tiles_n, void* __restrict__ y, EpilogueArgs e) {
   constexpr bool kGate = kEpi == kGated;
   constexpr int kProj = kGate ? 2 : 1;   // weight rows of one column of Y
   constexpr int kBM = 64 * TI, kBN = 64 * TJ;
-  static_assert(NS == 2 || NS == 4, "stages take turns within four");
   // objects of their own: the compiler then knows that a copy to one does not touch another
   __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st0;
   __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st1;
@@ -160,13 +251,13 @@ void mx_flow_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
   const TileCoord tc = tile_of(blockIdx.x, tiles_m, tiles_n);
   const int tm = tc.tm, tn = tc.tn;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = kSplit == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) - 4 * group;
   const int lr = lane & 31, h = lane >> 5;
   const uint32_t kb2 = K / 2, kb32 = K / 32;
   const int ra = (wave >> 1) * (32 * TI) + lr;
   const int rb = (wave & 1) * (32 * TJ) + lr;
-  const int stages = K / kStageK, last = stages - 1;
-  constexpr int kMfmas = TI * TJ, kReads = TI + TJ, kCopies = TI + TJ;
+  const int stages = K / kStageK;
 
   FlowOperands p;
   p.a = __builtin_amdgcn_make_buffer_rsrc((void*)ad, 0, (int)((uint32_t)M * kb2), kRsrcWord3);
@@ -198,87 +289,70 @@ void mx_flow_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
 #pragma unroll
     for (int n = 0; n < TJ; ++n) acc[i][n] = f32x16{};
 
-  // what is copied past the last stage is the last one again, where nobody reads it
-  flow_load_scales(sc, p, 0, wave);
-  flow_load<TI, TJ, kGate>(st0, p, 0, wave);
-  flow_load<TI, TJ, kGate>(st1, p, min(1, last), wave);
-  if constexpr (NS == 4) {
-    flow_load<TI, TJ, kGate>(st2, p, min(2, last), wave);
-    flow_load<TI, TJ, kGate>(st3, p, min(3, last), wave);
+  if constexpr (kSplit == 1) {
+    flow_products<TI, TJ, NS, kGate, 1>(st0, st1, st2, st3, sc, p, acc, ra, rb, h, wave, stages, 0);
+    __builtin_amdgcn_s_waitcnt(0);   // no copy outlives the workgroup
+    store_fused<TI, TJ, kGate>(e, y, M, N, tm * kBM + (wave >> 1) * (32 * TI),
+                               (tn * kBN + (wave & 1) * (32 * TJ)) / kProj, lane, 1.0f, acc);
+  } else {
+    static_assert(kSplit == 4 && TI == 1 && TJ == 1 && NS == 4, "one tile to a wave, joined");
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st4;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st5;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st6;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st7;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st8;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st9;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st10;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st11;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st12;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st13;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st14;
+    __shared__ __attribute__((aligned(16))) FlowStage<TI, TJ> st15;
+    __shared__ __attribute__((aligned(16))) FlowScales<TI, TJ> sc1;
+    __shared__ __attribute__((aligned(16))) FlowScales<TI, TJ> sc2;
+    __shared__ __attribute__((aligned(16))) FlowScales<TI, TJ> sc3;
+    if (group == 0)
+      flow_products<TI, TJ, NS, kGate, 4>(st0, st1, st2, st3, sc, p, acc, ra, rb, h, wave, stages, 0);
+    else if (group == 1)
+      flow_products<TI, TJ, NS, kGate, 4>(st4, st5, st6, st7, sc1, p, acc, ra, rb, h, wave, stages, 1);
+    else if (group == 2)
+      flow_products<TI, TJ, NS, kGate, 4>(st8, st9, st10, st11, sc2, p, acc, ra, rb, h, wave, stages, 2);
+    else
+      flow_products<TI, TJ, NS, kGate, 4>(st12, st13, st14, st15, sc3, p, acc, ra, rb, h, wave, stages, 3);
+    __builtin_amdgcn_s_waitcnt(0);   // no copy is on its way to where the sums go
+    static_assert(kJoinBytes == 2 * sizeof(FlowStage<TI, TJ>), "the sums take two stages' place");
+    store_joined<kGate>(e, y, M, N, tm, tn, wave, group, lane, 1.0f, acc[0][0], [&](int g, int half) {
+      return g == 0 ? (half ? st1 : st0).a : g == 1 ? (half ? st5 : st4).a
+           : g == 2 ? (half ? st9 : st8).a : (half ? st13 : st12).a;
+    });
   }
-  flow_barrier<(NS - 1) * kCopies>();
-  uint4 sa[TI], sb[TJ];
-  i32x8 A[TI], B[TJ], An[TI], Bn[TJ];
-  flow_scales(sc.a, ra, sa);
-  flow_scales(sc.b, rb, sb);
-  flow_operands(st0.a, ra, h, A);
-  flow_operands(st0.b, rb, h, B);
-
-  // Stage S, the J-th of its four.  At its barrier the copies of the NS - 2 stages behind the
-  // next one may be on their way, and those of the scales until they are read (J = 3).
-#define FOS_FLOW_STAGE(S, J)                                                                        \
-  {                                                                                                 \
-    FlowStage<TI, TJ>& cur = pick<(J) % NS>(st0, st1, st2, st3);                                    \
-    FlowStage<TI, TJ>& next = pick<((J) + 1) % NS>(st0, st1, st2, st3);                             \
-    int xa[TI], xb[TJ];                                                                             \
-    _Pragma("unroll") for (int i = 0; i < TI; ++i) xa[i] = (int)(scale_word(sa[i], J) >> (8 * h));  \
-    _Pragma("unroll") for (int i = 0; i < TJ; ++i) xb[i] = (int)(scale_word(sb[i], J) >> (8 * h));  \
-    flow_operands(cur.a, ra, 2 + h, An);                                                            \
-    flow_operands(cur.b, rb, 2 + h, Bn);                                                            \
-    flow_mma<0>(A, B, xa, xb, acc);                                                                 \
-    flow_schedule<kMfmas, kReads, 0>();                                                             \
-    flow_barrier<(NS - 2) * kCopies + ((J) >= 1 && (J) < NS && (J) < 3 ? 2 : 0)>();                 \
-    flow_load<TI, TJ, kGate>(cur, p, min((S) + NS, last), wave);                                    \
-    if (J == 0) flow_load_scales(sc, p, ((S) + 4) / 4, wave);                                       \
-    if (J == 3) {                                                                                   \
-      flow_scales(sc.a, ra, sa);                                                                    \
-      flow_scales(sc.b, rb, sb);                                                                    \
-    }                                                                                               \
-    flow_operands(next.a, ra, h, A);                                                                \
-    flow_operands(next.b, rb, h, B);                                                                \
-    flow_mma<2>(An, Bn, xa, xb, acc);                                                               \
-    flow_schedule<kMfmas, kReads + (J == 3 ? kReads : 0), kCopies + (J == 0 ? 2 : 0)>();            \
-    __builtin_amdgcn_sched_barrier(0);                                                              \
-  }
-  int s = 0;
-  for (; s + 3 < stages; s += 4) {
-    FOS_FLOW_STAGE(s, 0)
-    FOS_FLOW_STAGE(s + 1, 1)
-    FOS_FLOW_STAGE(s + 2, 2)
-    FOS_FLOW_STAGE(s + 3, 3)
-  }
-  if (s < stages) {   // K % 256 == 0: two stages
-    FOS_FLOW_STAGE(s, 0)
-    FOS_FLOW_STAGE(s + 1, 1)
-  }
-#undef FOS_FLOW_STAGE
-  __builtin_amdgcn_s_waitcnt(0);   // no copy outlives the workgroup
-  store_fused<TI, TJ, kGate>(e, y, M, N, tm * kBM + (wave >> 1) * (32 * TI),
-                             (tn * kBN + (wave & 1) * (32 * TJ)) / kProj, lane, 1.0f, acc);
 }
 
-template <int TI, int TJ, int NS, int kEpi>
+template <int TI, int TJ, int NS, int kEpi, int kSplit = 1>
 hipError_t launch_flow(const QLinearArgs& a, hipStream_t s) {
   constexpr int kCols = 64 * TJ / (kEpi == kGated ? 2 : 1);
   const int tiles_m = (int)((a.M + 64 * TI - 1) / (64 * TI));
   const int tiles_n = (int)((a.N + kCols - 1) / kCols);
-  mx_flow_kernel<TI, TJ, NS, kEpi><<<tiles_m * tiles_n, 256, 0, s>>>(
+  mx_flow_kernel<TI, TJ, NS, kEpi, kSplit><<<tiles_m * tiles_n, 256 * kSplit, 0, s>>>(
       a.xd, a.xs, a.wd, a.ws, (int)a.M, (int)a.N, (int)a.K, tiles_m, tiles_n, a.y, a.e);
   return hipGetLastError();
 }
 
 // Kernel of an epilogue's product, by what a round of workgroups takes (us, measured with
-// silu: fixed, and per 4096 of K): 128 x 128 tiles, two to a CU or (half a round) one, while
+// silu: fixed, and per 4096 of K): 64 x 64 tiles with K split over four groups of waves, while
+// every tile has a CU of its own; 128 x 128 tiles, two to a CU or (half a round) one, while
 // there are few; 256 x 128, whose epilogues run beside another workgroup's products, for a
-// short K; 256 x 256, which copies least for its products, for a long one (8192 x 8192 x 1024: 72,
-// 67 and 86 us; x 4096: 226, 183 and 175; 512 x 4096 x 4096: 14, 19 and 34).
+// short K; 256 x 256, which copies least for its products, for a long one.  In this order:
+// 16 x 4096 x 4096 8.9, 11.0, - and 17; 64 x 4096 x 12288 18, 23, - and 37; 1024 x 4096 x 4096
+// -, 19, 24 and 36; 8192 x 8192 x 1024 -, 70, 64 and 86; 4096 x 4096 x 12288 -, 155, 126 and 108.
 struct MxShape {
-  int ti, tj, resident;
+  int ti, tj, split, resident;
   float half, half_k, full, full_k;
 };
-constexpr MxShape kMxShapes[] = {{2, 2, 512, 3.3f, 10.2f, 3.0f, 26.0f},
-                                 {4, 2, 512, 5.0f, 18.0f, 7.0f, 38.9f},
-                                 {4, 4, 256, 14.0f, 29.7f, 14.0f, 29.7f}};
+constexpr MxShape kMxShapes[] = {{1, 1, 4, 256, 5.5f, 4.8f, 6.0f, 5.6f},
+                                 {2, 2, 1, 512, 6.0f, 12.4f, 5.0f, 24.0f},
+                                 {4, 2, 1, 512, 8.0f, 21.0f, 7.0f, 38.5f},
+                                 {4, 4, 1, 256, 14.0f, 29.7f, 14.0f, 29.7f}};
 int64_t mx_tiles(const QLinearArgs& a, const MxShape& h) {
   const int64_t cols = a.gated ? 32 * h.tj : 64 * h.tj;
   return ((a.M + 64 * h.ti - 1) / (64 * h.ti)) * ((a.N + cols - 1) / cols);
@@ -289,6 +363,8 @@ const MxShape& mx_shape(const QLinearArgs& a) {
   const float k = (float)a.K / 4096.0f;
   for (const MxShape& h : kMxShapes) {
     const int64_t tiles = mx_tiles(a, h), full = tiles / h.resident, rest = tiles % h.resident;
+    // no second four stages to split, or more than one round
+    if (h.split > 1 && (a.K <= 4 * kStageK || tiles > h.resident)) continue;
     float us = (float)full * (h.full + h.full_k * k);
     if (rest) us += 2 * rest <= h.resident ? h.half + h.half_k * k : h.full + h.full_k * k;
     if (!best || us < least) {
@@ -302,6 +378,7 @@ const MxShape& mx_shape(const QLinearArgs& a) {
 template <int kEpi>
 hipError_t launch_mx_epi(const QLinearArgs& a, hipStream_t s) {
   const MxShape& h = mx_shape(a);
+  if (h.split == 4) return launch_flow<1, 1, 4, kEpi, 4>(a, s);
   if (h.tj == 4) return launch_flow<4, 4, 4, kEpi>(a, s);
   if (h.ti == 4) return launch_flow<4, 2, 2, kEpi>(a, s);
   return launch_flow<2, 2, 4, kEpi>(a, s);

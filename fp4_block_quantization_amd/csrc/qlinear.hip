@@ -80,7 +80,6 @@ struct Operands {
 };
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint4 ld16(__amdgpu_buffer_rsrc_t r, uint32_t off, int soff) {
   const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0);
@@ -550,33 +549,12 @@ void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restric
         lds_products<TI, TJ, 4, kGate, true>(st4, st5, p, acc, ra, rb, h, wave, 2, nsc, blocks);
       else if (group == 3)
         lds_products<TI, TJ, 4, kGate, true>(st6, st7, p, acc, ra, rb, h, wave, 3, nsc, blocks);
-      // a wave of the first group sums a tile of Y over the groups (with a gate: waves 0 and 1,
-      // of both projections, whose sums are the neighbouring waves')
-      static_assert(TI == 1 && TJ == 1 && 256 * sizeof(f32x16) <= sizeof(LdsStage<TI, TJ>),
+      static_assert(TI == 1 && TJ == 1 && kJoinBytes <= sizeof(LdsStage<TI, TJ>),
                     "the sums take the stages' place");
-      __syncthreads();   // every wave has read its operands
-      f32x4* to = reinterpret_cast<f32x4*>(group == 0 ? st0.a : group == 1 ? st2.a : group == 2 ? st4.a : st6.a);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        to[256 * q + 64 * wave + lane] =
-            f32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
-      __syncthreads();
-      if (group != 0 || wave >= 4 / kProj) return;
-      f32x16 sum[1][kProj];
-#pragma unroll
-      for (int t = 0; t < kProj; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int at = 256 * q + 64 * (kProj * wave + t) + lane;
-          f32x4 v = reinterpret_cast<const f32x4*>(st0.a)[at];
-          v += reinterpret_cast<const f32x4*>(st2.a)[at];
-          v += reinterpret_cast<const f32x4*>(st4.a)[at];
-          v += reinterpret_cast<const f32x4*>(st6.a)[at];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sum[0][t][4 * q + k] = v[k];
-        }
-      store_fused<1, kProj, kGate>(e, y, M, N, tm * kBM + 32 * (kGate ? wave : wave >> 1),
-                                   kGate ? tn * 32 : tn * kBN + 32 * (wave & 1), lane, xt[0] * wt[0], sum);
+      store_joined<kGate>(e, y, M, N, tm, tn, wave, group, lane, xt[0] * wt[0], acc[0][0],
+                          [&](int g, int half) {
+                            return (g == 0 ? st0 : g == 1 ? st2 : g == 2 ? st4 : st6).a + half * kJoinBytes / 2;
+                          });
       return;
     } else {
       // each group gets the other's sums of half of the wave's rows, and finishes those
