@@ -70,8 +70,8 @@ __device__ __forceinline__ float activate(int act, float z) {
 }
 
 // Value and slope.  s(u) and s(-u) come from e^-|u|, which does not overflow; z^2 is taken
-// of a z within +-10^6 (there the slope is 0 or 1).  fminf and fmaxf would make a number of a
-// NaN: the value has it from z, and the slope where it depends on z.
+// of a z within +-10^6 (there the slope is 0 or 1).  fminf and fmaxf make a number of a
+// NaN, which value and slope then have from z itself.
 template <int kAct>
 __device__ __forceinline__ void activate_slope(float z, float& f, float& df) {
   if constexpr (kAct == kActNone) {
@@ -87,9 +87,9 @@ __device__ __forceinline__ void activate_slope(float z, float& f, float& df) {
     f = z * p;
     df = __builtin_fmaf(fminf(fmaxf(z, -1e6f), 1e6f), e * 0.39894228f, p);   // z / sqrt(2 pi) e^..
   } else {
-    const float zc = z > 1e6f ? 1e6f : z < -1e6f ? -1e6f : z;
+    const float zc = fminf(fmaxf(z, -1e6f), 1e6f);
     const float z2 = zc * zc;
-    const float u = kAct == kActSilu ? zc : zc * __builtin_fmaf(z2, kTanhC * kTanhCubic, kTanhC);
+    const float u = kAct == kActSilu ? z : z * __builtin_fmaf(z2, kTanhC * kTanhCubic, kTanhC);
     const float du = kAct == kActSilu ? 1.0f : __builtin_fmaf(z2, 3.0f * kTanhC * kTanhCubic, kTanhC);
     const float e = fast_exp2(fabsf(u) * -kLog2e), r = fast_rcp(1.0f + e), er = e * r;
     const float p = u < 0.0f ? er : r;
