@@ -876,6 +876,7 @@ def paged_decode(q: torch.Tensor, cache: PagedKVCache, block_table: torch.Tensor
 _ACTIVATIONS = {"none": FOS_ACT_NONE, "relu": FOS_ACT_RELU, "gelu": FOS_ACT_GELU,
                 "gelu_tanh": FOS_ACT_GELU_TANH, "silu": FOS_ACT_SILU}
 _SCALE_WORKSPACE = int(_lib.fos_quantize_workspace_bytes())
+_EPILOGUE_SIZE = ctypes.sizeof(FosEpilogue)
 _RECORDS = {"bf16": FOS_RECORD_NONE, "nvfp4": FOS_RECORD_NVFP4, "mxfp4": FOS_RECORD_MXFP4}
 
 
@@ -1043,35 +1044,41 @@ def _epilogue(M: int, W: int, gated: bool, like: torch.Tensor, dev: int, bias, a
         if residual is not None:
             _no_overlap(out, residual, "the residual's in part")
     preact = like.new_empty(M, W, dtype=_BF16) if return_preact else None
-    e = FosEpilogue(ctypes.sizeof(FosEpilogue), act, int(gated), _OUT_CODE[out_dtype],
-                    _address(bias), _address(residual), stride, _address(preact), 0)
+    e = FosEpilogue(_EPILOGUE_SIZE, act, gated, _OUT_CODE[out_dtype],
+                    None if bias is None else bias.data_ptr(),
+                    None if residual is None else residual.data_ptr(), stride,
+                    None if preact is None else preact.data_ptr(), 0)
     return N, e, out, preact
 
 
-def _check_kind(q, block: int) -> None:
+def _check_record_of(q, block: int):
+    """(device, rows, values of a row) of a record of the block length's format.  One condition
+    and few calls: the checks of both records were 2 of a small product's 9 us on the host."""
     if not isinstance(q, NVFP4Tensor if block == 16 else MXFP4Tensor):
         raise ValueError(f"an {'NVFP4' if block == 16 else 'MXFP4'} record is needed here")
+    data, scales = q.data, q.scales
+    shape, dev = data.shape, data.get_device()
+    if len(shape) != 2 or dev < 0:
+        raise ValueError("record data must be 2-D CUDA tensors")
+    rows, half = shape
+    if (data.dtype != _U8 or scales.dtype != _U8 or scales.shape != (rows, 2 * half // block)
+            or scales.get_device() != dev or not data.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError(f"a record [{rows}, {2 * half}] needs contiguous uint8 data [{rows}, {half}] and "
+                         f"scales [{rows}, {2 * half // block}] on one device")
+    if block == 16:
+        t = q.tensor_scale
+        if t.numel() != 1 or t.dtype != _F32 or t.get_device() != dev:
+            raise ValueError("tensor_scale must be a one-element fp32 tensor on the record's device")
+    return dev, rows, 2 * half
 
 
 def _check_product_records(xq, wq, block: int):
     """(device, M, W, K) of two records blocked along K."""
-    _check_kind(xq, block)
-    _check_kind(wq, block)
-    xd, wd = xq.data, wq.data
-    dev = xd.get_device()
-    if dev < 0 or xd.dim() != 2 or wd.dim() != 2:
-        raise ValueError("record data must be 2-D CUDA tensors")
-    M, half = xd.shape
-    W, half2 = wd.shape
-    if half != half2:
-        raise ValueError("inner dimensions differ")
-    for r, rows in ((xq, M), (wq, W)):
-        _whole(r.data, (rows, half), _U8, dev, "record data")
-        _whole(r.scales, (rows, 2 * half // block), _U8, dev, "record scales")
-        if block == 16 and (r.tensor_scale.numel() != 1 or r.tensor_scale.dtype != _F32
-                            or r.tensor_scale.get_device() != dev):
-            raise ValueError("tensor_scale must be a one-element fp32 tensor on the record's device")
-    return dev, M, W, 2 * half
+    dev, M, K = _check_record_of(xq, block)
+    dev2, W, K2 = _check_record_of(wq, block)
+    if K != K2 or dev != dev2:
+        raise ValueError("the records' inner dimensions or devices differ")
+    return dev, M, W, K
 
 
 def _qlinear_epilogue(xq, wq, gated, bias, activation, residual, out_dtype, return_preact, out):
@@ -1134,31 +1141,23 @@ def mx_qglu_fwd(aq: MXFP4Tensor, bq: MXFP4Tensor, activation: str = "silu",
 
 
 def _wlinear_epilogue(x, wq, block, gated, bias, activation, residual, out_dtype, return_preact, out):
-    _check_kind(wq, block)
-    data, scales = wq.data, wq.scales
-    dev = data.get_device()
-    if dev < 0 or data.dim() != 2 or x.dim() != 2:
-        raise ValueError("x and the record's data must be 2-D CUDA tensors")
-    W, half = data.shape
-    M, K = x.shape[0], 2 * half
+    dev, W, K = _check_record_of(wq, block)
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D CUDA tensor")
+    M = x.shape[0]
     stride = _rows_of(x, M, K, dev, "x")
-    _whole(data, (W, half), _U8, dev, "record data")
-    _whole(scales, (W, K // block), _U8, dev, "record scales")
     N, e, y, z = _epilogue(M, W, gated, x, dev, bias, activation, residual, out_dtype,
                            return_preact, out)
     if out is not None:
         _no_overlap(out, x, "x's", whole=False)
     if block == 16:
-        t = wq.tensor_scale
         if wq.hadamard_seed is not None:
             raise ValueError("the weight record carries a Hadamard transform that x does not")
-        if t.numel() != 1 or t.dtype != _F32 or t.get_device() != dev:
-            raise ValueError("tensor_scale must be a one-element fp32 tensor on x's device")
-        _call(dev, "fos_wlinear_epilogue_fwd", x.data_ptr(), stride, data.data_ptr(),
-              scales.data_ptr(), t.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
+        _call(dev, "fos_wlinear_epilogue_fwd", x.data_ptr(), stride, wq.data.data_ptr(),
+              wq.scales.data_ptr(), wq.tensor_scale.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
     else:
-        _call(dev, "fos_mx_wlinear_epilogue_fwd", x.data_ptr(), stride, data.data_ptr(),
-              scales.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
+        _call(dev, "fos_mx_wlinear_epilogue_fwd", x.data_ptr(), stride, wq.data.data_ptr(),
+              wq.scales.data_ptr(), M, N, K, ctypes.byref(e), y.data_ptr())
     return (y, z) if return_preact else y
 
 
