@@ -15,8 +15,11 @@ namespace fos {
 namespace {
 
 // Rows of one group: few enough for about 2048 workgroups, 16 at least, so that the partial
-// sums are little beside dZ (one fp32 for 16 bf16 values or more).
+// sums are little beside dZ (one fp32 for 16 bf16 values or more).  Up to 32 rows are one
+// group, whose sums are dbias itself: no second launch, if there is no tensor scale to join
+// (16 x 4096: 4.0 us, 5.9 with two launches; 32 x 12288: 5.8 and 6.1).
 int rows_of_group(int64_t M, int64_t N) {
+  if (M <= 32) return 32;
   const int64_t strips = (N + 511) / 512;
   int64_t rows = (M * strips + 2047) / 2048;
   rows = (rows + 15) / 16 * 16;
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(256) void epilogue_bwd_kernel(EpilogueBwdArgs a, in
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) v += sums[w][h][c * 64 + lane];
-    a.partials[(int64_t)group * width + h * a.N + n + c] = v;
+    (gridDim.x == strips ? a.dbias : a.partials)[(int64_t)group * width + h * a.N + n + c] = v;
   }
 }
 
@@ -187,7 +190,8 @@ hipError_t launch_epilogue_bwd(const EpilogueBwdArgs& a, hipStream_t s) {
   }
   if (a.M == 0 && !a.dbias && !a.t) return hipSuccess;
   const int64_t width = a.gated ? 2 * a.N : a.N;
-  const int64_t join = (a.dbias ? (width + 63) / 64 : 0) + (a.t ? 1 : 0);
+  const bool sums = a.dbias && groups != 1;   // of no rows: zeros
+  const int64_t join = (sums ? (width + 63) / 64 : 0) + (a.t ? 1 : 0);
   if (join)
     epilogue_join_kernel<<<join, 256, 0, s>>>(a.partials, groups, width,
                                               (int)(wide(a) ? grid8 : grid1), a.dbias, a.t);

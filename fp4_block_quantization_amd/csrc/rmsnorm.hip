@@ -465,10 +465,13 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s) {
 }
 
 // Workgroups of the backward pass, each with a partial dw: what runs at once (two waves to a
-// SIMD), but at least four rounds of rows to each, down to one workgroup to a CU.
+// SIMD), but at least four rounds of rows to each, down to one workgroup to a CU.  Up to two
+// rounds are one workgroup, whose sums are dw itself: no second launch (2 x 4096: 4.7 us, 6.0 with
+// two launches; four rounds of 64 x 512 9.5 and 6.8).
 int norm_bwd_partials(int64_t M, int K) {
   const int lanes = bwd_lanes_of(M, K), rows = lanes > 256 ? 1 : 256 / lanes;
   const int64_t groups = (M + rows - 1) / rows, most = lanes > 256 ? 256 : 512;
+  if (groups <= 2) return 1;
   const int64_t want = groups / 4 < 256 ? 256 : groups / 4 < most ? groups / 4 : most;
   return (int)(groups < want ? groups : want);
 }
