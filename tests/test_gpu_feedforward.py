@@ -62,7 +62,7 @@ def bits(t):
 
 NORM_SHAPES = [(1, 16), (3, 32), (5, 48), (1, 4096), (17, 512), (40, 528), (64, 1040), (1030, 1024),
                (1100, 2080), (1025, 4096), (9, 4112), (7, 8192), (3, 16384), (2, 16400), (2, 32768), (1027, 2064),
-               (2500, 96), (9000, 64)]
+               (2500, 96), (9000, 64), (4, 4096), (3, 2064), (2, 1040), (5, 1040), (16, 512)]
 
 
 def norm_inputs(m, k, seed, residual):
@@ -172,7 +172,7 @@ def test_norm_extreme_rows(fos, fmt):
         assert_same_bytes(o.record.data.cpu().numpy(), MX.quantize(bits(y))["data"], "data")
 
 
-@pytest.mark.parametrize("m,k", [(5, 96), (2, 4096), (1200, 4096), (3, 16384), (2, 32768)])
+@pytest.mark.parametrize("m,k", [(5, 96), (2, 4096), (1200, 4096), (3, 16384), (2, 32768), (17, 512), (6, 4096)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_norm_of_values_that_are_not_finite(fos, m, k, bad):
     """One such value makes its row NaN; the records are those of y, whatever it holds."""
