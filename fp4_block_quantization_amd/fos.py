@@ -1194,7 +1194,8 @@ def mx_wglu_fwd(x: torch.Tensor, wq: MXFP4Tensor, activation: str = "silu",
     return _wlinear_epilogue(x, wq, 32, True, bias, activation, None, out_dtype, return_preact, out)
 
 
-def _epilogue_bwd(dy, preact, activation, gated, need_dbias, need_scale):
+def _check_epilogue_bwd(dy, preact, activation, gated):
+    """(device, M, N, columns of preact, activation code) of an epilogue's backward pass."""
     act = _activation(activation)
     if dy.dim() != 2 or dy.get_device() < 0:
         raise ValueError("dy must be a contiguous 2-D bfloat16 CUDA tensor")
@@ -1202,15 +1203,7 @@ def _epilogue_bwd(dy, preact, activation, gated, need_dbias, need_scale):
     dev, W = dy.get_device(), 2 * N if gated else N
     _whole(dy, (M, N), _BF16, dev, "dy")
     _whole(preact, (M, W), _BF16, dev, "preact")
-    dz = dy.new_empty(M, W)
-    dbias = dy.new_empty(W, dtype=_F32) if need_dbias else None
-    t = dy.new_empty(1, dtype=_F32) if need_scale else None
-    ws = None
-    if need_dbias or need_scale:
-        ws = dy.new_empty(int(_lib.fos_epilogue_bwd_workspace_bytes(M, N, int(gated))), dtype=_U8)
-    _call(dev, "fos_epilogue_bwd", dy.data_ptr(), preact.data_ptr(), M, N, act, int(gated),
-          dz.data_ptr(), _address(dbias), _address(t), _address(ws), 0 if ws is None else ws.numel())
-    return dz, dbias, t
+    return dev, M, N, W, act
 
 
 def epilogue_bwd(dy: torch.Tensor, preact: torch.Tensor, activation: str = "none",
@@ -1220,7 +1213,15 @@ def epilogue_bwd(dy: torch.Tensor, preact: torch.Tensor, activation: str = "none
     pre-activation ([M, N], of a gated block [M, 2N]).  Returns dZ, with ``return_dbias`` also
     its column sums (fp32), with ``return_tensor_scale`` also the NVFP4 tensor scale of dZ
     (fp32 [1]).  The residual's gradient is dY itself."""
-    dz, dbias, t = _epilogue_bwd(dy, preact, activation, gated, return_dbias, return_tensor_scale)
+    dev, M, N, W, act = _check_epilogue_bwd(dy, preact, activation, gated)
+    dz = dy.new_empty(M, W)
+    dbias = dy.new_empty(W, dtype=_F32) if return_dbias else None
+    t = dy.new_empty(1, dtype=_F32) if return_tensor_scale else None
+    ws = None
+    if return_dbias or return_tensor_scale:
+        ws = dy.new_empty(int(_lib.fos_epilogue_bwd_workspace_bytes(M, N, int(gated))), dtype=_U8)
+    _call(dev, "fos_epilogue_bwd", dy.data_ptr(), preact.data_ptr(), M, N, act, int(gated),
+          dz.data_ptr(), _address(dbias), _address(t), _address(ws), 0 if ws is None else ws.numel())
     got = (dz,) + ((dbias,) if return_dbias else ()) + ((t,) if return_tensor_scale else ())
     return got if len(got) > 1 else dz
 
@@ -1231,19 +1232,42 @@ def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, roundi
         raise ValueError("nothing to compute")
     outputs = (("row",) if need_dx else ()) + (("col",) if need_dw else ())
     cfg = make_config(rounding=rounding, outputs=outputs, sr_seed=sr_seed)
-    dz, dbias, t = _epilogue_bwd(dy, preact, activation, gated, return_dbias, True)
-    (M, W), dev = dz.shape, dz.get_device()
-    record = lambda r, c: NVFP4Tensor(dz.new_empty(r, c // 2, dtype=_U8), dz.new_empty(r, c // 16, dtype=_U8), t)
-    rows = record(M, W) if need_dx else None
-    cols = record(W, M) if need_dw else None
-    _call(dev, "fos_quantize_scaled", ctypes.byref(cfg), dz.data_ptr(), M, W, t.data_ptr(),
-          *((rows.data.data_ptr(), rows.scales.data_ptr()) if need_dx else (None, None)),
-          *((cols.data.data_ptr(), cols.scales.data_ptr()) if need_dw else (None, None)))
+    dev, M, N, W, act = _check_epilogue_bwd(dy, preact, activation, gated)
+    for q, inner in ([(wq_t, W)] if need_dx else []) + ([(xq_t, M)] if need_dw else []):
+        where, _, cols = _check_record_of(q, 16)
+        if where != dev or cols != inner or q.hadamard_seed is not None:
+            raise ValueError("xq_t and wq_t must be the column-wise records of X and W, without a "
+                             "Hadamard transform")
+    # dZ, its tensor scale and records and the workspace in one allocation (one each of ten
+    # took 12 of a small call's 44 us on the host)
+    sizes = [2 * M * W, 4, int(_lib.fos_epilogue_bwd_workspace_bytes(M, N, int(gated)))]
+    for wanted in (need_dx, need_dw):
+        sizes += [M * W // 2, M * W // 16] if wanted else [0, 0]
+    at = [0]
+    for n in sizes:
+        at.append(at[-1] + (n + 255) // 256 * 256)
+    scratch = dy.new_empty(at[-1], dtype=_U8)
+    base = scratch.data_ptr()
+    dz, t, ws, rows, row_scales, cols, col_scales = (base + a for a in at[:-1])
+    dbias = dy.new_empty(W, dtype=_F32) if return_dbias else None
+    _call(dev, "fos_epilogue_bwd", dy.data_ptr(), preact.data_ptr(), M, N, act, int(gated), dz,
+          _address(dbias), t, ws, sizes[2])
+    _call(dev, "fos_quantize_scaled", ctypes.byref(cfg), dz, M, W, t,
+          *((rows, row_scales) if need_dx else (None, None)),
+          *((cols, col_scales) if need_dw else (None, None)))
     # the products of fos_qlinear_bwd, on the tiles that suit their shapes (dX of 2048 x 4096
     # with an inner dimension of 8192 has 128 tiles of 256 x 256, half a GPU)
-    product = lambda a, b: _qlinear_epilogue(a, b, False, None, "none", None, _BF16, False, None)
-    dx = product(rows, wq_t) if need_dx else None
-    dw = product(cols, xq_t) if need_dw else None
+    plain = FosEpilogue(_EPILOGUE_SIZE, FOS_ACT_NONE, 0, FOS_OUT_BF16, None, None, 0, None, 0)
+    product = lambda data, scales, m, k, q, out: _call(
+        dev, "fos_qlinear_epilogue_fwd", data, scales, t, q.data.data_ptr(), q.scales.data_ptr(),
+        q.tensor_scale.data_ptr(), m, out.shape[1], k, ctypes.byref(plain), out.data_ptr())
+    dx = dw = None
+    if need_dx:
+        dx = dy.new_empty(M, wq_t.data.shape[0])
+        product(rows, row_scales, M, W, wq_t, dx)
+    if need_dw:
+        dw = dy.new_empty(W, xq_t.data.shape[0])
+        product(cols, col_scales, W, M, xq_t, dw)
     return (dx, dw, dbias) if return_dbias else (dx, dw)
 
 

@@ -628,7 +628,12 @@ def test_binding_refuses_what_the_library_could_not_address(fos):
         lambda: fos.wlinear_epilogue_fwd(x.repeat(1, 2)[:, :64].T, rec),
         lambda: fos.epilogue_bwd(y, y[:8]), lambda: fos.epilogue_bwd(y, y, gated=True),
         lambda: fos.epilogue_bwd(y.float(), y), lambda: fos.epilogue_bwd(y[:, :16], y[:, :16].contiguous()),
-        lambda: fos.qlinear_epilogue_bwd(y, y, None, None, need_dx=False, need_dw=False)]
+        lambda: fos.qlinear_epilogue_bwd(y, y, None, None, need_dx=False, need_dw=False),
+        lambda: fos.qlinear_epilogue_bwd(y, y, None, rec), lambda: fos.qlinear_epilogue_bwd(y, y, rec, mx),
+        lambda: fos.qlinear_epilogue_bwd(y, y, None, rec, need_dw=False),
+        lambda: fos.qlinear_epilogue_bwd(y, y, rec, None, need_dx=False),
+        lambda: fos.qglu_bwd(y, y, None, rec, need_dw=False),
+        lambda: fos.qglu_bwd(torch.cat((y, y), 1)[:, :32].contiguous(), torch.cat((y, y), 1), None, turned, need_dw=False)]
     for i, call in enumerate(calls):
         with pytest.raises(ValueError):
             call()
