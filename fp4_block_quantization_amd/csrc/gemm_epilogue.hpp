@@ -182,15 +182,15 @@ __device__ __forceinline__ void store_fused(const EpilogueArgs& e, void* y, int 
 }
 
 // The epilogue of a 64 x 64 tile whose K is split over four groups of four waves, each wave
-// with one 32x32 tile of its group's sums.  place(g, half): 16-byte aligned LDS for half of the
+// with one 32x32 tile of its group's sums (2 x 2, `at` counts them).  place(g, half): 16-byte aligned LDS for half of the
 // kJoinBytes of group g's, which may hold operands that a wave still reads.  A wave of the first group sums a tile of
 // Y in the groups' order (with a gate: waves 0 and 1, both projections, whose sums are two
 // neighbouring waves').
 constexpr int kJoinBytes = 256 * sizeof(f32x16);
 template <bool kGate, typename Place>
 __device__ __forceinline__ void store_joined(const EpilogueArgs& e, void* y, int M, int N, int tm,
-                                             int tn, int wave, int group, int lane, float s,
-                                             const f32x16& acc, Place place) {
+                                             int tn, int wave, int at, int group, int lane,
+                                             float s, const f32x16& acc, Place place) {
   constexpr int kProj = kGate ? 2 : 1;
   auto quarter = [&](int g, int q) {   // values 4q .. 4q + 3 of every lane
     return reinterpret_cast<f32x4*>(place(g, q >> 1)) + 256 * (q & 1);
@@ -198,7 +198,7 @@ __device__ __forceinline__ void store_joined(const EpilogueArgs& e, void* y, int
   __syncthreads();   // every wave has read its operands
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    quarter(group, q)[64 * wave + lane] = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    quarter(group, q)[64 * at + lane] = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
   __syncthreads();
   if (group != 0 || wave >= 4 / kProj) return;
   f32x16 sum[1][kProj];
@@ -206,10 +206,10 @@ __device__ __forceinline__ void store_joined(const EpilogueArgs& e, void* y, int
   for (int t = 0; t < kProj; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int at = 64 * (kProj * wave + t) + lane;
-      f32x4 v = quarter(0, q)[at];
+      const int l = 64 * (kProj * wave + t) + lane;
+      f32x4 v = quarter(0, q)[l];
 #pragma unroll
-      for (int g = 1; g < 4; ++g) v += quarter(g, q)[at];
+      for (int g = 1; g < 4; ++g) v += quarter(g, q)[l];
 #pragma unroll
       for (int k = 0; k < 4; ++k) sum[0][t][4 * q + k] = v[k];
     }

@@ -321,7 +321,7 @@ void mx_flow_kernel(const uint8_t* __restrict__ ad, const uint8_t* __restrict__ 
       flow_products<TI, TJ, NS, kGate, 4>(st12, st13, st14, st15, sc3, p, acc, ra, rb, h, wave, stages, 3);
     __builtin_amdgcn_s_waitcnt(0);   // no copy is on its way to where the sums go
     static_assert(kJoinBytes == 2 * sizeof(FlowStage<TI, TJ>), "the sums take two stages' place");
-    store_joined<kGate>(e, y, M, N, tm, tn, wave, group, lane, 1.0f, acc[0][0], [&](int g, int half) {
+    store_joined<kGate>(e, y, M, N, tm, tn, wave, wave, group, lane, 1.0f, acc[0][0], [&](int g, int half) {
       return g == 0 ? (half ? st1 : st0).a : g == 1 ? (half ? st5 : st4).a
            : g == 2 ? (half ? st9 : st8).a : (half ? st13 : st12).a;
     });

@@ -428,11 +428,12 @@ __device__ __forceinline__ void stage_mma(const LdsStage<TI, TJ>& st, f32x16 (&a
 // (so every wave's copies have landed and the other stage is no longer read), then
 // multiply while copying the next super-chunk into the other stage.  A single-exit
 // loop keeps the 256 accumulator registers in place.
+// With `idle` (a wave whose rows or columns are all outside of Y) it copies only.
 template <int TI, int TJ, int kSplit, bool kGate, bool kTail>
 __device__ __forceinline__ void lds_products(LdsStage<TI, TJ>& st0, LdsStage<TI, TJ>& st1,
                                              const LdsOperands& p, f32x16 (&acc)[TI][TJ], int ra,
                                              int rb, int h, int wave, int first, int nsc,
-                                             int blocks) {
+                                             int blocks, bool idle) {
   auto chunk = [&](int i) { return kSplit * i + first; };
   // with a split the last of them may be past the end: any copy does, its scales are cleared
   auto copied = [&](int i) {
@@ -443,17 +444,20 @@ __device__ __forceinline__ void lds_products(LdsStage<TI, TJ>& st0, LdsStage<TI,
   for (; i + 1 < nsc; i += 2) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    stage_mma<TI, TJ, true, kGate, false>(st0, acc, ra, rb, h, st1, p, copied(i + 1), wave, 16);
+    if (kSplit == 4 && idle) stage_load<TI, TJ, kGate>(st1, p, copied(i + 1), wave);
+    else stage_mma<TI, TJ, true, kGate, false>(st0, acc, ra, rb, h, st1, p, copied(i + 1), wave, 16);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     // unconditional (a redundant copy of the last super-chunk when none is left): a
     // branch here lets the compiler sink the previous stage's MFMAs past the barrier
-    stage_mma<TI, TJ, true, kGate, kTail>(st1, acc, ra, rb, h, st0, p, copied(min(i + 2, nsc - 1)),
-                                          wave, blocks - 16 * chunk(i + 1));
+    if (kSplit == 4 && idle) stage_load<TI, TJ, kGate>(st0, p, copied(min(i + 2, nsc - 1)), wave);
+    else
+      stage_mma<TI, TJ, true, kGate, kTail>(st1, acc, ra, rb, h, st0, p, copied(min(i + 2, nsc - 1)),
+                                            wave, blocks - 16 * chunk(i + 1));
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (i < nsc)
+  if (i < nsc && !(kSplit == 4 && idle))
     stage_mma<TI, TJ, false, kGate, kTail>(st0, acc, ra, rb, h, st1, p, 0, wave,
                                            blocks - 16 * chunk(i));
 }
@@ -526,32 +530,38 @@ void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restric
 #pragma unroll
     for (int n = 0; n < TJ; ++n) acc[i][n] = f32x16{};
 
-  const int ra = (wave >> 1) * (32 * TI) + lr;     // this lane's first A row in the tile
-  const int rb = (wave & 1) * (32 * TJ) + lr;      // and first B row
+  // Where the wave is in the tile.  Of a tile in four groups the waves of the same place are
+  // on different SIMDs: what the last rows and columns leave idle is the same for all of them
+  // (16 x 4096 x 4096: 11.2 us, 14.7 where they multiply zeros).
+  const int place = kSplit == 4 ? (wave + group) & 3 : wave;
+  const int ra = (place >> 1) * (32 * TI) + lr;    // this lane's first A row in the tile
+  const int rb = (place & 1) * (32 * TJ) + lr;     // and first B row
+  const bool idle = tm * kBM + (place >> 1) * (32 * TI) >= M ||
+                    (kGate ? tn * (kBN / 2) : tn * kBN + (place & 1) * (32 * TJ)) >= N;
   const int nsc = (K + kSuper * kSplit - 1) / (kSuper * kSplit), blocks = K / 16;
   if constexpr (kSplit == 1) {
-    lds_products<TI, TJ, 1, kGate, kTail>(st0, st1, p, acc, ra, rb, h, wave, 0, nsc, blocks);
+    lds_products<TI, TJ, 1, kGate, kTail>(st0, st1, p, acc, ra, rb, h, wave, 0, nsc, blocks, idle);
   } else {
     __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st2;
     __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st3;
     // branches, not sets of pointers: the compiler has to know which stage a copy goes to, or
     // it waits for it before the next read
     if (group == 0)
-      lds_products<TI, TJ, kSplit, kGate, true>(st0, st1, p, acc, ra, rb, h, wave, 0, nsc, blocks);
+      lds_products<TI, TJ, kSplit, kGate, true>(st0, st1, p, acc, ra, rb, h, wave, 0, nsc, blocks, idle);
     else if (group == 1)
-      lds_products<TI, TJ, kSplit, kGate, true>(st2, st3, p, acc, ra, rb, h, wave, 1, nsc, blocks);
+      lds_products<TI, TJ, kSplit, kGate, true>(st2, st3, p, acc, ra, rb, h, wave, 1, nsc, blocks, idle);
     if constexpr (kSplit == 4) {
       __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st4;
       __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st5;
       __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st6;
       __shared__ __attribute__((aligned(16))) LdsStage<TI, TJ> st7;
       if (group == 2)
-        lds_products<TI, TJ, 4, kGate, true>(st4, st5, p, acc, ra, rb, h, wave, 2, nsc, blocks);
+        lds_products<TI, TJ, 4, kGate, true>(st4, st5, p, acc, ra, rb, h, wave, 2, nsc, blocks, idle);
       else if (group == 3)
-        lds_products<TI, TJ, 4, kGate, true>(st6, st7, p, acc, ra, rb, h, wave, 3, nsc, blocks);
+        lds_products<TI, TJ, 4, kGate, true>(st6, st7, p, acc, ra, rb, h, wave, 3, nsc, blocks, idle);
       static_assert(TI == 1 && TJ == 1 && kJoinBytes <= sizeof(LdsStage<TI, TJ>),
                     "the sums take the stages' place");
-      store_joined<kGate>(e, y, M, N, tm, tn, wave, group, lane, xt[0] * wt[0], acc[0][0],
+      store_joined<kGate>(e, y, M, N, tm, tn, wave, place, group, lane, xt[0] * wt[0], acc[0][0],
                           [&](int g, int half) {
                             return (g == 0 ? st0 : g == 1 ? st2 : g == 2 ? st4 : st6).a + half * kJoinBytes / 2;
                           });
@@ -636,7 +646,7 @@ hipError_t launch_cfg(const uint8_t* xd, const uint8_t* xs, const float* xt, con
 // fixed, and per 4096 of K): 64 x 64 with K split over four groups of waves, while every tile
 // has a CU of its own; 128 x 128, two workgroups to a CU or one (half a round, or all
 // that there is: then of eight waves that split K); 256 x 256, which converts a value for
-// twice as many products, where it fills the GPU.  In this order: 16 x 4096 x 4096 14.6, 29.0,
+// twice as many products, where it fills the GPU.  In this order: 16 x 4096 x 4096 11.2, 29.0,
 // 31.5 and 77 us; 256 x 4096 x 4096 16.9, 29.7, 31.9 and 77; 64 x 4096 x 512 7.5, 8.4, 8.9 and
 // 23; 333 x 8198 x 4160 -, 39, 40 and 90; 2048 x 4096 x 4096 -, 69, 65 and 90; 4096 x 4096 x
 // 4096 -, -, 125 and 110.
