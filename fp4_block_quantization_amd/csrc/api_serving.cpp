@@ -47,7 +47,7 @@ fos_status check_wlinear(const fos::WLinearArgs& a, int out_dtype) {
 fos_status run_wlinear(const void* x, int64_t x_stride, const uint8_t* wd, const uint8_t* ws,
                        const float* wt, const void* bias, int64_t M, int64_t N, int64_t K,
                        int out_dtype, void* y, bool mx, void* stream) {
-  fos::WLinearArgs a;
+  fos::WLinearArgs a = {};
   a.x = static_cast<const uint16_t*>(x);
   a.x_stride = x_stride;
   a.wd = wd;

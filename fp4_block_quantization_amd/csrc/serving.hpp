@@ -75,8 +75,9 @@ struct WLinearArgs {
   void* y;                 // [M][N] bf16 or fp32
   int64_t M, N, K;         // N: weight rows, with a gate two for each column of y
   bool mx, f32_out;
-  bool fused, gated;       // an epilogue other than the bias
-  EpilogueArgs e;          // its activation, residual and pre-activation
+  // an epilogue other than the bias: none unless the caller says so
+  bool fused = false, gated = false;
+  EpilogueArgs e = {};     // its activation, residual and pre-activation
 };
 int64_t wlinear_threads(const WLinearArgs& a);   // work-items of the launch
 hipError_t launch_wlinear(const WLinearArgs& a, hipStream_t s);

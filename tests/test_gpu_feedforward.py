@@ -443,6 +443,26 @@ def test_wlinear_epilogue_residual_in_place(fos, m):
     assert (stream[0] == 7).all() and (stream[-1] == 7).all()
 
 
+@pytest.mark.parametrize("m", [1, 5, 40, 65])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_plain_weight_only_product_between_epilogues(fos, m, fmt):
+    """A plain product has no epilogue, whatever calls came before it."""
+    nv = fmt == "nvfp4"
+    n, k = 40, 352
+    wd, ws, wt, wq = (nv_weight if nv else mx_weight)(fos, n, k, m)
+    x, bias = W.random_bf16(m, k, 1, "normal").to(DEV), W.random_bf16(1, n, 2, "normal")[0].to(DEV)
+    plain = fos.wlinear_fwd if nv else fos.mx_wlinear_fwd
+    glu = fos.wglu_fwd if nv else fos.mx_wglu_fwd
+    epi = fos.wlinear_epilogue_fwd if nv else fos.mx_wlinear_epilogue_fwd
+    b = operand_exact(wd, ws) * wt if nv else MX.operand_exact(wd, ws)
+    for i in range(8):
+        glu(x, wq, activation="gelu", bias=bias, return_preact=True)
+        y = plain(x, wq, bias=bias, out_dtype=torch.float32)
+        check_epilogue(y, None, f64(x), b, f64(bias), "none", False, None, k)
+        epi(x, wq, activation="silu", bias=bias, residual=y.to(BF16), return_preact=True)
+        assert torch.equal(plain(x, wq, bias=bias, out_dtype=torch.float32), y)
+
+
 def test_wlinear_epilogue_of_no_rows(fos):
     _, _, _, wq = nv_weight(fos, 32, 64, 1)
     x = torch.empty(0, 64, dtype=BF16, device=DEV)
