@@ -182,10 +182,10 @@ __device__ __forceinline__ void store_fused(const EpilogueArgs& e, void* y, int 
 }
 
 // The epilogue of a 64 x 64 tile whose K is split over four groups of four waves, each wave
-// with one 32x32 tile of its group's sums (2 x 2, `at` counts them).  place(g, half): 16-byte aligned LDS for half of the
-// kJoinBytes of group g's, which may hold operands that a wave still reads.  A wave of the first group sums a tile of
-// Y in the groups' order (with a gate: waves 0 and 1, both projections, whose sums are two
-// neighbouring waves').
+// with one 32x32 tile of its group's sums (2 x 2, `at` counts them).  place(g, half): 16-byte
+// aligned LDS for half of the kJoinBytes of group g's, which may hold operands that a wave
+// still reads.  A wave of the first group sums a tile of Y in the groups' order (with a gate:
+// waves 0 and 1, both projections, whose sums are two neighbouring waves').
 constexpr int kJoinBytes = 256 * sizeof(f32x16);
 template <bool kGate, typename Place>
 __device__ __forceinline__ void store_joined(const EpilogueArgs& e, void* y, int M, int N, int tm,

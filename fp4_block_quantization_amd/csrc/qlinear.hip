@@ -683,8 +683,11 @@ const QShape& shape_of(const QLinearArgs& a) {
 template <int kEpi>
 hipError_t launch_epi(const QLinearArgs& a, hipStream_t s) {
   const QShape& h = shape_of(a);
-  return (h.split == 4 ? launch_lds<1, 1, kEpi, 4> : h.split == 2 ? launch_lds<2, 2, kEpi, 2> : h.t == 2 ? launch_lds<2, 2, kEpi> : launch_lds<4, 4, kEpi>)(
-      a.xd, a.xs, a.xt, a.wd, a.ws, a.wt, a.M, a.N, a.K, a.y, a.e, s);
+  const auto launch = h.split == 4   ? launch_lds<1, 1, kEpi, 4>
+                      : h.split == 2 ? launch_lds<2, 2, kEpi, 2>
+                      : h.t == 2     ? launch_lds<2, 2, kEpi>
+                                     : launch_lds<4, 4, kEpi>;
+  return launch(a.xd, a.xs, a.xt, a.wd, a.ws, a.wt, a.M, a.N, a.K, a.y, a.e, s);
 }
 
 }  // namespace
