@@ -108,13 +108,17 @@ __device__ __forceinline__ void flow_mma(const i32x8 (&A)[TI], const i32x8 (&B)[
                                                                    kByte, xa[i], kByte, xb[n]);
 }
 
+// What stands before it is issued before what stands behind it.
+__device__ __forceinline__ void flow_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 // A workgroup barrier behind a wait for all but the newest kCopies copies of the wave and for
 // all its LDS reads (__syncthreads would wait for every copy).
 template <int kCopies>
 __device__ __forceinline__ void flow_barrier() {
   static_assert(kCopies < 64, "the counter's range");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
+  flow_order();
   __builtin_amdgcn_s_waitcnt((kCopies & 15) | 7 << 4 | (kCopies >> 4) << 14);
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
@@ -141,6 +145,33 @@ __device__ __forceinline__ T& pick(T& a, T& b, T& c, T& d) {
   return d;
 }
 
+// Copies are counted from the newest.  Phase p (of four, again and again) issues, behind stage p's
+// barrier, the data copies of stage p + NS, and phase 0 those of the scales too, which the read in
+// phase 3 takes.  Within a phase they may be issued in any order: they go to different objects
+// and share scheduling groups.  So only whole phases count as on their way at stage J's barrier,
+// those after the phase of stage J + 1's copies.
+constexpr int kScaleCopies = 2;
+constexpr int flow_in_flight(int ns, int copies, int j) {
+  int n = 0;
+  for (int p = j + 2 - ns; p < j; ++p) n += copies + (p == 0 ? kScaleCopies : 0);
+  return n;
+}
+// Whether with these counts everything has landed that is read behind a barrier, whichever way
+// the copies of phase 0 are ordered: two rounds of four stages played through.
+constexpr bool flow_lands(int ns, int copies, bool scales_first) {
+  constexpr int kRounds = 2, kStages = 4 * kRounds;
+  int data_end[kStages + 4] = {}, scales_end[kRounds] = {}, issued = ns * copies;
+  for (int s = 0; s < ns; ++s) data_end[s] = (s + 1) * copies;
+  for (int s = 0; s < kStages; ++s) {
+    const int landed = issued - flow_in_flight(ns, copies, s % 4);
+    if (data_end[s + 1] > landed || (s % 4 == 3 && scales_end[s / 4] > landed)) return false;
+    if (s % 4 == 0 && scales_first) scales_end[s / 4] = issued += kScaleCopies;
+    data_end[s + ns] = issued += copies;
+    if (s % 4 == 0 && !scales_first) scales_end[s / 4] = issued += kScaleCopies;
+  }
+  return true;
+}
+
 // The products of this wave's tiles.  With kSplit > 1 a group of four waves has every
 // kSplit-th four stages, all groups as many: those past the last count with scales of 2^-127,
 // whose products are 0 in fp32.
@@ -152,6 +183,8 @@ __device__ __forceinline__ void flow_products(FlowStage<TI, TJ>& st0, FlowStage<
                                               int wave, int stages, int group) {
   static_assert(NS == 2 || NS == 4, "stages take turns within four");
   constexpr int kMfmas = TI * TJ, kReads = TI + TJ, kCopies = TI + TJ;
+  static_assert(flow_lands(NS, kCopies, false) && flow_lands(NS, kCopies, true),
+                "a barrier waits for what is read behind it");
   // the stage behind the group's s-th
   auto at = [&](int s) { return kSplit == 1 ? s : (s & ~3) * kSplit + 4 * group + (s & 3); };
   // what is copied past the last stage is the last one again
@@ -160,9 +193,12 @@ __device__ __forceinline__ void flow_products(FlowStage<TI, TJ>& st0, FlowStage<
   };
   flow_load_scales(sc, p, at(0) / 4, wave);
   load(st0, 0);
+  flow_order();   // the barriers' counts take the stages' copies in their order
   load(st1, 1);
   if constexpr (NS == 4) {
+    flow_order();
     load(st2, 2);
+    flow_order();
     load(st3, 3);
   }
   flow_barrier<(NS - 1) * kCopies>();
@@ -173,8 +209,7 @@ __device__ __forceinline__ void flow_products(FlowStage<TI, TJ>& st0, FlowStage<
   flow_operands(st0.a, ra, h, A);
   flow_operands(st0.b, rb, h, B);
 
-  // Stage S, the J-th of its four.  At its barrier the copies of the NS - 2 stages behind the
-  // next one may be on their way, and those of the scales until they are read (J = 3).
+  // Stage S, the J-th of its four.
 #define FOS_FLOW_STAGE(S, J)                                                                        \
   {                                                                                                 \
     FlowStage<TI, TJ>& cur = pick<(J) % NS>(st0, st1, st2, st3);                                    \
@@ -190,7 +225,7 @@ __device__ __forceinline__ void flow_products(FlowStage<TI, TJ>& st0, FlowStage<
     flow_operands(cur.b, rb, 2 + h, Bn);                                                            \
     flow_mma<0>(A, B, xa, xb, acc);                                                                 \
     flow_schedule<kMfmas, kReads, 0>();                                                             \
-    flow_barrier<(NS - 2) * kCopies + ((J) >= 1 && (J) < NS && (J) < 3 ? 2 : 0)>();                 \
+    flow_barrier<flow_in_flight(NS, kCopies, J)>();                                                 \
     load(cur, (S) + NS);                                                                            \
     if (J == 0) flow_load_scales(sc, p, at((S) + 4) / 4, wave);                                     \
     if (J == 3) {                                                                                   \
@@ -200,7 +235,7 @@ __device__ __forceinline__ void flow_products(FlowStage<TI, TJ>& st0, FlowStage<
     flow_operands(next.a, ra, h, A);                                                                \
     flow_operands(next.b, rb, h, B);                                                                \
     flow_mma<2>(An, Bn, xa, xb, acc);                                                               \
-    flow_schedule<kMfmas, kReads + (J == 3 ? kReads : 0), kCopies + (J == 0 ? 2 : 0)>();            \
+    flow_schedule<kMfmas, kReads + (J == 3 ? kReads : 0), kCopies + (J == 0 ? kScaleCopies : 0)>(); \
     __builtin_amdgcn_sched_barrier(0);                                                              \
   }
   if constexpr (kSplit > 1) {

@@ -1,0 +1,39 @@
+"""GPU tests of the feed-forward operators where their kernels' inner loops, registers and
+sizes could go wrong.  Bounds as in test_gpu_feedforward.py (u = 2^-24)."""
+import pytest
+import torch
+
+from fp4_block_quantization_amd import workloads as W
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def fos():
+    from fp4_block_quantization_amd import fos as mod
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    return mod
+
+
+# 1100 x 8200 takes tiles of 256 x 128 (two stages of K in LDS), 700 x 6000 of 128 x 128 (four):
+# through every length of the last round of four stages, and several rounds of scale copies
+@pytest.mark.parametrize("m,n", [(1100, 8200), (700, 6000)])
+@pytest.mark.parametrize("k", [512, 768, 1024, 1280, 2304])
+@pytest.mark.parametrize("gated", [False, True])
+def test_mxfp4_stages_take_turns(fos, m, n, k, gated):
+    """The sums of the plain product, in its order, from operands whose blocks differ in scale."""
+    gen = torch.Generator().manual_seed(m + k)
+    a, b = (torch.randn(r, k, generator=gen) * torch.exp2(torch.randint(-6, 7, (r, k // 32), generator=gen)
+                                                          .repeat_interleave(32, 1)) for r in (m, n))
+    aq, bq = (fos.mx_quantize(t.to(BF16).to(DEV)) for t in (a, b))
+    want = fos.mx_qlinear_fwd(aq, bq)
+    if gated:
+        y, z = fos.mx_qglu_fwd(aq, bq, activation="none", return_preact=True)
+        assert y.shape == (m, n // 2)
+    else:
+        y, z = fos.mx_qlinear_epilogue_fwd(aq, bq, return_preact=True)
+        assert torch.equal(y, want)
+    assert torch.equal(z, want)
