@@ -3,9 +3,9 @@
 // column lr of a 32x32 tile.  Nothing of it overlaps the products of its own workgroup, and
 // its arithmetic bounds it: a wave alone on its SIMD (the 256x256 tile, 256 values a lane)
 // issues a VALU instruction every 8 cycles.  8192 x 12288 x 4096 NVFP4, six rounds of tiles:
-// 602 us without an activation, 633 with silu, 678 with gelu, 617 with Z kept, 674 with a
-// residual, beside 570 for the plain product.  (Eight waves of 128 x 64, two to a SIMD, take
-// less for the epilogue and convert each operand more often: 645, 655, 682, 719 and 708.)
+// 608 us without an activation, 636 with silu, 677 with gelu, 631 with Z kept, 641 with a
+// residual, beside 575 for the plain product.  (Eight waves of 128 x 64, two to a SIMD, take
+// less for the epilogue and convert each operand more often: 645, 655, 682 and 719.)
 #pragma once
 
 #include "activation.hpp"
@@ -54,42 +54,50 @@ __device__ __forceinline__ uint32_t swap_pairs(uint32_t p, int odd) {
 
 // The 16 values of one 32x32 tile of bf16 in packed pairs of rows (a, a + 1): stored, or
 // loaded.  `row`: the tile's first row in the window; `col`: the lane's column, kNowhere if
-// there is none.  `pair`: 4-byte accesses of two columns (even columns, 4-byte alignment).
+// there is none.  kPair: 4-byte accesses of two columns (even columns, 4-byte alignment).
+template <bool kPair>
+__device__ __forceinline__ uint32_t tile_offset(const RowWindow& w, int row, uint32_t col, int h, int odd) {
+  if (col == kNowhere) return col;
+  return kPair ? (row + 4 * h + odd) * w.row_bytes + 2 * (col - odd) : (row + 4 * h) * w.row_bytes + 2 * col;
+}
+__device__ __forceinline__ int tile_row_offset(const RowWindow& w, int a) {
+  return (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes);
+}
 __device__ __forceinline__ void store_bf16_tile(const RowWindow& w, const uint32_t (&v)[8], int row,
                                                 uint32_t col, int h, int odd, bool pair) {
   if (pair) {
-    const uint32_t at = col == kNowhere ? col : (row + 4 * h + odd) * w.row_bytes + 2 * (col - odd);
+    const uint32_t at = tile_offset<true>(w, row, col, h, odd);
 #pragma unroll
     for (int a = 0; a < 16; a += 2)
-      __builtin_amdgcn_raw_buffer_store_b32(swap_pairs(v[a / 2], odd), w.r, at,
-                                            (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
+      __builtin_amdgcn_raw_buffer_store_b32(swap_pairs(v[a / 2], odd), w.r, at, tile_row_offset(w, a), 0);
   } else {
-    const uint32_t at = col == kNowhere ? col : (row + 4 * h) * w.row_bytes + 2 * col;
+    const uint32_t at = tile_offset<false>(w, row, col, h, odd);
 #pragma unroll
     for (int a = 0; a < 16; ++a)
       __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[a / 2] >> (16 * (a & 1))), w.r, at,
-                                            (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
+                                            tile_row_offset(w, a), 0);
   }
 }
-__device__ __forceinline__ void load_bf16_tile(const RowWindow& w, uint32_t (&v)[16], int row,
-                                               uint32_t col, int h, int odd, bool pair) {
-  if (pair) {
-    const uint32_t at = col == kNowhere ? col : (row + 4 * h + odd) * w.row_bytes + 2 * (col - odd);
+// As they are in memory: kPair 8 words of two columns each, else 16 values.
+template <bool kPair>
+__device__ __forceinline__ void load_bf16_tile(const RowWindow& w, uint32_t (&v)[kPair ? 8 : 16], int row,
+                                               uint32_t col, int h, int odd) {
+  const uint32_t at = tile_offset<kPair>(w, row, col, h, odd);
 #pragma unroll
-    for (int a = 0; a < 16; a += 2)
-      v[a / 2] = __builtin_amdgcn_raw_buffer_load_b32(
-          w.r, at, (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
-  } else {
-    const uint32_t at = col == kNowhere ? col : (row + 4 * h) * w.row_bytes + 2 * col;
-#pragma unroll
-    for (int a = 0; a < 16; ++a)
-      v[a] = __builtin_amdgcn_raw_buffer_load_b16(
-          w.r, at, (int)(((a & 3) + 8 * (a >> 2)) * w.row_bytes), 0);
+  for (int a = 0; a < 16; a += kPair ? 2 : 1) {
+    if constexpr (kPair) v[a / 2] = __builtin_amdgcn_raw_buffer_load_b32(w.r, at, tile_row_offset(w, a), 0);
+    else v[a] = __builtin_amdgcn_raw_buffer_load_b16(w.r, at, tile_row_offset(w, a), 0);
   }
 }
 
+// The lane, asked for again where the register that held it is worth more in the loop before.
+__device__ __forceinline__ int lane_again() {
+  return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+}
+
 // The tile of a wave, rows m0 .. and columns n0 .. of y: act(s acc + bias) (times the other
-// projection) + residual.  A tile's residual is on its way while the tile before is computed.
+// projection) + residual.  A tile's residual is on its way while the tile before is computed, with
+// single columns while the tile itself is.
 template <int TI, int TJ, bool kGate, int kAct>
 __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, int M, int N, int m0,
                                                int n0, int lane, float s,
@@ -113,17 +121,22 @@ __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, i
       if (kGate) bias_up[t] = bf16_lo(e.bias[N + n]);
     }
   }
-  uint32_t next[16] = {};
-  if (e.residual) load_bf16_tile(wr, next, 0, col[0], h, odd, pair);
+  // (arrays of their own: one that holds either layout is kept in scratch memory)
+  uint32_t next[8] = {};
+  if (!kGate && e.residual && pair) load_bf16_tile<true>(wr, next, 0, col[0], h, odd);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      uint32_t res[16];
+      uint32_t res[8], one[16];
 #pragma unroll
-      for (int a = 0; a < 16; ++a) res[a] = next[a];
-      if (e.residual && (i + 1 < TI || t + 1 < kTiles))
-        load_bf16_tile(wr, next, 32 * (t + 1 < kTiles ? i : i + 1), col[(t + 1) % kTiles], h, odd, pair);
+      for (int a = 0; a < 8; ++a) res[a] = next[a];
+      if (!kGate && e.residual) {
+        if (!pair)
+          load_bf16_tile<false>(wr, one, 32 * i, col[t], h, odd);
+        else if (i + 1 < TI || t + 1 < kTiles)
+          load_bf16_tile<true>(wr, next, 32 * (t + 1 < kTiles ? i : i + 1), col[(t + 1) % kTiles], h, odd);
+      }
       float v[16];
       uint32_t z[8], zu[8];
 #pragma unroll
@@ -146,13 +159,16 @@ __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, i
         if constexpr (kGate)
           store_bf16_tile(wz, zu, 32 * i, col[t] == kNowhere ? kNowhere : col[t] + N, h, odd, pair);
       }
-      if (e.residual) {
+      if (!kGate && e.residual && pair) {
 #pragma unroll
         for (int a = 0; a < 16; a += 2) {
-          const uint32_t r = pair ? swap_pairs(res[a / 2], odd) : res[a] | res[a + 1] << 16;
+          const uint32_t r = swap_pairs(res[a / 2], odd);
           v[a] += bf16_lo(r);
           v[a + 1] += bf16_hi(r);
         }
+      } else if (!kGate && e.residual) {
+#pragma unroll
+        for (int a = 0; a < 16; ++a) v[a] += bf16_lo(one[a]);
       }
       if (e.f32_out) {
         const uint32_t at = col[t] == kNowhere ? kNowhere : (32 * i + 4 * h) * wy.row_bytes + 4 * col[t];

@@ -607,7 +607,7 @@ void qlinear_lds_kernel(const uint8_t* __restrict__ xd, const uint8_t* __restric
     store_tile(static_cast<uint16_t*>(y), M, N, tm, tn, wave, lr, h, xt[0] * wt[0], acc);
   } else if constexpr (kSplit == 1) {
     store_fused<TI, TJ, kGate>(e, y, M, N, tm * kBM + (wave >> 1) * (32 * TI),
-                               (tn * kBN + (wave & 1) * (32 * TJ)) / kProj, lane, xt[0] * wt[0], acc);
+                               (tn * kBN + (wave & 1) * (32 * TJ)) / kProj, lane_again(), xt[0] * wt[0], acc);
   }
 }
 
