@@ -56,3 +56,9 @@ def test_the_library_was_read(scratch):
 def test_products_with_an_epilogue_keep_nothing_in_scratch(scratch, kernel):
     mine = {k: v for k, v in scratch.items() if kernel in k}
     assert len(mine) >= 8 and not {k: v for k, v in mine.items() if v}
+
+
+def test_norms_keep_nothing_in_scratch(scratch):
+    mine = {k: v for k, v in scratch.items() if "rmsnorm" in k}
+    assert any("rmsnorm_bwd_kernelILi512ELi4" in k for k in mine)      # the longest rows
+    assert not {k: v for k, v in mine.items() if v}
