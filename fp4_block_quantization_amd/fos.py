@@ -1226,6 +1226,22 @@ def epilogue_bwd(dy: torch.Tensor, preact: torch.Tensor, activation: str = "none
     return got if len(got) > 1 else dz
 
 
+_PLAIN = FosEpilogue(_EPILOGUE_SIZE, FOS_ACT_NONE, 0, FOS_OUT_BF16, None, None, 0, None, 0)
+
+
+def _check_plain_product(m: int, n: int, k: int, q: NVFP4Tensor) -> None:
+    """Raises what ``fos_qlinear_epilogue_fwd`` of [m, k] and the record q [n, k] would, without a
+    launch.  Sizes that are surely accepted do not ask the library (2 us a call)."""
+    if (k % 64 or k < 64 or m < 1 or n < 1 or n > 1 << 20 or max(m, n, 256) * k >= 1 << 32
+            or m * n >= 1 << 32):
+        # it looks at the sizes first: NULL is what remains to complain of
+        status = _lib.fos_qlinear_epilogue_fwd(*[None] * 6, m, n, k, ctypes.byref(_PLAIN), None, None)
+        if status != FOS_E_NULL:
+            _check(status, "fos_qlinear_epilogue_fwd")
+    if q.data.data_ptr() % 16 or q.scales.data_ptr() % 4:
+        raise FosError(FOS_E_ALIGN, "fos_qlinear_epilogue_fwd")
+
+
 def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, rounding, sr_seed,
                  need_dx, need_dw):
     if not (need_dx or need_dw):
@@ -1238,6 +1254,12 @@ def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, roundi
         if where != dev or cols != inner or q.hadamard_seed is not None:
             raise ValueError("xq_t and wq_t must be the column-wise records of X and W, without a "
                              "Hadamard transform")
+    if need_dx:
+        _check_plain_product(M, wq_t.data.shape[0], W, wq_t)
+    if need_dw:
+        _check_plain_product(W, xq_t.data.shape[0], M, xq_t)
+        if W % 16:
+            raise FosError(FOS_E_SHAPE, "fos_quantize_scaled")
     # dZ, its tensor scale and records and the workspace in one allocation (one each of ten
     # took 12 of a small call's 44 us on the host)
     sizes = [2 * M * W, 4, int(_lib.fos_epilogue_bwd_workspace_bytes(M, N, int(gated)))]
@@ -1257,10 +1279,9 @@ def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, roundi
           *((cols, col_scales) if need_dw else (None, None)))
     # the products of fos_qlinear_bwd, on the tiles that suit their shapes (dX of 2048 x 4096
     # with an inner dimension of 8192 has 128 tiles of 256 x 256, half a GPU)
-    plain = FosEpilogue(_EPILOGUE_SIZE, FOS_ACT_NONE, 0, FOS_OUT_BF16, None, None, 0, None, 0)
     product = lambda data, scales, m, k, q, out: _call(
         dev, "fos_qlinear_epilogue_fwd", data, scales, t, q.data.data_ptr(), q.scales.data_ptr(),
-        q.tensor_scale.data_ptr(), m, out.shape[1], k, ctypes.byref(plain), out.data_ptr())
+        q.tensor_scale.data_ptr(), m, out.shape[1], k, ctypes.byref(_PLAIN), out.data_ptr())
     dx = dw = None
     if need_dx:
         dx = dy.new_empty(M, wq_t.data.shape[0])

@@ -1,0 +1,69 @@
+"""The feed-forward binding's own work, without a GPU: CPU tensors stand for a device's, and
+the entry points' names are noted instead of called."""
+import pytest
+import torch
+
+from fp4_block_quantization_amd import fos
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names of the entry points that a call of the binding reaches."""
+    seen = []
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(fos, "_call", lambda dev, name, *args: seen.append(name))
+    return seen
+
+
+def record(rows, cols):
+    return fos.NVFP4Tensor(torch.zeros(rows, cols // 2, dtype=torch.uint8),
+                           torch.zeros(rows, cols // 16, dtype=torch.uint8), torch.zeros(1))
+
+
+def product_bwd(m, n, k, gated=False, x=None, w=None, **kw):
+    rows = 2 * n if gated else n
+    dy, z = torch.zeros(m, n, dtype=BF16), torch.zeros(m, rows, dtype=BF16)
+    f = fos.qglu_bwd if gated else fos.qlinear_epilogue_bwd
+    return f(dy, z, x or record(k, m), w or record(k, rows), **kw)
+
+
+# dX has W's rows as its inner dimension, dW those of X; only the wanted ones count
+@pytest.mark.parametrize("m,n,gated,kw", [
+    (48, 64, False, {}), (48, 64, True, {}), (64, 48, False, {}), (64, 16, True, {}),
+    (64, 48, False, dict(need_dw=False)), (80, 64, True, dict(need_dx=False)),
+    (32, 64, False, {}), (0, 64, False, {}), (0, 64, False, dict(need_dw=False)),
+])
+def test_backward_of_a_product_refuses_sizes_before_the_first_launch(calls, m, n, gated, kw):
+    with pytest.raises(fos.FosError) as e:
+        product_bwd(m, n, 64, gated, **kw)
+    assert e.value.status == fos.FOS_E_SHAPE and calls == []
+
+
+@pytest.mark.parametrize("m,n,gated,kw", [
+    (64, 64, False, {}), (128, 32, True, {}), (64, 48, False, dict(need_dx=False)),
+    (48, 64, False, dict(need_dw=False)), (1, 64, True, dict(need_dw=False))])
+def test_backward_of_a_product_launches_what_it_accepts(calls, m, n, gated, kw):
+    product_bwd(m, n, 48, gated, **kw)
+    assert calls == ["fos_epilogue_bwd", "fos_quantize_scaled"] + ["fos_qlinear_epilogue_fwd"] * (2 - len(kw))
+
+
+def test_backward_of_a_product_refuses_what_is_too_large_or_misaligned(calls):
+    # a packed operand of 4 GiB, and more columns than an epilogue addresses; no memory behind them
+    many = torch.zeros(1, dtype=torch.uint8)
+    for rows, inner in (((1 << 20) + 64, 64), (1 << 20, 8192)):
+        big = fos.NVFP4Tensor(many.expand(rows, inner // 2), many.expand(rows, inner // 16), torch.zeros(1))
+        with pytest.raises(fos.FosError) as e:
+            fos._check_plain_product(64, rows, inner, big)
+        assert e.value.status == fos.FOS_E_SHAPE
+    buf = torch.zeros(64 * 32 + 32, dtype=torch.uint8)
+    start = -buf.data_ptr() % 16
+    x = record(64, 64)
+    x.data = buf[start + 8:][:64 * 32].view(64, 32)
+    with pytest.raises(fos.FosError) as e:
+        product_bwd(64, 64, 64, x=x)
+    assert e.value.status == fos.FOS_E_ALIGN and calls == []
+    x.data = buf[start:][:64 * 32].view(64, 32)
+    product_bwd(64, 64, 64, x=x)
+    assert len(calls) == 4
