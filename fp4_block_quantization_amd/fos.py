@@ -1001,7 +1001,8 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: t
                 dh: Optional[torch.Tensor] = None, need_dweight: bool = True
                 ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Backward of ``rmsnorm_fwd`` from the gradient dy of its output (quantization counts as
-    the identity) and its h and rstd.  ``dh``: the gradient that reaches h past the norm.
+    the identity) and its h and rstd.  h may have strided rows, as the x has that it is without a
+    residual; they are copied together first.  ``dh``: the gradient that reaches h past the norm.
     Returns the gradient of x, which is the residual's too (bf16 [M, K]), and that of the
     weight (fp32 [K], or None)."""
     if dy.dim() != 2 or dy.get_device() < 0:
@@ -1009,11 +1010,12 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: t
     M, K = dy.shape
     dev = dy.get_device()
     _whole(dy, (M, K), _BF16, dev, "dy")
-    _whole(h, (M, K), _BF16, dev, "h")
+    _rows_of(h, M, K, dev, "h")
     _whole(weight, (K,), _BF16, dev, "weight")
     _whole(rstd, (M,), _F32, dev, "rstd")
     if dh is not None:
         _whole(dh, (M, K), _BF16, dev, "dh")
+    h = h.contiguous()
     dx = dy.new_empty(M, K)
     dw = ws = None
     if need_dweight:

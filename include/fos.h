@@ -553,7 +553,8 @@ enum { FOS_RECORD_NONE = 0, FOS_RECORD_NVFP4 = 1, FOS_RECORD_MXFP4 = 2 };
  *   (for rows > 1); weight [cols]; h, y bf16 [rows][cols], contiguous; all 16-byte aligned.
  *   h, rstd (fp32 [rows]) and y may be NULL, but y not without a record, rstd not where the
  *   tensor scale is computed, nor h there with a residual.  h may be the memory of x or of
- *   the residual, if that is contiguous.  data [rows][cols/2] 8-byte aligned, scales
+ *   the residual, if that is contiguous; without a residual it is a copy of x with its rows
+ *   together, as fos_rmsnorm_bwd takes them.  data [rows][cols/2] 8-byte aligned, scales
  *   [rows][cols/16] (MXFP4: [rows][cols/32]), tensor_scale 4-byte aligned.
  *   rows >= 0, below 2^31; cols a multiple of 16 (MXFP4: of 32) from 16 to 32768; eps
  *   finite, at least 1e-38.  No rows: a computed tensor scale is 0, nothing else is written.

@@ -67,3 +67,18 @@ def test_backward_of_a_product_refuses_what_is_too_large_or_misaligned(calls):
     x.data = buf[start:][:64 * 32].view(64, 32)
     product_bwd(64, 64, 64, x=x)
     assert len(calls) == 4
+
+
+def test_backward_of_the_norm_takes_the_rows_that_its_forward_took(calls):
+    """Without a residual h is x itself, whose rows may be strided."""
+    wide, w, rstd = torch.zeros(6, 200, dtype=BF16), torch.ones(64, dtype=BF16), torch.ones(6)
+    dy = torch.zeros(6, 64, dtype=BF16)
+    for h in (wide[:, 8:72], wide[:, :64], dy):
+        fos.rmsnorm_bwd(dy, h, w, rstd)
+    assert calls == ["fos_rmsnorm_bwd"] * 3
+    for h in (torch.zeros(64, 6, dtype=BF16).T, wide[:, :128:2], wide[:4, :64], wide[:, :64].float(), w):
+        with pytest.raises(ValueError):
+            fos.rmsnorm_bwd(dy, h, w, rstd)
+    with pytest.raises(ValueError):
+        fos.rmsnorm_bwd(wide[:, :64], dy, w, rstd)
+    assert len(calls) == 3

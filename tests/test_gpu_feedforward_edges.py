@@ -59,3 +59,34 @@ def test_norm_bwd_of_long_rows(fos, m, k, direct):
     again = fos.rmsnorm_bwd(dy, h, w, rstd, dh=dh)
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
     assert torch.equal(fos.rmsnorm_bwd(dy, h, w, rstd, dh=dh, need_dweight=False)[0], dx)
+
+
+@pytest.mark.parametrize("m,k", [(1, 64), (5, 320), (300, 4096)])
+@pytest.mark.parametrize("fmt", ["bf16", "nvfp4"])
+def test_norm_backward_follows_a_strided_forward(fos, m, k, fmt):
+    """Rows of a wider tensor, NaN beside them; eager, then captured and replayed with new rows."""
+    wide = torch.full((m, 2 * k + 48), float("nan"), dtype=BF16, device=DEV)
+    x = wide[:, 8:8 + k]
+    w = W.random_bf16(1, k, 2, "normal")[0].to(DEV)
+    dy = W.random_bf16(m, k, 3, "normal").to(DEV)
+
+    def step():
+        n = fos.rmsnorm_fwd(x, w, format=fmt)
+        return n.rstd, *fos.rmsnorm_bwd(dy, n.h, w, n.rstd)
+
+    def check(got):
+        rstd = fos.rmsnorm_fwd(x.contiguous(), w).rstd
+        want = rstd, *fos.rmsnorm_bwd(dy, x.contiguous(), w, rstd)
+        assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
+
+    x.copy_(W.random_bf16(m, k, 4, "normal"))
+    check(step())
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    for seed in (5, 6, 7):
+        x.copy_(W.random_bf16(m, k, seed, "normal"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(got)
