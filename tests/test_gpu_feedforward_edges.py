@@ -3,6 +3,7 @@ sizes could go wrong.  Bounds as in test_gpu_feedforward.py (u = 2^-24)."""
 import numpy as np
 import pytest
 import torch
+from scipy.special import ndtr
 
 from fp4_block_quantization_amd import workloads as W
 from oracle import feedforward as FF
@@ -90,3 +91,23 @@ def test_norm_backward_follows_a_strided_forward(fos, m, k, fmt):
         graph.replay()
         torch.cuda.synchronize()
         check(got)
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_gelu_of_small_values_keeps_its_digits(fos, few):
+    """Relative to a value that falls to 1e-32.  Z is the bias alone, exact.  The exponent
+    -z^2 / 2 log2 e has three roundings, which e has as 1.5 z^2 u; the fit 1.9e-7 = 3.2 u; t (two
+    roundings and the reciprocal's 2 u) moves t P by at most as much, Horner's last steps, the
+    exponential (2 u), three products and z's own add the rest of 20 u."""
+    z = torch.cat((torch.linspace(-12.5, -1 / 16, 4000), torch.linspace(1 / 16, 12.5, 96))).to(BF16)
+    rec = fos.mx_quantize(torch.zeros(z.numel(), 256, dtype=BF16, device=DEV))
+    if few:
+        x = torch.zeros(2, 256, dtype=BF16, device=DEV)
+        y = fos.mx_wlinear_epilogue_fwd(x, rec, bias=z.to(DEV), activation="gelu", out_dtype=torch.float32)
+    else:
+        x = fos.mx_quantize(torch.zeros(2, 256, dtype=BF16, device=DEV))
+        y = fos.mx_qlinear_epilogue_fwd(x, rec, bias=z.to(DEV), activation="gelu", out_dtype=torch.float32)
+    z = z.double().numpy()
+    want = z * ndtr(z)
+    for row in y.double().cpu().numpy():
+        within(row, want, (1.5 * z ** 2 + 20) * U * np.abs(want), "gelu")
