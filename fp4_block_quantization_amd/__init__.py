@@ -8,7 +8,10 @@ re-exported lazily from ``fos``.
 """
 _EXPORTS = ("quantize", "dequantize", "qlinear_fwd", "tensor_scale", "NVFP4Tensor", "FosError",
             "make_config", "wlinear_fwd", "mx_wlinear_fwd", "PagedKVCache", "kv_cache", "kv_append",
-           "kv_gather", "paged_decode", "paged_decode_workspace")
+           "kv_gather", "paged_decode", "paged_decode_workspace", "rmsnorm_fwd", "rmsnorm_bwd",
+           "RMSNormOutput", "qlinear_epilogue_fwd", "mx_qlinear_epilogue_fwd", "qglu_fwd", "mx_qglu_fwd",
+           "wlinear_epilogue_fwd", "mx_wlinear_epilogue_fwd", "wglu_fwd", "mx_wglu_fwd", "epilogue_bwd",
+           "qlinear_epilogue_bwd", "qglu_bwd")
 
 
 def __getattr__(name):

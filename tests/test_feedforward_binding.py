@@ -3,6 +3,7 @@ the entry points' names are noted instead of called."""
 import pytest
 import torch
 
+import fp4_block_quantization_amd as package
 from fp4_block_quantization_amd import fos
 
 BF16 = torch.bfloat16
@@ -82,3 +83,12 @@ def test_backward_of_the_norm_takes_the_rows_that_its_forward_took(calls):
     with pytest.raises(ValueError):
         fos.rmsnorm_bwd(wide[:, :64], dy, w, rstd)
     assert len(calls) == 3
+
+
+@pytest.mark.parametrize("name", [
+    "rmsnorm_fwd", "rmsnorm_bwd", "RMSNormOutput", "qlinear_epilogue_fwd", "mx_qlinear_epilogue_fwd", "qglu_fwd",
+    "mx_qglu_fwd", "wlinear_epilogue_fwd", "mx_wlinear_epilogue_fwd", "wglu_fwd", "mx_wglu_fwd", "epilogue_bwd",
+    "qlinear_epilogue_bwd", "qglu_bwd"])
+def test_the_package_offers_the_operators(name):
+    """As it does the quantizers, the plain products and the calls of a decode step."""
+    assert getattr(package, name) is getattr(fos, name)
