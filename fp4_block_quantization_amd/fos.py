@@ -1256,6 +1256,8 @@ def _product_bwd(dy, preact, xq_t, wq_t, activation, gated, return_dbias, roundi
         if where != dev or cols != inner or q.hadamard_seed is not None:
             raise ValueError("xq_t and wq_t must be the column-wise records of X and W, without a "
                              "Hadamard transform")
+    if need_dx and need_dw and wq_t.data.shape[0] != xq_t.data.shape[0]:
+        raise ValueError("X and W disagree on the inner dimension of their product")
     if need_dx:
         _check_plain_product(M, wq_t.data.shape[0], W, wq_t)
     if need_dw:

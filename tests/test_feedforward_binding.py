@@ -70,6 +70,14 @@ def test_backward_of_a_product_refuses_what_is_too_large_or_misaligned(calls):
     assert len(calls) == 4
 
 
+def test_backward_of_a_product_refuses_operands_of_different_inner_dimensions(calls):
+    with pytest.raises(ValueError, match="inner dimension"):
+        product_bwd(64, 64, None, x=record(48, 64), w=record(80, 64))
+    assert calls == []
+    product_bwd(64, 64, None, x=record(48, 64), w=record(80, 64), need_dw=False)     # X is not looked at
+    assert len(calls) == 3
+
+
 def test_backward_of_the_norm_takes_the_rows_that_its_forward_took(calls):
     """Without a residual h is x itself, whose rows may be strided."""
     wide, w, rstd = torch.zeros(6, 200, dtype=BF16), torch.ones(64, dtype=BF16), torch.ones(6)
