@@ -3,9 +3,10 @@
 // column lr of a 32x32 tile.  Nothing of it overlaps the products of its own workgroup, and
 // its arithmetic bounds it: a wave alone on its SIMD (the 256x256 tile, 256 values a lane)
 // issues a VALU instruction every 8 cycles.  8192 x 12288 x 4096 NVFP4, six rounds of tiles:
-// 608 us without an activation, 636 with silu, 677 with gelu, 631 with Z kept, 641 with a
-// residual, beside 575 for the plain product.  (Eight waves of 128 x 64, two to a SIMD, take
-// less for the epilogue and convert each operand more often: 645, 655, 682 and 719.)
+// 581 us without an activation, 606 with silu, 659 with gelu, 611 with Z kept, 646 with a
+// residual, beside 576 for the plain product.  (Eight waves of 128 x 64, two to a SIMD, take
+// less for the epilogue and convert each operand more often: 645, 655, 682 and 719 without a
+// residual.)
 #pragma once
 
 #include "activation.hpp"
@@ -97,8 +98,9 @@ __device__ __forceinline__ int lane_again() {
 
 // The tile of a wave, rows m0 .. and columns n0 .. of y: act(s acc + bias) (times the other
 // projection) + residual.  A tile's residual is on its way while the tile before is computed, with
-// single columns while the tile itself is.
-template <int TI, int TJ, bool kGate, int kAct>
+// single columns while the tile itself is.  Without a residual nothing of it is in the loop (asked
+// for tile by tile, it took 27 us more without an activation).
+template <int TI, int TJ, bool kGate, bool kRes, int kAct>
 __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, int M, int N, int m0,
                                                int n0, int lane, float s,
                                                const f32x16 (&acc)[TI][TJ]) {
@@ -108,7 +110,7 @@ __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, i
   const bool pair = e.pair;
   const RowWindow wy = row_window(y, m0, rows, N, N, e.f32_out ? 4 : 2);
   const RowWindow wz = row_window(e.preact, m0, e.preact ? rows : 0, kStep * (int64_t)N, kStep * N, 2);
-  const RowWindow wr = row_window(e.residual, m0, e.residual ? rows : 0, e.residual_stride, N, 2);
+  const RowWindow wr = row_window(e.residual, m0, kRes ? rows : 0, e.residual_stride, N, 2);
   uint32_t col[kTiles];
   float bias[kTiles], bias_up[kTiles];
 #pragma unroll
@@ -123,7 +125,7 @@ __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, i
   }
   // (arrays of their own: one that holds either layout is kept in scratch memory)
   uint32_t next[8] = {};
-  if (!kGate && e.residual && pair) load_bf16_tile<true>(wr, next, 0, col[0], h, odd);
+  if (kRes && pair) load_bf16_tile<true>(wr, next, 0, col[0], h, odd);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
 #pragma unroll
@@ -131,7 +133,7 @@ __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, i
       uint32_t res[8], one[16];
 #pragma unroll
       for (int a = 0; a < 8; ++a) res[a] = next[a];
-      if (!kGate && e.residual) {
+      if (kRes) {
         if (!pair)
           load_bf16_tile<false>(wr, one, 32 * i, col[t], h, odd);
         else if (i + 1 < TI || t + 1 < kTiles)
@@ -159,14 +161,14 @@ __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, i
         if constexpr (kGate)
           store_bf16_tile(wz, zu, 32 * i, col[t] == kNowhere ? kNowhere : col[t] + N, h, odd, pair);
       }
-      if (!kGate && e.residual && pair) {
+      if (kRes && pair) {
 #pragma unroll
         for (int a = 0; a < 16; a += 2) {
           const uint32_t r = swap_pairs(res[a / 2], odd);
           v[a] += bf16_lo(r);
           v[a + 1] += bf16_hi(r);
         }
-      } else if (!kGate && e.residual) {
+      } else if (kRes) {
 #pragma unroll
         for (int a = 0; a < 16; ++a) v[a] += bf16_lo(one[a]);
       }
@@ -185,16 +187,24 @@ __device__ __forceinline__ void store_fused_as(const EpilogueArgs& e, void* y, i
   }
 }
 
+template <int TI, int TJ, bool kGate, bool kRes>
+__device__ __forceinline__ void store_fused_act(const EpilogueArgs& e, void* y, int M, int N, int m0, int n0,
+                                                int lane, float s, const f32x16 (&acc)[TI][TJ]) {
+  switch (e.act) {
+    case kActRelu: store_fused_as<TI, TJ, kGate, kRes, kActRelu>(e, y, M, N, m0, n0, lane, s, acc); break;
+    case kActGelu: store_fused_as<TI, TJ, kGate, kRes, kActGelu>(e, y, M, N, m0, n0, lane, s, acc); break;
+    case kActGeluTanh: store_fused_as<TI, TJ, kGate, kRes, kActGeluTanh>(e, y, M, N, m0, n0, lane, s, acc); break;
+    case kActSilu: store_fused_as<TI, TJ, kGate, kRes, kActSilu>(e, y, M, N, m0, n0, lane, s, acc); break;
+    default: store_fused_as<TI, TJ, kGate, kRes, kActNone>(e, y, M, N, m0, n0, lane, s, acc);
+  }
+}
 template <int TI, int TJ, bool kGate>
 __device__ __forceinline__ void store_fused(const EpilogueArgs& e, void* y, int M, int N, int m0,
                                             int n0, int lane, float s, const f32x16 (&acc)[TI][TJ]) {
-  switch (e.act) {
-    case kActRelu: store_fused_as<TI, TJ, kGate, kActRelu>(e, y, M, N, m0, n0, lane, s, acc); break;
-    case kActGelu: store_fused_as<TI, TJ, kGate, kActGelu>(e, y, M, N, m0, n0, lane, s, acc); break;
-    case kActGeluTanh: store_fused_as<TI, TJ, kGate, kActGeluTanh>(e, y, M, N, m0, n0, lane, s, acc); break;
-    case kActSilu: store_fused_as<TI, TJ, kGate, kActSilu>(e, y, M, N, m0, n0, lane, s, acc); break;
-    default: store_fused_as<TI, TJ, kGate, kActNone>(e, y, M, N, m0, n0, lane, s, acc);
+  if constexpr (!kGate) {   // with a gate there is no residual
+    if (e.residual) return store_fused_act<TI, TJ, kGate, true>(e, y, M, N, m0, n0, lane, s, acc);
   }
+  store_fused_act<TI, TJ, kGate, false>(e, y, M, N, m0, n0, lane, s, acc);
 }
 
 // The epilogue of a 64 x 64 tile whose K is split over four groups of four waves, each wave
