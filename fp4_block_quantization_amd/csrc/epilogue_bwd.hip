@@ -4,7 +4,7 @@
 // with which dZ is quantized next.
 //
 // Bound by memory: 4096 x 12288 with gelu_tanh 59 us (5.1 TB/s; VALU busy 66%), the sums of
-// dbias joined in 5 more.  A wave takes 64 x kCols columns (one 16-byte load a lane, or one value
+// dbias joined in 5 more (4096 x 12287, value by value: 92).  A wave takes 64 x kCols columns (one 16-byte load a lane, or one value
 // where rows are not aligned for that) of every fourth row of the workgroup's rows, and keeps
 // the columns' sums in registers; the workgroup's four waves join theirs in LDS, and a
 // second launch joins the groups of rows, always in the same order.

@@ -8,9 +8,9 @@
 // 256 x 128 share a CU.  The E8M0 bytes of four stages (16 a row) are copied at once, apart,
 // and go to registers: a row's scale bytes of one stage are a request of their own to the
 // address unit, as dear as 64 bytes of nibbles.  The copies are what bounds the kernel: the
-// matrix cores are busy 41% of the time, VALU 16 to 24% (4096 x 12288 x 4096 gated with silu
-// 245 to 256 us, 3.2 to 3.4 PFLOP/s; two stages of 256 with their scales beside them: 257
-// where this took 244).
+// matrix cores are busy 43% of the time, VALU 17 to 24% (4096 x 12288 x 4096 gated with silu
+// 233 to 238 us, 3.5 PFLOP/s; two stages of 256 with their scales beside them: 257 where
+// this took 244).
 //
 // A stage is two k-steps of 64.  While one multiplies, the operands of the next are read from
 // LDS; between the two stands the stage's one barrier, where every wave has read all of this
@@ -378,8 +378,10 @@ hipError_t launch_flow(const QLinearArgs& a, hipStream_t s) {
 // every tile has a CU of its own; 128 x 128 tiles, two to a CU or (half a round) one, while
 // there are few; 256 x 128, whose epilogues run beside another workgroup's products, for a
 // short K; 256 x 256, which copies least for its products, for a long one.  In this order:
-// 16 x 4096 x 4096 8.9, 11.0, - and 17; 64 x 4096 x 12288 18, 23, - and 37; 1024 x 4096 x 4096
-// -, 19, 24 and 36; 8192 x 8192 x 1024 -, 70, 64 and 86; 4096 x 4096 x 12288 -, 155, 126 and 108.
+// 16 x 4096 x 4096 8.9, 11.0, - and 17; 64 x 4096 x 12288 18, 23, - and 37 with the weight in a
+// cache (23 with the first from memory); 1024 x 4096 x 4096 -, 19, 24 and 36; 8192 x 8192 x 1024
+// -, 70, 64 and 86; 4096 x 4096 x 12288 -, 155, 126 and 108.  (All measured with an earlier epilogue;
+// the chosen ones now take 8.5, 17, 17, 62 and 104.)
 struct MxShape {
   int ti, tj, split, resident;
   float half, half_k, full, full_k;

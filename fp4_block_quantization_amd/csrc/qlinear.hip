@@ -649,7 +649,8 @@ hipError_t launch_cfg(const uint8_t* xd, const uint8_t* xs, const float* xt, con
 // twice as many products, where it fills the GPU.  In this order: 16 x 4096 x 4096 11.2, 29.0,
 // 31.5 and 77 us; 256 x 4096 x 4096 16.9, 29.7, 31.9 and 77; 64 x 4096 x 512 7.5, 8.4, 8.9 and
 // 23; 333 x 8198 x 4160 -, 39, 40 and 90; 2048 x 4096 x 4096 -, 69, 65 and 90; 4096 x 4096 x
-// 4096 -, -, 125 and 110.
+// 4096 -, -, 125 and 110.  (All measured with an earlier epilogue; the chosen ones now take 10.5,
+// 16, 9.0 from Python, 34, 61 and 101.)
 struct QShape {
   int t, split, resident;
   float half, half_k, full, full_k;

@@ -12,8 +12,8 @@
 //
 // Both are bound by memory, but for the second launch of an NVFP4 record under its own tensor
 // scale, whose rounding of every block twice takes 77% of the VALU cycles.  8192 x 4096 with
-// a residual: 36 us for h and the maxima (5.5 TB/s) and 26 for the record, in one launch with
-// a given tensor scale; backward 48 (5.6 TB/s) and 5 for dw's partial sums.  2047 x 12288
+// a residual: 36 us for h and the maxima (5.5 TB/s) and 26 for the record, 42 in one launch
+// with a given tensor scale; backward 48 (5.6 TB/s) and 5 for dw's partial sums.  2047 x 12288
 // with a residual to MXFP4 32 us (5.2 TB/s); one row of 4096 2.5.
 //
 // kLanes lanes share a row and keep it in registers, kBlocks blocks of 16 values each; lane l
